@@ -1,6 +1,7 @@
 """Build the gfx950 HIP libraries in place with hipcc: libepdc.so (the
-dispatch/combine path) and libepdc_probe.so (the HBM rate probes the
-benchmark compares it with).
+dispatch/combine path), libepdc_layer.so (the gate, the experts' products and
+the gradients) and libepdc_probe.so (the HBM rate probes the benchmark
+compares the path with).
 
 Flags: -O3 without fast-math (IEEE fp32 division, denormals kept), and the
 packed-fp32 instructions disabled for device code: hipcc would otherwise form
@@ -22,6 +23,12 @@ PROBE_SRC = os.path.join(PKG, "csrc", "hbm_probe.hip")
 PROBE_DEPS = [PROBE_SRC, os.path.join(ROOT, "include", "epdc_probe.h"),
               os.path.join(ROOT, "include", "epdc.h")]
 PROBE_LIB = os.path.join(PKG, "libepdc_probe.so")
+LAYER_SRC = os.path.join(PKG, "csrc", "layer.hip")
+LAYER_DEPS = [LAYER_SRC, os.path.join(PKG, "csrc", "layer_product.hpp"),
+              os.path.join(PKG, "csrc", "layer_gate.hpp"),
+              os.path.join(ROOT, "include", "epdc_layer.h"),
+              os.path.join(ROOT, "include", "epdc.h")]
+LAYER_LIB = os.path.join(PKG, "libepdc_layer.so")
 ARCH = "gfx950"
 
 
@@ -52,8 +59,10 @@ def _compile(src: str, lib: str, verbose: bool) -> None:
 
 
 def build(verbose: bool = False) -> str:
-    """Compile libepdc.so and libepdc_probe.so (always; a few seconds)."""
+    """Compile libepdc.so, libepdc_layer.so and libepdc_probe.so (always; some
+    tens of seconds)."""
     _compile(SRC, LIB, verbose)
+    _compile(LAYER_SRC, LAYER_LIB, verbose)
     _compile(PROBE_SRC, PROBE_LIB, verbose)
     _write_build_info()
     return LIB
@@ -79,7 +88,7 @@ def _write_build_info() -> None:
 
 
 def is_stale() -> bool:
-    for lib, deps in ((LIB, DEPS), (PROBE_LIB, PROBE_DEPS)):
+    for lib, deps in ((LIB, DEPS), (LAYER_LIB, LAYER_DEPS), (PROBE_LIB, PROBE_DEPS)):
         if not os.path.exists(lib):
             return True
         t = os.path.getmtime(lib)

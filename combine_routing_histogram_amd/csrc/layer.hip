@@ -1,0 +1,486 @@
+// layer.hip -- host side of the C ABI declared in include/epdc_layer.h: argument
+// checks, the choice of kernel form, and the launches.  Nothing here waits for
+// the device or allocates.
+#include "epdc_layer.h"
+#include "layer_product.hpp"
+#include "layer_gate.hpp"
+
+#include <hip/hip_runtime.h>
+
+#include <cstdarg>
+#include <cstdio>
+#include <string>
+
+using namespace epdc_layer;
+
+namespace {
+
+thread_local std::string g_last_error;
+
+epdc_status fail(epdc_status s, const char *fmt, ...)
+{
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    g_last_error = buf;
+    return s;
+}
+
+epdc_status ok()
+{
+    g_last_error.clear();
+    return EPDC_SUCCESS;
+}
+
+bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+
+template <typename F>
+epdc_status launch(const char *name, F &&f)
+{
+    f();
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess)
+        return fail(EPDC_ERR_GPU_OP, "%s launch failed: %s", name, hipGetErrorString(err));
+    return EPDC_SUCCESS;
+}
+
+// ---- gate -------------------------------------------------------------------
+
+constexpr int kMaxFeatures = 1 << 20;
+constexpr int64_t kMaxExpertBytes = (int64_t)0x7fff0000;
+
+int gate_blocks(int64_t tokens, int limit)
+{
+    const int64_t b = (tokens + kGateTokens - 1) / kGateTokens;
+    return (int)(b < 1 ? 1 : (b < limit ? b : limit));
+}
+
+epdc_status check_gate(const epdc_gate_args *g)
+{
+    if (!g)
+        return fail(EPDC_ERR_INVALID_ARGS, "args is NULL");
+    if (g->num_tokens < 0)
+        return fail(EPDC_ERR_INVALID_ARGS, "num_tokens must be >= 0");
+    if (g->num_experts < 1 || g->num_experts > kMaxExperts)
+        return fail(EPDC_ERR_INVALID_ARGS, "num_experts must be in [1, %d]", kMaxExperts);
+    if (g->topk < 1 || g->topk > kMaxTopk || g->topk > g->num_experts)
+        return fail(EPDC_ERR_INVALID_ARGS, "topk must be in [1, %d] and at most num_experts",
+                    kMaxTopk);
+    if (g->score != EPDC_GATE_SOFTMAX && g->score != EPDC_GATE_SIGMOID)
+        return fail(EPDC_ERR_INVALID_ARGS, "unknown score %d", g->score);
+    if (g->logits_dtype != EPDC_DT_FP32 && g->logits_dtype != EPDC_DT_BF16)
+        return fail(EPDC_ERR_INVALID_ARGS, "logits must be fp32 or bf16");
+    if (!(g->scale > 0.0f) || g->scale > 3.4e38f)
+        return fail(EPDC_ERR_INVALID_ARGS, "scale must be positive and finite");
+    if (g->num_tokens > 0 && !g->logits)
+        return fail(EPDC_ERR_INVALID_ARGS, "logits is required");
+    if (!aligned(g->logits, 16) || !aligned(g->bias, 4))
+        return fail(EPDC_ERR_INVALID_ARGS, "logits must be 16-byte aligned, bias 4-byte aligned");
+    return EPDC_SUCCESS;
+}
+
+GateArgs gate_args(const epdc_gate_args *g)
+{
+    GateArgs a = {};
+    a.tokens = g->num_tokens;
+    a.experts = g->num_experts;
+    a.topk = g->topk;
+    a.score = g->score;
+    a.renorm = g->renormalize != 0;
+    a.bf16 = g->logits_dtype == EPDC_DT_BF16;
+    a.scale = g->scale;
+    a.logits = g->logits;
+    a.bias = g->bias;
+    a.mask = g->mask;
+    return a;
+}
+
+template <bool kBalance>
+void launch_gate(int grid, size_t lds, hipStream_t st, const GateArgs &a)
+{
+    if (a.experts <= 64)
+        k_gate<4, kBalance><<<grid, kGateThreads, lds, st>>>(a);
+    else if (a.experts <= 128)
+        k_gate<8, kBalance><<<grid, kGateThreads, lds, st>>>(a);
+    else if (a.experts <= 256)
+        k_gate<16, kBalance><<<grid, kGateThreads, lds, st>>>(a);
+    else
+        k_gate<32, kBalance><<<grid, kGateThreads, lds, st>>>(a);
+}
+
+void launch_gate_backward(int grid, size_t lds, hipStream_t st, const GateArgs &a)
+{
+    if (a.experts <= 64)
+        k_gate_backward<4><<<grid, kGateThreads, lds, st>>>(a);
+    else if (a.experts <= 128)
+        k_gate_backward<8><<<grid, kGateThreads, lds, st>>>(a);
+    else if (a.experts <= 256)
+        k_gate_backward<16><<<grid, kGateThreads, lds, st>>>(a);
+    else
+        k_gate_backward<32><<<grid, kGateThreads, lds, st>>>(a);
+}
+
+// ---- products -----------------------------------------------------------------
+
+epdc_status check_product(const epdc_product_args *p)
+{
+    if (!p)
+        return fail(EPDC_ERR_INVALID_ARGS, "args is NULL");
+    if (p->rows < 0 || p->rows > (1 << 30))
+        return fail(EPDC_ERR_INVALID_ARGS, "rows must be in [0, 2^30]");
+    if (p->num_experts < 1 || p->num_experts > kMaxExperts)
+        return fail(EPDC_ERR_INVALID_ARGS, "num_experts must be in [1, %d]", kMaxExperts);
+    if (p->activation < EPDC_ACT_NONE || p->activation > EPDC_ACT_GEGLU)
+        return fail(EPDC_ERR_INVALID_ARGS, "unknown activation %d", p->activation);
+    if (p->dtype != EPDC_DT_BF16 && p->dtype != EPDC_DT_E4M3)
+        return fail(EPDC_ERR_INVALID_ARGS, "operands must be bf16 or e4m3");
+    const bool e4m3 = p->dtype == EPDC_DT_E4M3;
+    const int unit_in = e4m3 ? 128 : 8, unit_out = act_gated(p->activation) ? 16 : 8;
+    if (p->in_features < unit_in || p->in_features > kMaxFeatures || p->in_features % unit_in)
+        return fail(EPDC_ERR_INVALID_ARGS, "in_features must be a multiple of %d, at most 2^20",
+                    unit_in);
+    if (p->out_features < unit_out || p->out_features > kMaxFeatures ||
+        p->out_features % unit_out)
+        return fail(EPDC_ERR_INVALID_ARGS, "out_features must be a multiple of %d, at most 2^20",
+                    unit_out);
+    if ((int64_t)p->in_features * p->out_features * (e4m3 ? 1 : 2) > kMaxExpertBytes)
+        return fail(EPDC_ERR_INVALID_ARGS, "one expert's weight must be smaller than 2 GiB");
+    if (!p->expert_off)
+        return fail(EPDC_ERR_INVALID_ARGS, "expert_off is required");
+    if (!aligned(p->expert_off, 4) || !aligned(p->bias, 4) || !aligned(p->scales, 4) ||
+        !aligned(p->weight_scales, 4) || !aligned(p->input, 16) || !aligned(p->weight, 16))
+        return fail(EPDC_ERR_INVALID_ARGS,
+                    "input and weight must be 16-byte aligned, the other arrays 4-byte aligned");
+    return EPDC_SUCCESS;
+}
+
+// Row tiles that the experts' row counts can make at most, known to the device only.
+int64_t row_tile_bound(int64_t rows, int experts, int bm)
+{
+    const int64_t with_rows = rows < experts ? rows : experts;
+    return (rows + with_rows * (bm - 1)) / bm;
+}
+
+epdc_status grid_of(int64_t tiles, int *grid)
+{
+    const int64_t g = (tiles + kXcds - 1) / kXcds * kXcds;
+    if (g > 0x7fffffff)
+        return fail(EPDC_ERR_INVALID_ARGS, "more tiles than a launch can hold");
+    *grid = (int)g;
+    return EPDC_SUCCESS;
+}
+
+template <int kProduct, bool kE4m3, int kBM, int kBN, int kWM, int kWN>
+epdc_status launch_tile(const char *name, hipStream_t st, ProductArgs &a, int cols_per_tile)
+{
+    a.col_tiles = (a.out_cols + cols_per_tile - 1) / cols_per_tile;
+    int64_t tiles;
+    if (kProduct == kGradWeight) {
+        a.row_tiles = (a.out_rows + kBM - 1) / kBM;
+        tiles = (int64_t)a.experts * a.row_tiles * a.col_tiles;
+    } else {
+        tiles = row_tile_bound(a.rows, a.experts, kBM) * a.col_tiles;
+    }
+    int grid;
+    const epdc_status s = grid_of(tiles, &grid);
+    if (s != EPDC_SUCCESS)
+        return s;
+    return launch(name, [&] {
+        k_product_tile<kProduct, kE4m3, kBM, kBN, kWM, kWN>
+            <<<grid, kWM * kWN * kWave, 0, st>>>(a);
+    });
+}
+
+template <bool kE4m3, int kMI>
+epdc_status launch_stream(hipStream_t st, ProductArgs &a)
+{
+    a.col_tiles = (a.out_cols + 15) / 16;
+    int grid;
+    const epdc_status s = grid_of(row_tile_bound(a.rows, a.experts, kMI * 16) * a.col_tiles, &grid);
+    if (s != EPDC_SUCCESS)
+        return s;
+    return launch("k_product_stream", [&] {
+        if (act_gated(a.act))
+            k_product_stream<kE4m3, kMI, true><<<grid, kStreamWaves * kWave, 0, st>>>(a);
+        else
+            k_product_stream<kE4m3, kMI, false><<<grid, kStreamWaves * kWave, 0, st>>>(a);
+    });
+}
+
+template <bool kE4m3>
+epdc_status launch_forward(hipStream_t st, ProductArgs &a)
+{
+    const bool gated = act_gated(a.act);
+    const int64_t mean = (int64_t)a.rows / a.experts;
+    if (mean <= 8)
+        return launch_stream<kE4m3, 1>(st, a);
+    if (mean <= 64)
+        return launch_tile<kForward, kE4m3, 64, 256, 2, 4>("k_product_tile", st, a,
+                                                           gated ? 128 : 256);
+    return launch_tile<kForward, kE4m3, 256, 256, 2, 4>("k_product_tile", st, a, gated ? 128 : 256);
+}
+
+}  // namespace
+
+extern "C" {
+
+epdc_status epdc_gate_scratch_bytes(int32_t max_tokens, int32_t num_experts, size_t *bytes)
+{
+    if (max_tokens < 0 || num_experts < 1 || num_experts > kMaxExperts || !bytes)
+        return fail(EPDC_ERR_INVALID_ARGS, "max_tokens >= 0, num_experts in [1, %d] and bytes "
+                                           "are required", kMaxExperts);
+    *bytes = 256 + sizeof(float) * (size_t)gate_blocks(max_tokens, kGateMaxBlocks) *
+                       (size_t)gate_partial_words(num_experts);
+    return ok();
+}
+
+epdc_status epdc_gate(const epdc_gate_args *args, void *stream, float *weights, int32_t *indices,
+                      int32_t *counts, float *losses, void *scratch)
+{
+    epdc_status s = check_gate(args);
+    if (s != EPDC_SUCCESS)
+        return s;
+    if (args->num_tokens > 0 && (!weights || !indices))
+        return fail(EPDC_ERR_INVALID_ARGS, "weights and indices are required");
+    const bool balance = counts != nullptr;
+    if ((losses != nullptr) != balance || (scratch != nullptr) != balance)
+        return fail(EPDC_ERR_INVALID_ARGS,
+                    "counts, losses and scratch must all be given or all NULL");
+    if (!aligned(weights, 4) || !aligned(indices, 4) || !aligned(counts, 4) ||
+        !aligned(losses, 4) || !aligned(scratch, 256))
+        return fail(EPDC_ERR_INVALID_ARGS,
+                    "scratch must be 256-byte aligned, the other outputs 4-byte aligned");
+    if (args->num_tokens == 0 && !balance)
+        return ok();
+    GateArgs a = gate_args(args);
+    a.weights = weights;
+    a.indices = indices;
+    a.counts = counts;
+    a.losses = losses;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    if (balance) {
+        a.ticket = static_cast<uint32_t *>(scratch);
+        a.partial = reinterpret_cast<float *>(static_cast<uint8_t *>(scratch) + 256);
+        const int grid = gate_blocks(a.tokens, kGateMaxBlocks);
+        const size_t lds = sizeof(float) * ((size_t)a.experts + 1 +
+                                            kGateThreads / 64 * (size_t)a.experts + kGateTokens);
+        s = launch("k_gate", [&] { launch_gate<true>(grid, lds, st, a); });
+    } else {
+        s = launch("k_gate",
+                   [&] { launch_gate<false>(gate_blocks(a.tokens, 1 << 20), 0, st, a); });
+    }
+    return s == EPDC_SUCCESS ? ok() : s;
+}
+
+epdc_status epdc_gate_backward(const epdc_gate_args *args, void *stream, const int32_t *indices,
+                               const float *grad_weights, const int32_t *counts,
+                               const float *grad_losses, void *grad_logits)
+{
+    epdc_status s = check_gate(args);
+    if (s != EPDC_SUCCESS)
+        return s;
+    if ((counts != nullptr) != (grad_losses != nullptr))
+        return fail(EPDC_ERR_INVALID_ARGS, "counts and grad_losses must both be given or both NULL");
+    if (args->num_tokens > 0 && (!grad_logits || (grad_weights && !indices)))
+        return fail(EPDC_ERR_INVALID_ARGS,
+                    "grad_logits is required, and indices with grad_weights");
+    if (!aligned(grad_logits, 16) || !aligned(indices, 4) || !aligned(grad_weights, 4) ||
+        !aligned(counts, 4) || !aligned(grad_losses, 4))
+        return fail(EPDC_ERR_INVALID_ARGS,
+                    "grad_logits must be 16-byte aligned, the other arrays 4-byte aligned");
+    if (args->num_tokens == 0)
+        return ok();
+    GateArgs a = gate_args(args);
+    a.in_indices = indices;
+    a.grad_weights = grad_weights;
+    a.in_counts = counts;
+    a.grad_losses = grad_losses;
+    a.grad_logits = grad_logits;
+    const size_t lds = sizeof(float) * (size_t)a.experts;
+    s = launch("k_gate_backward", [&] {
+        launch_gate_backward(gate_blocks(a.tokens, 1 << 20), lds, static_cast<hipStream_t>(stream),
+                             a);
+    });
+    return s == EPDC_SUCCESS ? ok() : s;
+}
+
+epdc_status epdc_expert_product(const epdc_product_args *args, void *stream, const void *residual,
+                                void *out, void *preact)
+{
+    epdc_status s = check_product(args);
+    if (s != EPDC_SUCCESS)
+        return s;
+    const bool e4m3 = args->dtype == EPDC_DT_E4M3;
+    if (e4m3 != (args->scales != nullptr) || e4m3 != (args->weight_scales != nullptr))
+        return fail(EPDC_ERR_INVALID_ARGS,
+                    "scales and weight_scales belong to e4m3 operands, both of them");
+    if (args->rows > 0 && (!args->input || !args->weight || !out))
+        return fail(EPDC_ERR_INVALID_ARGS, "input, weight and out are required");
+    if (!aligned(residual, 16) || !aligned(out, 16) || !aligned(preact, 16))
+        return fail(EPDC_ERR_INVALID_ARGS, "residual, out and preact must be 16-byte aligned");
+    if (args->rows == 0)
+        return ok();
+    ProductArgs a = {};
+    a.rows = args->rows;
+    a.experts = args->num_experts;
+    a.contract = args->in_features;
+    a.p_bytes = a.q_bytes = args->in_features * (e4m3 ? 1 : 2);
+    a.weight_rows = args->out_features;
+    a.act = args->activation;
+    a.out_cols = act_gated(a.act) ? args->out_features / 2 : args->out_features;
+    a.p = static_cast<const uint8_t *>(args->input);
+    a.q = static_cast<const uint8_t *>(args->weight);
+    a.scales = args->scales;
+    a.weight_scales = args->weight_scales;
+    a.bias = args->bias;
+    a.residual = static_cast<const uint16_t *>(residual);
+    a.expert_off = args->expert_off;
+    a.out = static_cast<uint8_t *>(out);
+    a.preact = static_cast<uint16_t *>(preact);
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    s = e4m3 ? launch_forward<true>(st, a) : launch_forward<false>(st, a);
+    return s == EPDC_SUCCESS ? ok() : s;
+}
+
+epdc_status epdc_expert_backward(const epdc_product_args *args, void *stream,
+                                 const void *grad_out, const void *preact, void *dz,
+                                 void *grad_input, void *grad_weight, int32_t grad_weight_dtype,
+                                 float *grad_bias)
+{
+    epdc_status s = check_product(args);
+    if (s != EPDC_SUCCESS)
+        return s;
+    if (args->dtype != EPDC_DT_BF16)
+        return fail(EPDC_ERR_INVALID_ARGS, "the gradients take bf16 operands");
+    if (grad_weight_dtype != EPDC_DT_BF16 && grad_weight_dtype != EPDC_DT_FP32)
+        return fail(EPDC_ERR_INVALID_ARGS, "grad_weight must be bf16 or fp32");
+    const bool act = args->activation != EPDC_ACT_NONE;
+    if (args->rows > 0) {
+        if (!grad_out || (grad_input && !args->weight) || (grad_weight && !args->input))
+            return fail(EPDC_ERR_INVALID_ARGS, "grad_out is required, weight for grad_input and "
+                                               "input for grad_weight");
+        if (act && (!preact || (!dz && (grad_input || grad_weight))))
+            return fail(EPDC_ERR_INVALID_ARGS, "an activation's gradient needs preact and dz");
+    }
+    if (!aligned(grad_out, 16) || !aligned(preact, 16) || !aligned(dz, 16) ||
+        !aligned(grad_input, 16) || !aligned(grad_weight, 16) || !aligned(grad_bias, 4))
+        return fail(EPDC_ERR_INVALID_ARGS,
+                    "payload arrays must be 16-byte aligned, grad_bias 4-byte aligned");
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    const int in = args->in_features, of = args->out_features;
+    const void *z = grad_out;
+    if (act && args->rows > 0 && (grad_input || grad_weight)) {
+        ActGradArgs g = {};
+        g.rows = args->rows;
+        g.experts = args->num_experts;
+        g.act = args->activation;
+        g.cols = act_gated(g.act) ? of / 2 : of;
+        g.expert_off = args->expert_off;
+        g.grad_out = static_cast<const uint16_t *>(grad_out);
+        g.preact = static_cast<const uint16_t *>(preact);
+        g.dz = static_cast<uint16_t *>(dz);
+        const int blocks = (args->rows + kActRows - 1) / kActRows;
+        s = launch("k_act_grad", [&] {
+            k_act_grad<<<blocks < 16384 ? blocks : 16384, dim3(kWave, kActRows), 0, st>>>(g);
+        });
+        if (s != EPDC_SUCCESS)
+            return s;
+        z = dz;
+    }
+    ProductArgs a = {};
+    a.rows = args->rows;
+    a.experts = args->num_experts;
+    a.weight_rows = of;
+    a.p = static_cast<const uint8_t *>(z);
+    a.p_bytes = of * 2;
+    a.q_bytes = in * 2;
+    a.out_cols = in;
+    a.expert_off = args->expert_off;
+    if (grad_input && args->rows > 0) {
+        ProductArgs g = a;
+        g.contract = of;
+        g.q = static_cast<const uint8_t *>(args->weight);
+        g.out = static_cast<uint8_t *>(grad_input);
+        s = launch_tile<kGradInput, false, 256, 256, 2, 4>("k_product_tile", st, g, 256);
+        if (s != EPDC_SUCCESS)
+            return s;
+    }
+    if (grad_weight) {
+        ProductArgs g = a;
+        g.out_rows = of;
+        g.out_fp32 = grad_weight_dtype == EPDC_DT_FP32;
+        g.q = static_cast<const uint8_t *>(args->input);
+        g.out = static_cast<uint8_t *>(grad_weight);
+        s = launch_tile<kGradWeight, false, 256, 256, 2, 4>("k_product_tile", st, g, 256);
+        if (s != EPDC_SUCCESS)
+            return s;
+    }
+    if (grad_bias) {
+        BiasGradArgs b = {};
+        b.rows = args->rows;
+        b.experts = args->num_experts;
+        b.cols = of;
+        b.expert_off = args->expert_off;
+        b.act = args->activation;
+        b.grad_out = static_cast<const uint16_t *>(grad_out);
+        b.preact = static_cast<const uint16_t *>(preact);
+        b.grad_bias = grad_bias;
+        const dim3 grid(args->num_experts, (of + kWave * 8 - 1) / (kWave * 8));
+        s = launch("k_bias_grad",
+                   [&] { k_bias_grad<<<grid, dim3(kWave, kBiasSlices), 0, st>>>(b); });
+        if (s != EPDC_SUCCESS)
+            return s;
+    }
+    return ok();
+}
+
+epdc_status epdc_combine_backward(void *stream, int32_t num_tokens, int32_t topk, int32_t hidden,
+                                  const int32_t *slot_of, const void *grad_output,
+                                  const void *input, const float *weights, void *grad_input,
+                                  float *grad_weights)
+{
+    if (num_tokens < 0 || topk < 1 || topk > kMaxTopk ||
+        (int64_t)num_tokens * topk > (int64_t)(1 << 30))
+        return fail(EPDC_ERR_INVALID_ARGS,
+                    "num_tokens >= 0, topk in [1, %d] and num_tokens*topk <= 2^30 are required",
+                    kMaxTopk);
+    if (hidden < 8 || hidden % 8 != 0 || hidden > (1 << 24))
+        return fail(EPDC_ERR_INVALID_ARGS, "hidden must be a positive multiple of 8, at most 2^24");
+    if (num_tokens > 0 && (!slot_of || !grad_output || (grad_weights && !input)))
+        return fail(EPDC_ERR_INVALID_ARGS, "slot_of and grad_output are required, and input with "
+                                           "grad_weights");
+    if (!aligned(slot_of, 4) || !aligned(grad_output, 16) || !aligned(input, 16) ||
+        !aligned(weights, 4) || !aligned(grad_input, 16) || !aligned(grad_weights, 4))
+        return fail(EPDC_ERR_INVALID_ARGS,
+                    "rows must be 16-byte aligned, the other arrays 4-byte aligned");
+    if (num_tokens == 0 || (!grad_input && !grad_weights))
+        return ok();
+    CombineGradArgs a = {};
+    a.tokens = num_tokens;
+    a.topk = topk;
+    a.row_vecs = hidden / 8;
+    a.slot_of = slot_of;
+    a.grad_output = static_cast<const uint8_t *>(grad_output);
+    a.input = static_cast<const uint8_t *>(input);
+    a.weights = weights;
+    a.grad_input = static_cast<uint8_t *>(grad_input);
+    a.grad_weights = grad_weights;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    const epdc_status s = launch("k_combine_grad", [&] {
+        switch (topk) {
+        case 1: k_combine_grad<1><<<num_tokens, kCombineGradThreads, 0, st>>>(a); break;
+        case 2: k_combine_grad<2><<<num_tokens, kCombineGradThreads, 0, st>>>(a); break;
+        case 4: k_combine_grad<4><<<num_tokens, kCombineGradThreads, 0, st>>>(a); break;
+        case 6: k_combine_grad<6><<<num_tokens, kCombineGradThreads, 0, st>>>(a); break;
+        case 8: k_combine_grad<8><<<num_tokens, kCombineGradThreads, 0, st>>>(a); break;
+        default: k_combine_grad<0><<<num_tokens, kCombineGradThreads, 0, st>>>(a); break;
+        }
+    });
+    return s == EPDC_SUCCESS ? ok() : s;
+}
+
+const char *epdc_layer_last_error(void) { return g_last_error.c_str(); }
+
+}  // extern "C"

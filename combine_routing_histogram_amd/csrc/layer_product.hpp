@@ -1,0 +1,836 @@
+// layer_product.hpp -- gfx950 kernels of the experts' matrix products over the
+// received rows: out = act(x W^T + b) + residual per expert, and the gradients
+// dx = dz W, dW = dz^T x, db = sum dz.
+//
+// All three products run through one tile kernel.  A tile is kBM "P" rows by
+// kBN "Q" columns; the MFMA's first operand is Q and its second P, so a lane
+// ends with four consecutive output columns of one row.  Operands go from
+// HBM to LDS by direct loads (16 bytes a lane, no registers between) and from
+// LDS to the matrix cores as fragments whose contraction index lies along a
+// lane's registers.  Where memory has the contraction along the rows (W of dx,
+// both operands of dW) the fragment is read with the transposing LDS load.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace epdc_layer {
+
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kWave = 64;
+constexpr int kMaxExperts = 512;
+constexpr int kXcds = 8;
+constexpr int kStepBytes = 128;  // contraction bytes of one LDS row (untransposed operand)
+
+enum Product { kForward, kGradInput, kGradWeight };
+
+enum Act { kActNone, kActRelu, kActGelu, kActSilu, kActSwiglu, kActGeglu };
+
+struct ProductArgs {
+    int32_t rows;        // rows of the received layout the call may touch
+    int32_t experts;
+    int32_t contract;    // contraction length (rows of the expert for kGradWeight)
+    int32_t p_bytes;     // bytes of a row of p
+    int32_t q_bytes;     // bytes of a row of q
+    int32_t out_rows;    // kGradWeight: rows of one expert's gradient
+    int32_t out_cols;    // columns of out
+    int32_t weight_rows; // out_features
+    int32_t col_tiles;   // column tiles of an expert
+    int32_t row_tiles;   // kGradWeight: row tiles of an expert
+    int32_t act;
+    int32_t out_fp32;    // kGradWeight: out holds fp32
+    const uint8_t *p, *q;
+    const float *scales, *weight_scales;  // e4m3
+    const float *bias;
+    const uint16_t *residual;
+    const int32_t *expert_off;
+    uint8_t *out;
+    uint16_t *preact;
+};
+
+__device__ inline int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+__device__ inline float bf16_to_f32(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
+
+__device__ inline bf16x4 to_bf16(f32x4 v)
+{
+    return bf16x4{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
+}
+
+// The activations, in fp32.  x / (1 + exp(-x)) tends to -0 for large negative
+// x; exp and the reciprocal are the hardware's (about 1 ulp each, far below
+// the rounding of the bf16 result).
+__device__ inline float act_silu(float x)
+{
+    return x * __builtin_amdgcn_rcpf(1.0f + __expf(-x));
+}
+__device__ inline float act_gelu(float x) { return 0.5f * x * (1.0f + erff(x * 0.70710678f)); }
+
+__device__ inline float act_one(int act, float x)
+{
+    switch (act) {
+    case kActRelu: return x > 0.0f ? x : (x != x ? x : 0.0f);
+    case kActGelu:
+    case kActGeglu: return act_gelu(x);
+    case kActSilu:
+    case kActSwiglu: return act_silu(x);
+    default: return x;
+    }
+}
+
+__device__ inline float act_one_grad(int act, float x)
+{
+    switch (act) {
+    case kActRelu: return x > 0.0f ? 1.0f : (x != x ? x : 0.0f);
+    case kActGelu:
+    case kActGeglu:
+        return 0.5f * (1.0f + erff(x * 0.70710678f)) +
+               x * 0.39894228f * __expf(-0.5f * x * x);
+    case kActSilu:
+    case kActSwiglu: {
+        const float s = __builtin_amdgcn_rcpf(1.0f + __expf(-x));
+        return s * (1.0f + x * (1.0f - s));
+    }
+    default: return 1.0f;
+    }
+}
+
+__host__ __device__ inline bool act_gated(int act) { return act >= kActSwiglu; }
+
+// ---------------------------------------------------------------------------
+// Which tile a block computes
+// ---------------------------------------------------------------------------
+//
+// Tiles are numbered expert by expert, inside an expert rows fastest, so that
+// neighbours share the weight tile (same columns) or the row tile.  Blocks go
+// to the 8 XCDs in turn; block b takes tile (b % 8) * ceil(total/8) + b/8, so
+// that each XCD works on one contiguous run of tiles and its L2 serves the
+// neighbours.  The counts per expert are on the device only: every block scans
+// the offsets (at most 513 ints, in L2), and blocks past the total end.
+
+struct Tile {
+    int expert, row0, rows, row_tile, col_tile;
+};
+
+__device__ inline int clamp_row(const int32_t *off, int i, int rows)
+{
+    const int v = off[i];
+    return v < 0 ? 0 : (v > rows ? rows : v);
+}
+
+// lds: int[kThreads / 64 + 4].  Returns false (in the whole block) past the total.
+template <int kThreads>
+__device__ inline bool find_tile(const ProductArgs &a, int bm, int *lds, Tile &t)
+{
+    constexpr int kEach = (kMaxExperts + kThreads - 1) / kThreads;
+    constexpr int kWaves = kThreads / kWave;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid / kWave;
+    int r0[kEach], n[kEach], cnt = 0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        const int e = tid * kEach + i;
+        r0[i] = n[i] = 0;
+        if (e < a.experts) {
+            r0[i] = clamp_row(a.expert_off, e, a.rows);
+            const int r1 = clamp_row(a.expert_off, e + 1, a.rows);
+            n[i] = r1 > r0[i] ? r1 - r0[i] : 0;
+        }
+        cnt += (n[i] + bm - 1) / bm;
+    }
+    cnt *= a.col_tiles;
+    int incl = cnt;
+#pragma unroll
+    for (int d = 1; d < kWave; d <<= 1) {
+        const int u = __shfl_up(incl, d, kWave);
+        if (lane >= d)
+            incl += u;
+    }
+    if (lane == kWave - 1)
+        lds[wave] = incl;
+    __syncthreads();
+    int total = 0, before = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+        const int v = lds[w];
+        before += w < wave ? v : 0;
+        total += v;
+    }
+    const int per_xcd = (total + kXcds - 1) / kXcds;
+    const int slot = blockIdx.x / kXcds;
+    const int id = (int)(blockIdx.x % kXcds) * per_xcd + slot;
+    if (slot >= per_xcd || id >= total)
+        return false;
+    int first = before + incl - cnt;
+    if (id >= first && id < first + cnt) {
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const int mt = (n[i] + bm - 1) / bm, c = mt * a.col_tiles;
+            if (id >= first && id < first + c) {
+                lds[kWaves] = tid * kEach + i;
+                lds[kWaves + 1] = id - first;
+                lds[kWaves + 2] = r0[i];
+                lds[kWaves + 3] = n[i];
+            }
+            first += c;
+        }
+    }
+    __syncthreads();
+    t.expert = uniform(lds[kWaves]);
+    const int local = uniform(lds[kWaves + 1]);
+    const int start = uniform(lds[kWaves + 2]), have = uniform(lds[kWaves + 3]);
+    const int mt = (have + bm - 1) / bm;
+    t.col_tile = local / mt;
+    t.row_tile = local - t.col_tile * mt;
+    t.row0 = start + t.row_tile * bm;
+    const int left = have - t.row_tile * bm;
+    t.rows = left < bm ? left : bm;
+    return true;
+}
+
+// ---------------------------------------------------------------------------
+// Operand tiles in LDS
+// ---------------------------------------------------------------------------
+
+typedef __attribute__((address_space(3))) uint8_t lds_byte;
+
+__device__ inline __amdgpu_buffer_rsrc_t buffer_at(const uint8_t *base, uint32_t bytes)
+{
+    return __builtin_amdgcn_make_buffer_rsrc((void *)base, 0, (int)bytes, 0x00020000);
+}
+
+constexpr uint32_t kNowhere = 0x80000000u;  // past every buffer below: the load gives zeros
+constexpr uint32_t kOpen = 0x7fffffffu;
+
+// Row `r` of the MFMA's Q operand in a gated product: inside a wave's 64 rows
+// the first half are gate rows, the second half the up rows of the same
+// columns, so that a lane holds both factors of its outputs.
+__device__ inline int gated_row(int r, int col0, int half)
+{
+    const int c = col0 + (r / 64) * 32 + (r % 32);
+    const int cc = c < half ? c : half - 1;
+    return (r % 64) < 32 ? cc : half + cc;
+}
+
+// An operand whose contraction index runs along memory rows: LDS holds kRows
+// rows of 128 bytes.  A direct load fills 1 KiB (8 rows) of LDS in lane order,
+// so the bank swizzle -- 16-byte chunk c of row r sits at chunk c ^ (r & 7) --
+// is applied to the address a lane loads from.  Fragment reads of 16 rows x 16
+// bytes then touch every bank evenly.
+template <int kRows, int kWaves>
+struct StraightTile {
+    static constexpr int kBytes = kRows * kStepBytes;
+    static constexpr int kLoads = kRows / 8 / kWaves;
+    static_assert(kRows % (8 * kWaves) == 0, "whole loads per wave");
+    uint32_t off[kLoads];
+    const uint8_t *base;
+    int chunk;  // of this lane, in elements of 16 bytes
+
+    // row(r): the source row of LDS row r, in bounds
+    template <typename F>
+    __device__ inline void init(const uint8_t *b, int row_bytes, int wave, int lane, F &&row)
+    {
+        base = b;
+        chunk = (lane & 7) ^ (lane >> 3);
+#pragma unroll
+        for (int d = 0; d < kLoads; ++d)
+            off[d] = (uint32_t)row((d * kWaves + wave) * 8 + (lane >> 3)) * (uint32_t)row_bytes +
+                     (uint32_t)chunk * 16;
+    }
+    // step: which 128 bytes of the rows; left: contraction bytes from there on
+    __device__ inline void load(uint8_t *lds, int step, int left, int wave)
+    {
+        const __amdgpu_buffer_rsrc_t rs = buffer_at(base + (size_t)step * kStepBytes, kOpen);
+        const bool out = chunk * 16 >= left;
+#pragma unroll
+        for (int d = 0; d < kLoads; ++d)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                rs, (lds_byte *)(lds + (d * kWaves + wave) * 1024), 16, out ? kNowhere : off[d], 0,
+                0, 0);
+    }
+    // 16 rows from row0; half 0 or 1 of the step.  Lane l: row l % 16, 16 bytes.
+    __device__ static inline i32x4 frag(const uint8_t *lds, int row0, int half, int lane)
+    {
+        const int r = row0 + (lane & 15);
+        const int c = (half * 4 + (lane >> 4)) ^ (lane & 7);
+        return *reinterpret_cast<const i32x4 *>(lds + r * kStepBytes + c * 16);
+    }
+};
+
+// An operand whose contraction index runs across memory rows (bf16): LDS holds
+// 64 contraction rows of kCols elements.  The transposing read takes 8 bytes
+// per lane, four rows by 32 bytes per 16 lanes; chunk pairs are swizzled by
+// the row (r & 3, and bit 3) so that the rows of one read and its neighbour
+// lie in different banks.
+template <int kCols, int kWaves>
+struct CrossTile {
+    static constexpr int kRowBytes = kCols * 2;
+    static constexpr int kBytes = 64 * kRowBytes;
+    static constexpr int kChunks = kRowBytes / 16;
+    static constexpr int kRowsPerLoad = 64 / kChunks;
+    static constexpr int kLoads = kBytes / 1024 / kWaves;
+    static_assert(kChunks <= 64 && kChunks >= 16, "a load covers whole rows");
+    static_assert(kBytes % (1024 * kWaves) == 0, "whole loads per wave");
+    uint32_t off[kLoads];
+    const uint8_t *base;
+    int row_bytes;
+
+    __device__ static inline int key(int r) { return ((r & 3) | ((r >> 1) & 4)) << 1; }
+
+    // b: the first contraction row; col0_bytes: of the tile's first column
+    __device__ inline void init(const uint8_t *b, int rb, uint32_t col0_bytes, int wave, int lane)
+    {
+        base = b;
+        row_bytes = rb;
+#pragma unroll
+        for (int d = 0; d < kLoads; ++d) {
+            const int r = (d * kWaves + wave) * kRowsPerLoad + lane / kChunks;
+            off[d] = (uint32_t)r * (uint32_t)rb + col0_bytes +
+                     (uint32_t)((lane % kChunks) ^ key(r)) * 16;
+        }
+    }
+    // left: contraction rows from this step on; later rows read as zeros, and
+    // so does whatever a ragged column tile takes behind the last of them
+    __device__ inline void load(uint8_t *lds, int step, int left, int wave)
+    {
+        const uint32_t rows = left < 64 ? left : 64;
+        const __amdgpu_buffer_rsrc_t rs =
+            buffer_at(base + (size_t)step * 64 * row_bytes, rows * (uint32_t)row_bytes);
+#pragma unroll
+        for (int d = 0; d < kLoads; ++d)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                rs, (lds_byte *)(lds + (d * kWaves + wave) * 1024), 16, off[d], 0, 0, 0);
+    }
+    // 16 columns from col0, contraction rows half*32 + (lane/16)*8 ... +7
+    __device__ static inline i32x4 frag(const uint8_t *lds, int col0, int half, int lane)
+    {
+        const int g = lane >> 4, q = lane & 3, r = (lane >> 2) & 3;
+        const int row = half * 32 + g * 8 + r;
+        const int c = ((col0 >> 3) + (q >> 1)) ^ key(row);
+        const uint8_t *p = lds + row * kRowBytes + c * 16 + (q & 1) * 8;
+        typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p);
+        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + 4 * kRowBytes));
+        const s16x8 v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+        return __builtin_bit_cast(i32x4, v);
+    }
+};
+
+template <bool kCross, int kExtent, int kWaves>
+struct PickTile {
+    typedef StraightTile<kExtent, kWaves> type;
+};
+template <int kExtent, int kWaves>
+struct PickTile<true, kExtent, kWaves> {
+    typedef CrossTile<kExtent, kWaves> type;
+};
+
+__device__ inline f32x4 mfma_bf16(i32x4 a, i32x4 b, f32x4 c)
+{
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+// e4m3 x e4m3 over 128 contraction elements; the block scales of the
+// instruction are 1 (exponent byte 127).  The matrix cores cut the products of
+// 8 consecutive elements off at 2^-13 of the largest exponent among them
+// before they add them in fp32 (the instruction over 32 elements does the
+// same); the only way round it is to widen the codes to bf16, at half the
+// rate, for errors that lie 2^-15 or so of the result below its bf16 rounding.
+__device__ inline f32x4 mfma_e4m3(i32x8 a, i32x8 b, f32x4 c)
+{
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 0x7f7f7f7f, 0,
+                                                            0x7f7f7f7f);
+}
+
+__device__ inline i32x8 join(i32x4 a, i32x4 b)
+{
+    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// Four consecutive output columns of one row: bias, activation and residual in
+// fp32, one rounding.  z: the product; up: its second half (gated).
+__device__ inline void finish_forward(const ProductArgs &a, int expert, int row, int col,
+                                      f32x4 z, f32x4 up)
+{
+    const bool gated = act_gated(a.act);
+    if (a.bias) {
+        const float *b = a.bias + (size_t)expert * a.weight_rows + col;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            z[i] += b[i];
+            if (gated)
+                up[i] += b[a.out_cols + i];
+        }
+    }
+    if (a.preact) {
+        uint16_t *z0 = a.preact + (size_t)row * a.weight_rows + col;
+        *reinterpret_cast<bf16x4 *>(z0) = to_bf16(z);
+        if (gated)
+            *reinterpret_cast<bf16x4 *>(z0 + a.out_cols) = to_bf16(up);
+    }
+    f32x4 y;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        y[i] = act_one(a.act, z[i]);
+        if (gated)
+            y[i] *= up[i];
+    }
+    const size_t at = (size_t)row * a.out_cols + col;
+    if (a.residual) {
+        const ushort4 r = *reinterpret_cast<const ushort4 *>(a.residual + at);
+        y += f32x4{bf16_to_f32(r.x), bf16_to_f32(r.y), bf16_to_f32(r.z), bf16_to_f32(r.w)};
+    }
+    *reinterpret_cast<bf16x4 *>(a.out + at * 2) = to_bf16(y);
+}
+
+// ---------------------------------------------------------------------------
+// The tile kernel
+// ---------------------------------------------------------------------------
+
+template <int kProduct, bool kE4m3, int kBM, int kBN, int kWavesM, int kWavesN>
+__global__ __launch_bounds__(kWavesM *kWavesN *kWave) void k_product_tile(const ProductArgs a)
+{
+#ifdef __HIP_DEVICE_COMPILE__  // the host pass needs the launch stub only
+    constexpr int kWaves = kWavesM * kWavesN;
+    constexpr int kMI = kBM / kWavesM / 16, kNJ = kBN / kWavesN / 16;
+    static_assert(kProduct != kForward || kBN / kWavesN == 64, "gated columns pair inside 64");
+    typedef typename PickTile<kProduct == kGradWeight, kBM, kWaves>::type PTile;
+    typedef typename PickTile<kProduct != kForward, kBN, kWaves>::type QTile;
+    constexpr int kStage = PTile::kBytes + QTile::kBytes;
+    __shared__ __align__(1024) uint8_t lds[2 * kStage];
+
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x / kWave);
+    const int wm = wave / kWavesN, wn = wave % kWavesN;
+
+    Tile t;
+    int contract = a.contract;  // elements
+    if (kProduct == kGradWeight) {
+        const int per = a.row_tiles * a.col_tiles, total = per * a.experts;
+        const int per_xcd = (total + kXcds - 1) / kXcds, slot = blockIdx.x / kXcds;
+        const int id = (int)(blockIdx.x % kXcds) * per_xcd + slot;
+        if (slot >= per_xcd || id >= total)
+            return;
+        t.expert = id / per;
+        const int local = id - t.expert * per;
+        t.col_tile = local / a.row_tiles;
+        t.row_tile = local - t.col_tile * a.row_tiles;
+        t.row0 = uniform(clamp_row(a.expert_off, t.expert, a.rows));
+        contract = uniform(clamp_row(a.expert_off, t.expert + 1, a.rows)) - t.row0;
+        contract = contract < 0 ? 0 : contract;
+        t.rows = a.out_rows - t.row_tile * kBM;
+        t.rows = t.rows < kBM ? t.rows : kBM;
+    } else {
+        if (!find_tile<kWaves * kWave>(a, kBM, reinterpret_cast<int *>(lds), t))
+            return;
+        __syncthreads();  // the scan's LDS becomes the operands'
+    }
+    const bool gated = kProduct == kForward && act_gated(a.act);
+    const int col0 = t.col_tile * (gated ? kBN / 2 : kBN);
+
+    PTile pt;
+    QTile qt;
+    if constexpr (kProduct == kGradWeight)
+        pt.init(a.p + (size_t)t.row0 * a.p_bytes, a.p_bytes, (uint32_t)(t.row_tile * kBM) * 2,
+                wave, lane);
+    else
+        pt.init(a.p + (size_t)t.row0 * a.p_bytes, a.p_bytes, wave, lane,
+                [&](int r) { return r < t.rows ? r : t.rows - 1; });
+    if constexpr (kProduct == kForward) {
+        const int n = a.weight_rows;
+        qt.init(a.q + (size_t)t.expert * n * a.q_bytes, a.q_bytes, wave, lane, [&](int r) {
+            if (gated)
+                return gated_row(r, col0, n / 2);
+            return col0 + r < n ? col0 + r : n - 1;
+        });
+    } else if constexpr (kProduct == kGradInput) {
+        qt.init(a.q + (size_t)t.expert * a.weight_rows * a.q_bytes, a.q_bytes, (uint32_t)col0 * 2,
+                wave, lane);
+    } else {
+        qt.init(a.q + (size_t)t.row0 * a.q_bytes, a.q_bytes, (uint32_t)col0 * 2, wave, lane);
+    }
+
+    f32x4 acc[kMI][kNJ];
+#pragma unroll
+    for (int i = 0; i < kMI; ++i)
+#pragma unroll
+        for (int j = 0; j < kNJ; ++j)
+            acc[i][j] = f32x4{0, 0, 0, 0};
+
+    constexpr int kStep = kE4m3 ? 128 : 64;  // contraction elements per step
+    constexpr int kElem = kE4m3 ? 1 : 2;
+    const int steps = (contract + kStep - 1) / kStep;
+    auto load = [&](int s, int buf) {
+        uint8_t *stage = lds + buf * kStage;
+        const int left = contract - s * kStep;
+        if constexpr (kProduct == kGradWeight)
+            pt.load(stage, s, left, wave);
+        else
+            pt.load(stage, s, left * kElem, wave);
+        if constexpr (kProduct == kForward)
+            qt.load(stage + PTile::kBytes, s, left * kElem, wave);
+        else
+            qt.load(stage + PTile::kBytes, s, left, wave);
+    };
+    if (steps > 0)
+        load(0, 0);
+
+    const int prow = wm * (kMI * 16), qrow = wn * (kNJ * 16);
+    // e4m3: the rows' scales and the columns' block scales, one step ahead
+    const float *sx[kMI], *sw[kNJ];
+    if constexpr (kE4m3) {
+        const int blocks = contract / 128;
+#pragma unroll
+        for (int i = 0; i < kMI; ++i) {
+            int r = prow + i * 16 + (lane & 15);
+            r = r < t.rows ? r : t.rows - 1;
+            sx[i] = a.scales + (size_t)(t.row0 + r) * blocks;
+        }
+#pragma unroll
+        for (int j = 0; j < kNJ; ++j) {
+            const int r = qrow + j * 16 + (lane >> 4) * 4;
+            int c = gated ? gated_row(r, col0, a.weight_rows / 2) : col0 + r;
+            c = c < a.weight_rows ? c : a.weight_rows - 1;
+            sw[j] = a.weight_scales +
+                    ((size_t)t.expert * ((a.weight_rows + 127) / 128) + c / 128) * blocks;
+        }
+    }
+
+    for (int s = 0; s < steps; ++s) {
+        __syncthreads();  // step s has landed, and every wave is done with step s - 1
+        if (s + 1 < steps)
+            load(s + 1, (s + 1) & 1);
+        const uint8_t *ps = lds + (s & 1) * kStage, *qs = ps + PTile::kBytes;
+        if constexpr (kE4m3) {
+            i32x8 q[kNJ];
+            float fw[kNJ];
+#pragma unroll
+            for (int j = 0; j < kNJ; ++j) {
+                q[j] = join(QTile::frag(qs, qrow + j * 16, 0, lane),
+                            QTile::frag(qs, qrow + j * 16, 1, lane));
+                fw[j] = sw[j][s];
+            }
+#pragma unroll
+            for (int i = 0; i < kMI; ++i) {
+                const i32x8 p = join(PTile::frag(ps, prow + i * 16, 0, lane),
+                                     PTile::frag(ps, prow + i * 16, 1, lane));
+                const float fx = sx[i][s];
+#pragma unroll
+                for (int j = 0; j < kNJ; ++j) {
+                    const f32x4 d = mfma_e4m3(q[j], p, f32x4{0, 0, 0, 0});
+                    const float f = fx * fw[j];
+#pragma unroll
+                    for (int v = 0; v < 4; ++v)
+                        acc[i][j][v] = __builtin_fmaf(d[v], f, acc[i][j][v]);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                i32x4 q[kNJ];
+#pragma unroll
+                for (int j = 0; j < kNJ; ++j)
+                    q[j] = QTile::frag(qs, qrow + j * 16, half, lane);
+#pragma unroll
+                for (int i = 0; i < kMI; ++i) {
+                    const i32x4 p = PTile::frag(ps, prow + i * 16, half, lane);
+#pragma unroll
+                    for (int j = 0; j < kNJ; ++j)
+                        acc[i][j] = mfma_bf16(q[j], p, acc[i][j]);
+                }
+            }
+        }
+    }
+
+    // lane: row l % 16 of each P block, columns 4 * (l / 16) ... +3 of each Q block
+#pragma unroll
+    for (int i = 0; i < kMI; ++i) {
+        const int r = prow + i * 16 + (lane & 15);
+        if (r >= t.rows)
+            continue;
+        if constexpr (kProduct == kForward) {
+            if (gated) {
+#pragma unroll
+                for (int j = 0; j < kNJ / 2; ++j) {
+                    const int c = col0 + wn * 32 + j * 16 + (lane >> 4) * 4;
+                    if (c < a.out_cols)
+                        finish_forward(a, t.expert, t.row0 + r, c, acc[i][j], acc[i][j + kNJ / 2]);
+                }
+                continue;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kNJ; ++j) {
+            const int c = col0 + qrow + j * 16 + (lane >> 4) * 4;
+            if (c >= a.out_cols)
+                continue;
+            if constexpr (kProduct == kForward) {
+                finish_forward(a, t.expert, t.row0 + r, c, acc[i][j], f32x4{0, 0, 0, 0});
+            } else {
+                const size_t row = kProduct == kGradInput
+                                       ? (size_t)(t.row0 + r)
+                                       : (size_t)t.expert * a.out_rows + t.row_tile * kBM + r;
+                const size_t at = row * a.out_cols + c;
+                if (kProduct == kGradWeight && a.out_fp32)
+                    *reinterpret_cast<f32x4 *>(a.out + at * 4) = acc[i][j];
+                else
+                    *reinterpret_cast<bf16x4 *>(a.out + at * 2) = to_bf16(acc[i][j]);
+            }
+        }
+    }
+#endif
+}
+
+// ---------------------------------------------------------------------------
+// Few rows per expert: the weights stream past them
+// ---------------------------------------------------------------------------
+//
+// With at most kMI * 16 rows per tile the weights are the traffic, each element
+// used once, so they go straight to registers.  A block owns 16 output columns
+// (gated: 16 gate and 16 up rows) of one row tile; its four waves take the
+// contraction's 128-byte steps in turn, so a block reads 512 contiguous bytes
+// of each weight row per round, and add up through LDS at the end.  A lane
+// takes 32 contiguous bytes of a row per step; the contraction index is thus
+// permuted inside a step, alike for both operands.
+
+constexpr int kStreamWaves = 4;
+
+template <bool kE4m3, int kMI, bool kGated>
+__global__ __launch_bounds__(kStreamWaves *kWave) void k_product_stream(const ProductArgs a)
+{
+    constexpr int kQ = kGated ? 2 : 1;
+    __shared__ __align__(16) f32x4 part[kStreamWaves][kMI * kQ][kWave];
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x / kWave);
+    Tile t;
+    if (!find_tile<kStreamWaves * kWave>(a, kMI * 16, reinterpret_cast<int *>(part), t))
+        return;
+    __syncthreads();
+    const int col0 = t.col_tile * 16;
+    const int at = (lane >> 4) * 32;  // this lane's bytes of a step
+    const uint8_t *qp[kQ], *pp[kMI];
+    const float *sx[kMI], *sw[kQ];
+    const int bytes = a.contract * (kE4m3 ? 1 : 2), blocks = a.contract / 128;
+#pragma unroll
+    for (int q = 0; q < kQ; ++q) {
+        int c = col0 + (lane & 15);
+        c = (c < a.out_cols ? c : a.out_cols - 1) + q * a.out_cols;
+        qp[q] = a.q + ((size_t)t.expert * a.weight_rows + c) * a.q_bytes + at;
+        if constexpr (kE4m3) {
+            c = col0 + (lane >> 4) * 4;
+            c = (c < a.out_cols ? c : a.out_cols - 1) + q * a.out_cols;
+            sw[q] = a.weight_scales +
+                    ((size_t)t.expert * ((a.weight_rows + 127) / 128) + c / 128) * blocks;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kMI; ++i) {
+        int r = i * 16 + (lane & 15);
+        r = t.row0 + (r < t.rows ? r : t.rows - 1);
+        pp[i] = a.p + (size_t)r * a.p_bytes + at;
+        if constexpr (kE4m3)
+            sx[i] = a.scales + (size_t)r * blocks;
+    }
+    f32x4 acc[kMI][kQ];
+#pragma unroll
+    for (int i = 0; i < kMI; ++i)
+#pragma unroll
+        for (int q = 0; q < kQ; ++q)
+            acc[i][q] = f32x4{0, 0, 0, 0};
+
+    auto one = [&](const i32x4 (&w)[kQ][2], const i32x4 (&x)[kMI][2], int s) {
+#pragma unroll
+        for (int i = 0; i < kMI; ++i) {
+#pragma unroll
+            for (int q = 0; q < kQ; ++q) {
+                if constexpr (kE4m3) {
+                    const f32x4 d = mfma_e4m3(join(w[q][0], w[q][1]), join(x[i][0], x[i][1]),
+                                              f32x4{0, 0, 0, 0});
+                    const float f = sx[i][s] * sw[q][s];
+#pragma unroll
+                    for (int v = 0; v < 4; ++v)
+                        acc[i][q][v] = __builtin_fmaf(d[v], f, acc[i][q][v]);
+                } else {
+                    acc[i][q] = mfma_bf16(w[q][0], x[i][0], acc[i][q]);
+                    acc[i][q] = mfma_bf16(w[q][1], x[i][1], acc[i][q]);
+                }
+            }
+        }
+    };
+    const int full = bytes / kStepBytes;
+    constexpr int kBatch = 4;
+    int s = wave;
+    for (; s + (kBatch - 1) * kStreamWaves < full; s += kBatch * kStreamWaves) {
+        i32x4 w[kBatch][kQ][2], x[kBatch][kMI][2];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const size_t o = (size_t)(s + b * kStreamWaves) * kStepBytes;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int q = 0; q < kQ; ++q)
+                    w[b][q][h] = __builtin_nontemporal_load(
+                        reinterpret_cast<const i32x4 *>(qp[q] + o + h * 16));
+#pragma unroll
+                for (int i = 0; i < kMI; ++i)
+                    x[b][i][h] = *reinterpret_cast<const i32x4 *>(pp[i] + o + h * 16);
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b)
+            one(w[b], x[b], s + b * kStreamWaves);
+    }
+    for (; s * kStepBytes < bytes; s += kStreamWaves) {
+        i32x4 w[kQ][2], x[kMI][2];
+        const size_t o = (size_t)s * kStepBytes;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const bool in = s * kStepBytes + at + h * 16 < bytes;  // past the row: zeros
+#pragma unroll
+            for (int q = 0; q < kQ; ++q)
+                w[q][h] = in ? *reinterpret_cast<const i32x4 *>(qp[q] + o + h * 16)
+                             : i32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int i = 0; i < kMI; ++i)
+                x[i][h] = in ? *reinterpret_cast<const i32x4 *>(pp[i] + o + h * 16)
+                             : i32x4{0, 0, 0, 0};
+        }
+        one(w, x, s);
+    }
+#pragma unroll
+    for (int i = 0; i < kMI; ++i)
+#pragma unroll
+        for (int q = 0; q < kQ; ++q)
+            part[wave][i * kQ + q][lane] = acc[i][q];
+    __syncthreads();
+    // wave i finishes row block i, adding the waves' parts in order
+    for (int i = wave; i < kMI; i += kStreamWaves) {
+        f32x4 z[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}};
+#pragma unroll
+        for (int q = 0; q < kQ; ++q)
+#pragma unroll
+            for (int w = 0; w < kStreamWaves; ++w)
+                z[q] += part[w][i * kQ + q][lane];
+        const int r = i * 16 + (lane & 15), c = col0 + (lane >> 4) * 4;
+        if (r < t.rows && c < a.out_cols)
+            finish_forward(a, t.expert, t.row0 + r, c, z[0], z[1]);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Gradient of the activation, and of the bias
+// ---------------------------------------------------------------------------
+
+struct ActGradArgs {
+    int32_t rows, experts, cols, act;  // cols: of grad_out (gated: half of preact's)
+    const int32_t *expert_off;
+    const uint16_t *grad_out, *preact;
+    uint16_t *dz;
+};
+
+constexpr int kActRows = 4;
+
+// dz = grad_out * act'(preact), 8 columns per lane; gated: both halves.  dz is
+// rounded to bf16 because the two products that follow take bf16 operands.
+__global__ __launch_bounds__(kActRows *kWave) void k_act_grad(const ActGradArgs a)
+{
+    const int r0 = clamp_row(a.expert_off, 0, a.rows);
+    const int r1 = clamp_row(a.expert_off, a.experts, a.rows);
+    const bool gated = act_gated(a.act);
+    const int zcols = gated ? 2 * a.cols : a.cols;
+    for (int64_t row = (int64_t)r0 + (int64_t)blockIdx.x * kActRows + threadIdx.y; row < r1;
+         row += (int64_t)gridDim.x * kActRows) {
+        const uint16_t *dy = a.grad_out + (size_t)row * a.cols;
+        const uint16_t *z = a.preact + (size_t)row * zcols;
+        uint16_t *dz = a.dz + (size_t)row * zcols;
+        for (int c = threadIdx.x * 8; c < a.cols; c += kWave * 8) {
+            const bf16x8 g = *reinterpret_cast<const bf16x8 *>(dy + c);
+            const bf16x8 z0 = *reinterpret_cast<const bf16x8 *>(z + c);
+            bf16x8 o;
+            if (gated) {
+                const bf16x8 z1 = *reinterpret_cast<const bf16x8 *>(z + a.cols + c);
+                bf16x8 u;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float d = (float)g[i], x = (float)z0[i];
+                    o[i] = (__bf16)(d * (float)z1[i] * act_one_grad(a.act, x));
+                    u[i] = (__bf16)(d * act_one(a.act, x));
+                }
+                *reinterpret_cast<bf16x8 *>(dz + a.cols + c) = u;
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    o[i] = (__bf16)((float)g[i] * act_one_grad(a.act, (float)z0[i]));
+            }
+            *reinterpret_cast<bf16x8 *>(dz + c) = o;
+        }
+    }
+}
+
+struct BiasGradArgs {
+    int32_t rows, experts, cols, act;  // cols: out_features
+    const int32_t *expert_off;
+    const uint16_t *grad_out, *preact;  // preact unused without an activation
+    float *grad_bias;                   // [experts, cols]
+};
+
+constexpr int kBiasSlices = 8;
+
+// Column sums of an expert's dz in fp32, from its factors rather than the rounded
+// dz: a block takes 512 columns, its eight waves every eighth row; the waves'
+// sums are added in order, so the result does not vary.
+__global__ __launch_bounds__(kBiasSlices *kWave) void k_bias_grad(const BiasGradArgs a)
+{
+    __shared__ float part[kBiasSlices][kWave * 8 + 8];
+    const int e = blockIdx.x, c = blockIdx.y * kWave * 8 + threadIdx.x * 8;
+    const int r0 = clamp_row(a.expert_off, e, a.rows), r1 = clamp_row(a.expert_off, e + 1, a.rows);
+    const bool gated = act_gated(a.act);
+    const int gcols = gated ? a.cols / 2 : a.cols;
+    const bool up = gated && c >= gcols;  // out_features is a multiple of 16: never both in 8
+    const int gc = up ? c - gcols : c;
+    float s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (c < a.cols) {
+#pragma unroll 4
+        for (int r = r0 + (int)threadIdx.y; r < r1; r += kBiasSlices) {
+            const bf16x8 g =
+                *reinterpret_cast<const bf16x8 *>(a.grad_out + (size_t)r * gcols + gc);
+            if (a.act == kActNone) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    s[i] += (float)g[i];
+                continue;
+            }
+            const uint16_t *z = a.preact + (size_t)r * a.cols + gc;
+            const bf16x8 z0 = *reinterpret_cast<const bf16x8 *>(z);
+            bf16x8 z1 = z0;
+            if (gated && !up)
+                z1 = *reinterpret_cast<const bf16x8 *>(z + gcols);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float d = (float)g[i], x = (float)z0[i];
+                s[i] += up ? d * act_one(a.act, x)
+                           : d * act_one_grad(a.act, x) * (gated ? (float)z1[i] : 1.0f);
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        part[threadIdx.y][threadIdx.x * 8 + i] = s[i];
+    __syncthreads();
+    const int col = threadIdx.y * kWave + threadIdx.x;
+    if (blockIdx.y * kWave * 8 + col >= a.cols)
+        return;
+    float sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kBiasSlices; ++w)
+        sum += part[w][col];
+    a.grad_bias[(size_t)e * a.cols + blockIdx.y * kWave * 8 + col] = sum;
+}
+
+}  // namespace epdc_layer

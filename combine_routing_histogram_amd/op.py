@@ -18,6 +18,7 @@ from typing import Optional, Tuple
 import torch
 
 from . import binding as B
+from . import layer as L
 
 QUANT = {"none": B.EPDC_QUANT_NONE, "fp8_e4m3_b128": B.EPDC_QUANT_FP8_E4M3_B128,
          "mxfp4_b32": B.EPDC_QUANT_MXFP4_B32}
@@ -64,6 +65,26 @@ class EpDispatchCombineConfig:
                              self.scale_row_bytes)
 
 
+GATE_SCORES = {"softmax": L.EPDC_GATE_SOFTMAX, "sigmoid": L.EPDC_GATE_SIGMOID}
+ACTIVATIONS = {"none": L.EPDC_ACT_NONE, "relu": L.EPDC_ACT_RELU, "gelu": L.EPDC_ACT_GELU,
+               "silu": L.EPDC_ACT_SILU, "swiglu": L.EPDC_ACT_SWIGLU, "geglu": L.EPDC_ACT_GEGLU}
+GATED = ("swiglu", "geglu")
+
+
+@dataclasses.dataclass(frozen=True)
+class GateConfig:
+    """How a gate turns logits into routing weights (epdc_gate)."""
+    score: str = "softmax"         # "softmax" or "sigmoid"
+    renormalize: bool = True       # divide by the sum of the chosen scores
+    scale: float = 1.0             # multiplies the weights
+
+    def __post_init__(self):
+        if self.score not in GATE_SCORES:
+            raise ValueError(f"score must be one of {sorted(GATE_SCORES)}")
+        if not 0.0 < self.scale < float("inf"):
+            raise ValueError("scale must be positive and finite")
+
+
 def _ptr(t: Optional[torch.Tensor]) -> int:
     return 0 if t is None else t.data_ptr()
 
@@ -108,8 +129,8 @@ class EpDispatchCombineOp:
         self._scales_dtype = None
         self._dev_index = self.device.index if self.device.index is not None else \
             torch.cuda.current_device()
-        L = B.lib()
-        self._f_dispatch, self._f_combine = L.epdc_dispatch, L.epdc_combine
+        lib = B.lib()
+        self._f_dispatch, self._f_combine = lib.epdc_dispatch, lib.epdc_combine
         self._views = {}
         self._payload_v = self._payload_view(self._out)
         self._combined_cut = (-1, None)   # (T, (output view, weights view))
@@ -120,6 +141,8 @@ class EpDispatchCombineOp:
         self._last_dedup = False
         self._staging = None
         self._units = None          # unit-row buffers, allocated on first use
+        self._gate = None           # the gate's buffers, allocated on first use
+        self._gate_cut = (-1, None)
         self._unit_carried = (False, False)
 
     def __del__(self):
@@ -510,6 +533,256 @@ class EpDispatchCombineOp:
                              _ptr(self._combined), _ptr(self._combined_weights))
         T = self._tokens
         return self._combined[:T], self._combined_weights[:T]
+
+    # ---- the gate ------------------------------------------------------------------------
+    def _gate_buffers(self) -> dict:
+        if self._gate is None:
+            cfg, dev = self.config, self.device
+            with torch.cuda.device(dev):
+                self._gate = {
+                    "weights": torch.empty((cfg.max_tokens, cfg.topk), dtype=torch.float32,
+                                           device=dev),
+                    "indices": torch.empty((cfg.max_tokens, cfg.topk), dtype=torch.int32,
+                                           device=dev),
+                    "counts": torch.empty(cfg.num_experts + 1, dtype=torch.int32, device=dev),
+                    "losses": torch.empty(2, dtype=torch.float32, device=dev),
+                    "scratch": torch.zeros(L.epdc_gate_scratch_bytes(cfg.max_tokens,
+                                                                     cfg.num_experts),
+                                           dtype=torch.uint8, device=dev),
+                }
+        return self._gate
+
+    def _gate_args(self, logits, gate, bias, mask) -> L.epdc_gate_args:
+        cfg = self.config
+        if logits.dim() != 2 or logits.shape[1] != cfg.num_experts:
+            raise ValueError(f"logits must be [tokens, {cfg.num_experts}], got "
+                             f"{tuple(logits.shape)}")
+        T = logits.shape[0]
+        if T > cfg.max_tokens:
+            raise ValueError(f"logits have {T} tokens, the op holds {cfg.max_tokens}")
+        self._need(logits, "logits")
+        if logits.dtype not in (torch.float32, torch.bfloat16):
+            raise ValueError(f"logits must be float32 or bfloat16, got {logits.dtype}")
+        if bias is not None:
+            self._need(bias, "bias", torch.float32, (cfg.num_experts,))
+        if mask is not None:
+            if mask.dtype not in (torch.uint8, torch.bool):
+                raise ValueError(f"mask must be uint8 or bool, got {mask.dtype}")
+            self._need(mask, "mask", None, (T,))
+        return L.make_gate_args(T, cfg.num_experts, cfg.topk, GATE_SCORES[gate.score],
+                                int(gate.renormalize),
+                                L.EPDC_DT_FP32 if logits.dtype == torch.float32
+                                else L.EPDC_DT_BF16,
+                                gate.scale, logits.data_ptr(), _ptr(bias), _ptr(mask))
+
+    def gate(self, logits: torch.Tensor, gate: GateConfig = GateConfig(), *,
+             bias: Optional[torch.Tensor] = None, mask: Optional[torch.Tensor] = None,
+             balance: bool = False):
+        """Choose each token's experts from the router's logits.
+
+        logits: fp32 or bf16 [T, E], T <= max_tokens; bias: fp32 [E] added to the
+        scores for the choice only; mask: uint8 or bool [T], 0 = padding.
+        Returns (weights fp32 [T, K], indices int32 [T, K]) as dispatch takes
+        them, and with balance also (counts int32 [E + 1], losses fp32 [2]):
+        choices per expert followed by the number of tokens that took part, and
+        the balance and z losses (epdc_layer.h gives the formulas).  All are
+        views of buffers of the op that the next gate() overwrites."""
+        args = self._gate_args(logits, gate, bias, mask)
+        T = args.num_tokens
+        g = self._gate_buffers()
+        if self._gate_cut[0] != T:
+            self._gate_cut = (T, (g["weights"][:T], g["indices"][:T]))
+        views = self._gate_cut[1]
+        if not balance:
+            L.epdc_gate(args, self._stream(), _ptr(g["weights"]), _ptr(g["indices"]))
+            return views
+        L.epdc_gate(args, self._stream(), _ptr(g["weights"]), _ptr(g["indices"]),
+                    _ptr(g["counts"]), _ptr(g["losses"]), _ptr(g["scratch"]))
+        return views + (g["counts"], g["losses"])
+
+    def gate_backward(self, logits: torch.Tensor, indices: torch.Tensor,
+                      gate: GateConfig = GateConfig(), *,
+                      grad_weights: Optional[torch.Tensor] = None,
+                      mask: Optional[torch.Tensor] = None,
+                      counts: Optional[torch.Tensor] = None,
+                      grad_losses: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """Gradient of gate() with respect to the logits, in their dtype.
+
+        indices, counts: the forward's; grad_weights: fp32 [T, K] or None;
+        grad_losses: fp32 [2], with counts, or None."""
+        args = self._gate_args(logits, gate, None, mask)
+        T, cfg = args.num_tokens, self.config
+        self._need(indices, "indices", torch.int32, (T, cfg.topk))
+        if grad_weights is not None:
+            self._need(grad_weights, "grad_weights", torch.float32, (T, cfg.topk))
+        if (counts is None) != (grad_losses is None):
+            raise ValueError("counts and grad_losses go together")
+        if counts is not None:
+            self._need(counts, "counts", torch.int32, (cfg.num_experts + 1,))
+            self._need(grad_losses, "grad_losses", torch.float32, (2,))
+        grad = torch.empty_like(logits)
+        L.epdc_gate_backward(args, self._stream(), _ptr(indices), _ptr(grad_weights),
+                             _ptr(counts), _ptr(grad_losses), _ptr(grad))
+        return grad
+
+    # ---- the experts' products -------------------------------------------------------------
+    def _routed(self) -> int:
+        """Rows the last dispatch may have written; raises if there is none."""
+        if self._tokens == 0:
+            B.epdc_get_offsets(self._op)   # BAD_STATE without a recorded dispatch
+        return self._tokens * self.config.topk
+
+    def _product_args(self, rows, input, weight, scales, weight_scales, bias, activation,
+                      first_expert) -> L.epdc_product_args:
+        cfg = self.config
+        if activation not in ACTIVATIONS:
+            raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}")
+        self._need(weight, "weight")
+        if weight.dim() != 3:
+            raise ValueError("weight must be [experts, out_features, in_features]")
+        n, out_f, in_f = weight.shape
+        if n < 1 or first_expert < 0 or first_expert + n > cfg.num_experts:
+            raise ValueError(f"experts [{first_expert}, {first_expert + n}) are not within "
+                             f"[0, {cfg.num_experts})")
+        if weight.dtype == torch.bfloat16:
+            dtype = L.EPDC_DT_BF16
+        elif weight.dtype == torch.float8_e4m3fn:
+            dtype = L.EPDC_DT_E4M3
+        else:
+            raise ValueError(f"weight must be bfloat16 or float8_e4m3fn, got {weight.dtype}")
+        self._need(input, "input", weight.dtype)
+        if input.dim() != 2 or input.shape[1] != in_f or input.shape[0] < rows:
+            raise ValueError(f"input must be [>= {rows}, {in_f}], got {tuple(input.shape)}")
+        if dtype == L.EPDC_DT_E4M3:
+            if scales is None or weight_scales is None:
+                raise ValueError("e4m3 operands need scales and weight_scales")
+            blocks = in_f // 128
+            self._need(scales, "scales", torch.float32)
+            if scales.dim() != 2 or scales.shape[0] < rows or scales.shape[1] != blocks:
+                raise ValueError(f"scales must be [>= {rows}, {blocks}], got "
+                                 f"{tuple(scales.shape)}")
+            self._need(weight_scales, "weight_scales", torch.float32,
+                       (n, (out_f + 127) // 128, blocks))
+        elif scales is not None or weight_scales is not None:
+            raise ValueError("scales and weight_scales belong to e4m3 operands")
+        if bias is not None:
+            self._need(bias, "bias", torch.float32, (n, out_f))
+        off, _ = B.epdc_get_offsets(self._op)
+        return L.make_product_args(rows, n, in_f, out_f, dtype, ACTIVATIONS[activation],
+                                   input.data_ptr(), _ptr(scales), weight.data_ptr(),
+                                   _ptr(weight_scales), _ptr(bias), off + 4 * first_expert)
+
+    def _need_rows(self, t, name, rows, cols) -> None:
+        self._need(t, name, torch.bfloat16)
+        if t.dim() != 2 or t.shape[0] < rows or t.shape[1] != cols:
+            raise ValueError(f"{name} must be [>= {rows}, {cols}], got {tuple(t.shape)}")
+
+    def expert_product(self, input: torch.Tensor, weight: torch.Tensor, *,
+                       scales: Optional[torch.Tensor] = None,
+                       weight_scales: Optional[torch.Tensor] = None,
+                       bias: Optional[torch.Tensor] = None, activation: str = "none",
+                       residual: Optional[torch.Tensor] = None, first_expert: int = 0,
+                       out: Optional[torch.Tensor] = None,
+                       preact: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """The experts' matrix product over the rows of the last dispatch:
+        out[s] = act(input[s] @ weight[e].T + bias[e]) + residual[s] for every
+        row s of expert first_expert + e.
+
+        input: bf16 [>= T*K, in], or float8_e4m3fn with scales fp32 [>= T*K,
+        in/128], as dispatch gives them; weight: [n, out, in] in the same type,
+        e4m3 with weight_scales fp32 [n, ceil(out/128), in/128]; bias: fp32
+        [n, out].  activation: "none", "relu", "gelu", "silu", or "swiglu" /
+        "geglu", whose weight holds out/2 gate rows and then out/2 up rows.
+        residual: bf16 rows of the result.  preact: bf16 [>= T*K, out], filled
+        with the value before the activation for expert_product_backward.
+
+        Returns out, bf16 [>= T*K, out or out/2] (allocated with T*K rows if
+        None).  Only the rows of these experts are written."""
+        rows = self._routed()
+        args = self._product_args(rows, input, weight, scales, weight_scales, bias, activation,
+                                  first_expert)
+        cols = args.out_features // 2 if activation in GATED else args.out_features
+        if residual is not None:
+            self._need_rows(residual, "residual", rows, cols)
+        if preact is not None:
+            self._need_rows(preact, "preact", rows, args.out_features)
+        if out is None:
+            out = torch.empty((rows, cols), dtype=torch.bfloat16, device=self.device)
+        else:
+            self._need_rows(out, "out", rows, cols)
+        L.epdc_expert_product(args, self._stream(), _ptr(residual), out.data_ptr(), _ptr(preact))
+        return out
+
+    def expert_product_backward(self, grad_output: torch.Tensor, input: torch.Tensor,
+                                weight: torch.Tensor, *, activation: str = "none",
+                                preact: Optional[torch.Tensor] = None, bias: bool = False,
+                                first_expert: int = 0, need_input: bool = True,
+                                need_weight: bool = True,
+                                weight_dtype: torch.dtype = torch.bfloat16):
+        """Gradients of a bf16 expert_product.
+
+        grad_output: bf16 rows like its result; preact: what the forward filled
+        (with an activation).  Returns (grad_input bf16 [T*K, in], grad_weight
+        [n, out, in] in weight_dtype (bfloat16 or float32), grad_bias fp32 [n,
+        out]); None for what is not asked for.  Experts without rows get zero
+        weight and bias gradients.  The residual's gradient is grad_output."""
+        rows = self._routed()
+        if weight.dtype != torch.bfloat16:
+            raise ValueError("the gradients take bf16 operands")
+        if weight_dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError("weight_dtype must be bfloat16 or float32")
+        args = self._product_args(rows, input, weight, None, None, None, activation, first_expert)
+        n, out_f, in_f = weight.shape
+        self._need_rows(grad_output, "grad_output", rows,
+                        out_f // 2 if activation in GATED else out_f)
+        dz = None
+        if activation == "none":
+            preact = None
+        else:
+            if preact is None:
+                raise ValueError("an activation's gradient needs preact")
+            self._need_rows(preact, "preact", rows, out_f)
+            if need_input or need_weight:
+                dz = torch.empty((rows, out_f), dtype=torch.bfloat16, device=self.device)
+        new = lambda shape, dtype: torch.empty(shape, dtype=dtype, device=self.device)
+        grad_input = new((rows, in_f), torch.bfloat16) if need_input else None
+        grad_weight = new((n, out_f, in_f), weight_dtype) if need_weight else None
+        grad_bias = new((n, out_f), torch.float32) if bias else None
+        L.epdc_expert_backward(args, self._stream(), grad_output.data_ptr(), _ptr(preact),
+                               _ptr(dz), _ptr(grad_input), _ptr(grad_weight),
+                               L.EPDC_DT_FP32 if weight_dtype == torch.float32
+                               else L.EPDC_DT_BF16, _ptr(grad_bias))
+        return grad_input, grad_weight, grad_bias
+
+    # ---- gradients of combine and dispatch ---------------------------------------------------
+    def combine_backward(self, grad_output: torch.Tensor, input: torch.Tensor,
+                         weights: Optional[torch.Tensor] = None):
+        """Gradients of combine(input, weights) under the routing of the last
+        dispatch: (grad_input bf16 [T*K, H] in the received layout, grad_weights
+        fp32 [T, K] in token order, the gradient of dispatch's weights).  Only
+        rows that hold a pair are written; a pair without a slot gets 0."""
+        self._routed()
+        self._check_combine(input, weights)
+        cfg, T = self.config, self._tokens
+        self._need(grad_output, "grad_output", torch.bfloat16, (T, cfg.hidden))
+        _, _, slot_of = B.epdc_get_routing(self._op)
+        grad_input = torch.empty((T * cfg.topk, cfg.hidden), dtype=torch.bfloat16,
+                                 device=self.device)
+        grad_weights = torch.empty((T, cfg.topk), dtype=torch.float32, device=self.device)
+        L.epdc_combine_backward(self._stream(), T, cfg.topk, cfg.hidden, slot_of,
+                                grad_output.data_ptr(), input.data_ptr(), _ptr(weights),
+                                grad_input.data_ptr(), grad_weights.data_ptr())
+        return grad_input, grad_weights
+
+    def dispatch_backward(self, grad_output: torch.Tensor) -> torch.Tensor:
+        """Gradient of dispatch's bf16 input: bf16 [T, H], the fp32 sum of each
+        token's rows of grad_output (bf16 [>= T*K, H], received layout)."""
+        self._routed()
+        self._check_combine(grad_output, None)
+        grad = torch.empty((self._tokens, self.config.hidden), dtype=torch.bfloat16,
+                           device=self.device)
+        B.epdc_combine(self._op, self._stream(), grad_output.data_ptr(), 0, 0, grad.data_ptr(), 0)
+        return grad
 
     def reset(self) -> None:
         B.epdc_reset(self._op)

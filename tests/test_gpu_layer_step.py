@@ -1,0 +1,159 @@
+"""The layer operators together, as a model's layer uses them: gate, dispatch,
+the two experts' products, combine, and every gradient back to the logits, the
+tokens and the weights, against the layer written in 64 bits with autograd.
+Also under graph capture, on another stream, and with two ops interleaved.
+
+Bounds.  Values cross from operator to operator rounded to bf16 (2^-8 each).
+The chain from tokens to output has five such roundings (pre-activation is not
+one: the forward activates unrounded), and the gradients at most nine; errors
+add like the root of their number in the norm, so the relative error in the
+norm stays below 9 * 2^-8 even if every rounding were at its worst and
+aligned.  The losses and weights see only fp32.
+"""
+import numpy as np
+import pytest
+import torch
+
+from combine_routing_histogram_amd.op import (EpDispatchCombineConfig, EpDispatchCombineOp,
+                                              GateConfig)
+from layer_common import DEV, normal
+
+pytestmark = pytest.mark.gpu
+CFG = GateConfig("softmax", True, 1.0)
+
+
+class Layer:
+    """What a program keeps: the op, the weights and their gradients' inputs."""
+
+    def __init__(self, T, H, I, E, K, ranks=2, seed=0):
+        rng = np.random.default_rng(seed)
+        self.shape = (T, H, I, E, K)
+        self.op = EpDispatchCombineOp(EpDispatchCombineConfig(T, H, K, E, ranks), DEV)
+        self.w1 = normal(rng, (E, 2 * I, H), H ** -0.5)
+        self.w2 = normal(rng, (E, H, I), I ** -0.5)
+        self.b2 = normal(rng, (E, H), 0.1, torch.float32)
+        self.x = normal(rng, (T, H))
+        self.logits = normal(rng, (T, E), 1.5, torch.float32)
+        self.dy = normal(rng, (T, H))
+        self.gl = torch.tensor([0.02, 0.005], device=DEV)
+
+    def step(self, x, logits):
+        op = self.op
+        weights, indices, counts, losses = op.gate(logits, CFG, balance=True)
+        rows, row_w, _, _, _ = op.dispatch(x, weights, None, indices)
+        n = indices.numel()
+        z = torch.empty(n, self.w1.shape[1], dtype=torch.bfloat16, device=DEV)
+        h = op.expert_product(rows, self.w1, activation="swiglu", preact=z)
+        o = op.expert_product(h, self.w2, bias=self.b2)
+        y, _ = op.combine(o, row_w)
+        do, gw = op.combine_backward(self.dy, o, row_w)
+        dh, dw2, db2 = op.expert_product_backward(do, h, self.w2, bias=True)
+        drows, dw1, _ = op.expert_product_backward(dh, rows, self.w1, activation="swiglu",
+                                                   preact=z)
+        dx = op.dispatch_backward(drows)
+        dl = op.gate_backward(logits, indices, CFG, grad_weights=gw, counts=counts,
+                              grad_losses=self.gl)
+        return y, losses, dx, dl, dw1, dw2, db2, indices, counts
+
+    def exact(self):
+        T, H, I, E, K = self.shape
+        leaf = lambda t: t.double().requires_grad_(True)
+        x, l, w1, w2, b2 = map(leaf, (self.x, self.logits, self.w1, self.w2, self.b2))
+        p = torch.softmax(l, 1)
+        idx = torch.sort(l.detach(), dim=1, descending=True, stable=True).indices[:, :K]
+        w = torch.gather(p, 1, idx)
+        w = w / w.sum(1, keepdim=True)
+        y = torch.zeros(T, H, dtype=torch.float64, device=DEV)
+        for e in range(E):
+            t, k = torch.nonzero(idx == e, as_tuple=True)
+            g, u = (x[t] @ w1[e].t()).chunk(2, dim=1)
+            y = y.index_add(0, t, w[t, k][:, None] *
+                            ((torch.nn.functional.silu(g) * u) @ w2[e].t() + b2[e]))
+        c = torch.bincount(idx.reshape(-1), minlength=E)
+        losses = torch.stack([E * (c / (T * K) * p.mean(0)).sum(),
+                              torch.logsumexp(l, 1).square().mean()])
+        total = (y * self.dy.double()).sum() + (losses * self.gl.double()).sum()
+        gx, gl, g1, g2, gb = torch.autograd.grad(total, (x, l, w1, w2, b2))
+        return y.detach(), losses.detach(), gx, gl, g1, g2, gb, idx, c
+
+
+def _near(got, ref, rel, what):
+    d = float((got.double() - ref).norm() / ref.norm())
+    assert d <= rel, f"{what}: {d}"
+
+
+@pytest.mark.parametrize("T,H,I,E,K", [(3, 64, 32, 8, 2), (48, 256, 136, 16, 4),
+                                       (640, 512, 264, 8, 2)])
+def test_layer_step_matches_64_bits(T, H, I, E, K):
+    layer = Layer(T, H, I, E, K)
+    got, ref = layer.step(layer.x, layer.logits), layer.exact()
+    assert torch.equal(got[7].long(), ref[7])
+    assert torch.equal(got[8][:E].long(), ref[8]) and int(got[8][E]) == T
+    _near(got[0], ref[0], 5 * 2.0 ** -8, "output")
+    _near(got[1], ref[1], 1e-5, "losses")
+    for i, name in ((2, "tokens"), (3, "logits"), (4, "gate/up"), (5, "down"), (6, "bias")):
+        _near(got[i], ref[i], 9 * 2.0 ** -8, name)
+    assert layer.op.device_error() == 0
+
+
+def test_layer_step_on_another_stream_and_two_layers():
+    """Two layers stepped in turn on a side stream give what each gives alone."""
+    a, b = Layer(40, 128, 64, 8, 2, seed=1), Layer(100, 128, 72, 8, 4, seed=2)
+    want = [[t.clone() for t in m.step(m.x, m.logits)] for m in (a, b)]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        got = [m.step(m.x, m.logits) for m in (a, b, a, b)][2:]
+    side.synchronize()
+    for g, w in zip(got, want):
+        for p, q in zip(g, w):
+            assert torch.equal(p, q)
+
+
+def test_layer_step_captured():
+    """The whole step in one graph, replayed on new inputs with eager steps and
+    synchronizations between: every replay equals the eager result."""
+    layer = Layer(48, 256, 136, 16, 4, seed=3)
+    x, logits = layer.x.clone(), layer.logits.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        layer.step(x, logits)
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        outs = layer.step(x, logits)
+    for k in range(4):
+        rng = np.random.default_rng(100 + k)
+        nx, nl = normal(rng, tuple(x.shape)), normal(rng, tuple(logits.shape), 1.5, torch.float32)
+        want = [t.clone() for t in layer.step(nx, nl)]
+        torch.cuda.synchronize()
+        x.copy_(nx)
+        logits.copy_(nl)
+        g.replay()
+        torch.cuda.synchronize()
+        for i, (p, q) in enumerate(zip(outs, want)):
+            assert torch.equal(p, q), (k, i)
+
+
+def test_padded_batch():
+    """Padding tokens: masked in the gate, they get no rows, output 0 and zero
+    gradients; dispatch reports their ids as outside the range."""
+    T, H, I, E, K = 32, 64, 32, 8, 2
+    layer = Layer(T, H, I, E, K, seed=5)
+    op = layer.op
+    mask = torch.ones(T, dtype=torch.bool, device=DEV)
+    mask[20:] = False
+    w, idx, counts, losses = op.gate(layer.logits, CFG, mask=mask, balance=True)
+    assert bool((idx[20:] == -1).all()) and int(counts[E]) == 20
+    rows, row_w, _, _, recv = op.dispatch(layer.x, w, None, idx)
+    assert int(recv.sum()) == 20 * K
+    o = op.expert_product(op.expert_product(rows, layer.w1, activation="swiglu"), layer.w2)
+    y, _ = op.combine(o, row_w)
+    assert not y[20:].any() and bool(y[:20].any())
+    do, gw = op.combine_backward(layer.dy, o, row_w)
+    assert not gw[20:].any()
+    dl = op.gate_backward(layer.logits, idx, CFG, grad_weights=gw, mask=mask, counts=counts,
+                          grad_losses=layer.gl)
+    assert not dl[20:].any() and bool(dl[:20].any())
+    assert op.device_error() == 1
