@@ -156,16 +156,18 @@ epdc_status check_product(const epdc_product_args *p)
     return EPDC_SUCCESS;
 }
 
-// Row tiles that the experts' row counts can make at most, known to the device only.
+// Row tiles that `experts` experts with at most `rows` rows between them can
+// make; their counts are known to the device only.
 int64_t row_tile_bound(int64_t rows, int experts, int bm)
 {
     const int64_t with_rows = rows < experts ? rows : experts;
     return (rows + with_rows * (bm - 1)) / bm;
 }
 
+// Blocks for `tiles` tiles: whole rounds of one run per XCD (tile_number).
 epdc_status grid_of(int64_t tiles, int *grid)
 {
-    const int64_t g = (tiles + kXcds - 1) / kXcds * kXcds;
+    const int64_t round = kXcds * kRun, g = (tiles + round - 1) / round * round;
     if (g > 0x7fffffff)
         return fail(EPDC_ERR_INVALID_ARGS, "more tiles than a launch can hold");
     *grid = (int)g;

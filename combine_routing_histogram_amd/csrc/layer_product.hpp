@@ -109,16 +109,38 @@ __host__ __device__ inline bool act_gated(int act) { return act >= kActSwiglu; }
 // Which tile a block computes
 // ---------------------------------------------------------------------------
 //
-// Tiles are numbered expert by expert, inside an expert rows fastest, so that
-// neighbours share the weight tile (same columns) or the row tile.  Blocks go
-// to the 8 XCDs in turn; block b takes tile (b % 8) * ceil(total/8) + b/8, so
-// that each XCD works on one contiguous run of tiles and its L2 serves the
-// neighbours.  The counts per expert are on the device only: every block scans
-// the offsets (at most 513 ints, in L2), and blocks past the total end.
+// Tiles are numbered expert by expert, inside an expert by bands of up to 8 row
+// tiles, inside a band column by column.  Blocks go to the XCDs in turn (block b
+// is number b / 8 of XCD b % 8); each XCD takes runs of 32 consecutive tiles,
+// about a patch of 8 x 4, which its 32 CUs read through one L2 (12 operand
+// tiles instead of 64), and the 8 XCDs take neighbouring runs, mostly of one
+// expert, so that what one has read the others find in the last-level cache.
+// (One expert per XCD instead read 4.1 GB from HBM for 0.94 GB of operands:
+// 32768 x 7168 x 4096 over 8 experts 1944 us, now 1766.)  The counts per expert
+// are on the device only: every block scans the offsets (at most 513 ints, in
+// L2), and blocks past the total end.
 
 struct Tile {
     int expert, row0, rows, row_tile, col_tile;
 };
+
+constexpr int kBandRows = 8, kRun = 32;
+
+__device__ inline int tile_number()
+{
+    const int slot = blockIdx.x / kXcds;
+    return (slot / kRun * kXcds + (int)(blockIdx.x % kXcds)) * kRun + slot % kRun;
+}
+
+// Tile `local` of an expert of mt x nt tiles.
+__device__ inline void place(int local, int mt, int nt, Tile &t)
+{
+    const int band = local / (kBandRows * nt), in = local - band * (kBandRows * nt);
+    const int first = band * kBandRows;
+    const int rows = mt - first < kBandRows ? mt - first : kBandRows;
+    t.col_tile = in / rows;
+    t.row_tile = first + in - t.col_tile * rows;
+}
 
 __device__ inline int clamp_row(const int32_t *off, int i, int rows)
 {
@@ -163,16 +185,14 @@ __device__ inline bool find_tile(const ProductArgs &a, int bm, int *lds, Tile &t
         before += w < wave ? v : 0;
         total += v;
     }
-    const int per_xcd = (total + kXcds - 1) / kXcds;
-    const int slot = blockIdx.x / kXcds;
-    const int id = (int)(blockIdx.x % kXcds) * per_xcd + slot;
-    if (slot >= per_xcd || id >= total)
+    const int id = tile_number();
+    if (id >= total)
         return false;
     int first = before + incl - cnt;
     if (id >= first && id < first + cnt) {
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
-            const int mt = (n[i] + bm - 1) / bm, c = mt * a.col_tiles;
+            const int c = (n[i] + bm - 1) / bm * a.col_tiles;
             if (id >= first && id < first + c) {
                 lds[kWaves] = tid * kEach + i;
                 lds[kWaves + 1] = id - first;
@@ -186,9 +206,7 @@ __device__ inline bool find_tile(const ProductArgs &a, int bm, int *lds, Tile &t
     t.expert = uniform(lds[kWaves]);
     const int local = uniform(lds[kWaves + 1]);
     const int start = uniform(lds[kWaves + 2]), have = uniform(lds[kWaves + 3]);
-    const int mt = (have + bm - 1) / bm;
-    t.col_tile = local / mt;
-    t.row_tile = local - t.col_tile * mt;
+    place(local, (have + bm - 1) / bm, a.col_tiles, t);
     t.row0 = start + t.row_tile * bm;
     const int left = have - t.row_tile * bm;
     t.rows = left < bm ? left : bm;
@@ -245,12 +263,13 @@ struct StraightTile {
                      (uint32_t)chunk * 16;
     }
     // step: which 128 bytes of the rows; left: contraction bytes from there on
+    template <int kCount = kLoads>
     __device__ inline void load(uint8_t *lds, int step, int left, int wave)
     {
         const __amdgpu_buffer_rsrc_t rs = buffer_at(base + (size_t)step * kStepBytes, kOpen);
         const bool out = chunk * 16 >= left;
 #pragma unroll
-        for (int d = 0; d < kLoads; ++d)
+        for (int d = 0; d < kCount; ++d)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
                 rs, (lds_byte *)(lds + (d * kWaves + wave) * 1024), 16, out ? kNowhere : off[d], 0,
                 0, 0);
@@ -298,8 +317,10 @@ struct CrossTile {
     }
     // left: contraction rows from this step on; later rows read as zeros, and
     // so does whatever a ragged column tile takes behind the last of them
+    template <int kCount = kLoads>
     __device__ inline void load(uint8_t *lds, int step, int left, int wave)
     {
+        static_assert(kCount == kLoads, "all columns of the tile");
         const uint32_t rows = left < 64 ? left : 64;
         const __amdgpu_buffer_rsrc_t rs =
             buffer_at(base + (size_t)step * 64 * row_bytes, rows * (uint32_t)row_bytes);
@@ -355,6 +376,19 @@ __device__ inline i32x8 join(i32x4 a, i32x4 b)
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
+template <int kN>
+struct Count {
+    static constexpr int value = kN;
+};
+
+// Every direct load and LDS read of this wave is done, and so are the other
+// waves' at the same point.  Unlike __syncthreads this is also a point no LDS
+// access may be moved across by the compiler.
+__device__ inline void wait_and_meet()
+{
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
 // Four consecutive output columns of one row: bias, activation and residual in
 // fp32, one rounding.  z: the product; up: its second half (gated).
 __device__ inline void finish_forward(const ProductArgs &a, int expert, int row, int col,
@@ -402,6 +436,8 @@ __global__ __launch_bounds__(kWavesM *kWavesN *kWave) void k_product_tile(const 
     constexpr int kWaves = kWavesM * kWavesN;
     constexpr int kMI = kBM / kWavesM / 16, kNJ = kBN / kWavesN / 16;
     static_assert(kProduct != kForward || kBN / kWavesN == 64, "gated columns pair inside 64");
+    constexpr int kStep = kE4m3 ? 128 : 64;  // contraction elements per step
+    constexpr int kElem = kE4m3 ? 1 : 2;
     typedef typename PickTile<kProduct == kGradWeight, kBM, kWaves>::type PTile;
     typedef typename PickTile<kProduct != kForward, kBN, kWaves>::type QTile;
     constexpr int kStage = PTile::kBytes + QTile::kBytes;
@@ -413,15 +449,11 @@ __global__ __launch_bounds__(kWavesM *kWavesN *kWave) void k_product_tile(const 
     Tile t;
     int contract = a.contract;  // elements
     if (kProduct == kGradWeight) {
-        const int per = a.row_tiles * a.col_tiles, total = per * a.experts;
-        const int per_xcd = (total + kXcds - 1) / kXcds, slot = blockIdx.x / kXcds;
-        const int id = (int)(blockIdx.x % kXcds) * per_xcd + slot;
-        if (slot >= per_xcd || id >= total)
-            return;
+        const int per = a.row_tiles * a.col_tiles, id = tile_number();
         t.expert = id / per;
-        const int local = id - t.expert * per;
-        t.col_tile = local / a.row_tiles;
-        t.row_tile = local - t.col_tile * a.row_tiles;
+        if (t.expert >= a.experts)
+            return;
+        place(id - t.expert * per, a.row_tiles, a.col_tiles, t);
         t.row0 = uniform(clamp_row(a.expert_off, t.expert, a.rows));
         contract = uniform(clamp_row(a.expert_off, t.expert + 1, a.rows)) - t.row0;
         contract = contract < 0 ? 0 : contract;
@@ -464,95 +496,134 @@ __global__ __launch_bounds__(kWavesM *kWavesN *kWave) void k_product_tile(const 
         for (int j = 0; j < kNJ; ++j)
             acc[i][j] = f32x4{0, 0, 0, 0};
 
-    constexpr int kStep = kE4m3 ? 128 : 64;  // contraction elements per step
-    constexpr int kElem = kE4m3 ? 1 : 2;
+    const int qrow = wn * (kNJ * 16);
     const int steps = (contract + kStep - 1) / kStep;
-    auto load = [&](int s, int buf) {
-        uint8_t *stage = lds + buf * kStage;
-        const int left = contract - s * kStep;
-        if constexpr (kProduct == kGradWeight)
-            pt.load(stage, s, left, wave);
-        else
-            pt.load(stage, s, left * kElem, wave);
-        if constexpr (kProduct == kForward)
-            qt.load(stage + PTile::kBytes, s, left * kElem, wave);
-        else
-            qt.load(stage + PTile::kBytes, s, left, wave);
-    };
-    if (steps > 0)
-        load(0, 0);
-
-    const int prow = wm * (kMI * 16), qrow = wn * (kNJ * 16);
-    // e4m3: the rows' scales and the columns' block scales, one step ahead
-    const float *sx[kMI], *sw[kNJ];
-    if constexpr (kE4m3) {
-        const int blocks = contract / 128;
-#pragma unroll
-        for (int i = 0; i < kMI; ++i) {
-            int r = prow + i * 16 + (lane & 15);
-            r = r < t.rows ? r : t.rows - 1;
-            sx[i] = a.scales + (size_t)(t.row0 + r) * blocks;
-        }
-#pragma unroll
-        for (int j = 0; j < kNJ; ++j) {
-            const int r = qrow + j * 16 + (lane >> 4) * 4;
-            int c = gated ? gated_row(r, col0, a.weight_rows / 2) : col0 + r;
-            c = c < a.weight_rows ? c : a.weight_rows - 1;
-            sw[j] = a.weight_scales +
-                    ((size_t)t.expert * ((a.weight_rows + 127) / 128) + c / 128) * blocks;
-        }
-    }
-
-    for (int s = 0; s < steps; ++s) {
-        __syncthreads();  // step s has landed, and every wave is done with step s - 1
-        if (s + 1 < steps)
-            load(s + 1, (s + 1) & 1);
-        const uint8_t *ps = lds + (s & 1) * kStage, *qs = ps + PTile::kBytes;
+    // Row blocks of 16 go to the kWavesM waves of a SIMD in turn, so a ragged tile
+    // of g 64-row groups costs each of them g / kGroups of the work.
+    auto sweep = [&](auto groups) {
+        constexpr int kA = decltype(groups)::value;          // 64-row groups with rows
+        constexpr int kI = kA * 4 / kWavesM;                 // row blocks of this wave
+        constexpr int kPLoads = kProduct == kGradWeight ? PTile::kLoads : kA * 8 / kWaves;
+        auto load = [&](int s) {
+            uint8_t *stage = lds + (s & 1) * kStage;
+            const int left = contract - s * kStep;
+            pt.template load<kPLoads>(stage, s, kProduct == kGradWeight ? left : left * kElem,
+                                      wave);
+            qt.load(stage + PTile::kBytes, s, kProduct == kForward ? left * kElem : left, wave);
+        };
         if constexpr (kE4m3) {
-            i32x8 q[kNJ];
-            float fw[kNJ];
+            if (steps > 0)
+                load(0);
+            // the rows' scales and the columns' block scales
+            const float *sx[kI], *sw[kNJ];
+            const int blocks = contract / 128;
 #pragma unroll
-            for (int j = 0; j < kNJ; ++j) {
-                q[j] = join(QTile::frag(qs, qrow + j * 16, 0, lane),
-                            QTile::frag(qs, qrow + j * 16, 1, lane));
-                fw[j] = sw[j][s];
+            for (int i = 0; i < kI; ++i) {
+                int r = (i * kWavesM + wm) * 16 + (lane & 15);
+                r = r < t.rows ? r : t.rows - 1;
+                sx[i] = a.scales + (size_t)(t.row0 + r) * blocks;
             }
 #pragma unroll
-            for (int i = 0; i < kMI; ++i) {
-                const i32x8 p = join(PTile::frag(ps, prow + i * 16, 0, lane),
-                                     PTile::frag(ps, prow + i * 16, 1, lane));
-                const float fx = sx[i][s];
+            for (int j = 0; j < kNJ; ++j) {
+                const int r = qrow + j * 16 + (lane >> 4) * 4;
+                int c = gated ? gated_row(r, col0, a.weight_rows / 2) : col0 + r;
+                c = c < a.weight_rows ? c : a.weight_rows - 1;
+                sw[j] = a.weight_scales +
+                        ((size_t)t.expert * ((a.weight_rows + 127) / 128) + c / 128) * blocks;
+            }
+            for (int s = 0; s < steps; ++s) {
+                __syncthreads();  // step s has landed, and every wave is done with step s - 1
+                if (s + 1 < steps)
+                    load(s + 1);
+                const uint8_t *ps = lds + (s & 1) * kStage, *qs = ps + PTile::kBytes;
+                i32x8 q[kNJ];
+                float fw[kNJ];
 #pragma unroll
                 for (int j = 0; j < kNJ; ++j) {
-                    const f32x4 d = mfma_e4m3(q[j], p, f32x4{0, 0, 0, 0});
-                    const float f = fx * fw[j];
+                    q[j] = join(QTile::frag(qs, qrow + j * 16, 0, lane),
+                                QTile::frag(qs, qrow + j * 16, 1, lane));
+                    fw[j] = sw[j][s];
+                }
 #pragma unroll
-                    for (int v = 0; v < 4; ++v)
-                        acc[i][j][v] = __builtin_fmaf(d[v], f, acc[i][j][v]);
+                for (int i = 0; i < kI; ++i) {
+                    const int row = (i * kWavesM + wm) * 16;
+                    const i32x8 p = join(PTile::frag(ps, row, 0, lane),
+                                         PTile::frag(ps, row, 1, lane));
+                    const float fx = sx[i][s];
+#pragma unroll
+                    for (int j = 0; j < kNJ; ++j) {
+                        const f32x4 d = mfma_e4m3(q[j], p, f32x4{0, 0, 0, 0});
+                        const float f = fx * fw[j];
+#pragma unroll
+                        for (int v = 0; v < 4; ++v)
+                            acc[i][j][v] = __builtin_fmaf(d[v], f, acc[i][j][v]);
+                    }
                 }
             }
         } else {
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                i32x4 q[kNJ];
+            // Fragments run half a step ahead of the matrix cores: while half 0 of
+            // step s is multiplied half 1 is read, and while half 1 is multiplied
+            // half 0 of step s + 1.  The one barrier of a step stands between: by
+            // then every wave has the rest of step s in registers, so its buffer
+            // takes step s + 2, whose loads have a whole step to land.
+            i32x4 p0[kI], q0[kNJ], p1[kI], q1[kNJ];
+            auto frags = [&](int s, int half, i32x4 (&p)[kI], i32x4 (&q)[kNJ]) {
+                const uint8_t *ps = lds + (s & 1) * kStage, *qs = ps + PTile::kBytes;
 #pragma unroll
                 for (int j = 0; j < kNJ; ++j)
                     q[j] = QTile::frag(qs, qrow + j * 16, half, lane);
 #pragma unroll
-                for (int i = 0; i < kMI; ++i) {
-                    const i32x4 p = PTile::frag(ps, prow + i * 16, half, lane);
+                for (int i = 0; i < kI; ++i)
+                    p[i] = PTile::frag(ps, (i * kWavesM + wm) * 16, half, lane);
+            };
+            auto multiply = [&](const i32x4 (&p)[kI], const i32x4 (&q)[kNJ]) {
+#pragma unroll
+                for (int i = 0; i < kI; ++i)
 #pragma unroll
                     for (int j = 0; j < kNJ; ++j)
-                        acc[i][j] = mfma_bf16(q[j], p, acc[i][j]);
-                }
+                        acc[i][j] = mfma_bf16(q[j], p[i], acc[i][j]);
+            };
+            if (steps > 0) {
+                load(0);
+                if (steps > 1)
+                    load(1);
+                // wait for step 0 alone would need the load count; once per tile
+                wait_and_meet();
+                frags(0, 0, p0, q0);
+            }
+            for (int s = 0; s < steps; ++s) {
+                frags(s, 1, p1, q1);
+                multiply(p0, q0);
+                wait_and_meet();
+                if (s + 2 < steps)
+                    load(s + 2);
+                frags(s + 1, 0, p0, q0);  // after the last step: read, never used
+                multiply(p1, q1);
             }
         }
+    };
+    if constexpr (kProduct == kGradWeight) {
+        sweep(Count<kBM / 64>());
+    } else {
+        const int groups = (t.rows + 63) / 64;
+        if constexpr (kBM >= 256) {
+            if (groups >= 4)
+                sweep(Count<4>());
+            else if (groups == 3)
+                sweep(Count<3>());
+        }
+        if constexpr (kBM >= 128) {
+            if (groups == 2)
+                sweep(Count<2>());
+        }
+        if (groups == 1)
+            sweep(Count<1>());
     }
 
     // lane: row l % 16 of each P block, columns 4 * (l / 16) ... +3 of each Q block
 #pragma unroll
     for (int i = 0; i < kMI; ++i) {
-        const int r = prow + i * 16 + (lane & 15);
+        const int r = (i * kWavesM + wm) * 16 + (lane & 15);
         if (r >= t.rows)
             continue;
         if constexpr (kProduct == kForward) {
