@@ -174,9 +174,12 @@ epdc_status grid_of(int64_t tiles, int *grid)
     return EPDC_SUCCESS;
 }
 
-template <int kProduct, bool kE4m3, int kBM, int kBN, int kWM, int kWN>
-epdc_status launch_tile(const char *name, hipStream_t st, ProductArgs &a, int cols_per_tile)
+template <int kProduct, bool kE4m3, int kGroups>
+epdc_status launch_tile(hipStream_t st, ProductArgs &a)
 {
+    constexpr int kBM = kGroups * 64;
+    const int cols_per_tile =
+        kProduct == kForward && act_gated(a.act) ? kTileCols / 2 : kTileCols;
     a.col_tiles = (a.out_cols + cols_per_tile - 1) / cols_per_tile;
     int64_t tiles;
     if (kProduct == kGradWeight) {
@@ -189,9 +192,8 @@ epdc_status launch_tile(const char *name, hipStream_t st, ProductArgs &a, int co
     const epdc_status s = grid_of(tiles, &grid);
     if (s != EPDC_SUCCESS)
         return s;
-    return launch(name, [&] {
-        k_product_tile<kProduct, kE4m3, kBM, kBN, kWM, kWN>
-            <<<grid, kWM * kWN * kWave, 0, st>>>(a);
+    return launch("k_product_tile", [&] {
+        k_product_tile<kProduct, kE4m3, kGroups><<<grid, kTileWaves * kWave, 0, st>>>(a);
     });
 }
 
@@ -214,14 +216,12 @@ epdc_status launch_stream(hipStream_t st, ProductArgs &a)
 template <bool kE4m3>
 epdc_status launch_forward(hipStream_t st, ProductArgs &a)
 {
-    const bool gated = act_gated(a.act);
     const int64_t mean = (int64_t)a.rows / a.experts;
     if (mean <= 8)
         return launch_stream<kE4m3, 1>(st, a);
     if (mean <= 64)
-        return launch_tile<kForward, kE4m3, 64, 256, 2, 4>("k_product_tile", st, a,
-                                                           gated ? 128 : 256);
-    return launch_tile<kForward, kE4m3, 256, 256, 2, 4>("k_product_tile", st, a, gated ? 128 : 256);
+        return launch_tile<kForward, kE4m3, 1>(st, a);
+    return launch_tile<kForward, kE4m3, kE4m3 ? 3 : 4>(st, a);
 }
 
 }  // namespace
@@ -405,7 +405,7 @@ epdc_status epdc_expert_backward(const epdc_product_args *args, void *stream,
         g.contract = of;
         g.q = static_cast<const uint8_t *>(args->weight);
         g.out = static_cast<uint8_t *>(grad_input);
-        s = launch_tile<kGradInput, false, 256, 256, 2, 4>("k_product_tile", st, g, 256);
+        s = launch_tile<kGradInput, false, 4>(st, g);
         if (s != EPDC_SUCCESS)
             return s;
     }
@@ -415,7 +415,7 @@ epdc_status epdc_expert_backward(const epdc_product_args *args, void *stream,
         g.out_fp32 = grad_weight_dtype == EPDC_DT_FP32;
         g.q = static_cast<const uint8_t *>(args->input);
         g.out = static_cast<uint8_t *>(grad_weight);
-        s = launch_tile<kGradWeight, false, 256, 256, 2, 4>("k_product_tile", st, g, 256);
+        s = launch_tile<kGradWeight, false, 4>(st, g);
         if (s != EPDC_SUCCESS)
             return s;
     }

@@ -219,23 +219,38 @@ __device__ inline bool find_tile(const ProductArgs &a, int bm, int *lds, Tile &t
 
 typedef __attribute__((address_space(3))) uint8_t lds_byte;
 
+// base and bytes are the same in every lane; saying so keeps the descriptor in
+// scalar registers where the compiler took a vector division into them.
 __device__ inline __amdgpu_buffer_rsrc_t buffer_at(const uint8_t *base, uint32_t bytes)
 {
-    return __builtin_amdgcn_make_buffer_rsrc((void *)base, 0, (int)bytes, 0x00020000);
+    const uint64_t p = (uint64_t)base;
+    const uint64_t u = ((uint64_t)(uint32_t)uniform((int)(p >> 32)) << 32) |
+                       (uint32_t)uniform((int)(uint32_t)p);
+    return __builtin_amdgcn_make_buffer_rsrc((void *)u, 0, uniform((int)bytes), 0x00020000);
+}
+
+// 16 bytes per lane from `at + off` to LDS, lane order from `lds` on.  Written out
+// because the compiler, which cannot tell the two buffers of a tile apart,
+// else waits for every such load before a transposing LDS read; when they have
+// landed is wait_and_meet's business.  Nothing returns to registers.  M0 holds
+// the LDS address; the compiler itself has no use for M0 in these kernels.
+__device__ __forceinline__ void load_direct(__amdgpu_buffer_rsrc_t at, uint32_t off, uint8_t *lds)
+{
+    const int to = uniform((int)(uint32_t)(uintptr_t)(lds_byte *)lds);
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to),
+                 "v"(off), "s"(at));
+}
+
+// The same with 4 bytes per lane, from each lane's own address.
+__device__ __forceinline__ void load_direct4(const uint8_t *from, uint8_t *lds)
+{
+    const int to = uniform((int)(uint32_t)(uintptr_t)(lds_byte *)lds);
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(to),
+                 "v"(from));
 }
 
 constexpr uint32_t kNowhere = 0x80000000u;  // past every buffer below: the load gives zeros
 constexpr uint32_t kOpen = 0x7fffffffu;
-
-// Row `r` of the MFMA's Q operand in a gated product: inside a wave's 64 rows
-// the first half are gate rows, the second half the up rows of the same
-// columns, so that a lane holds both factors of its outputs.
-__device__ inline int gated_row(int r, int col0, int half)
-{
-    const int c = col0 + (r / 64) * 32 + (r % 32);
-    const int cc = c < half ? c : half - 1;
-    return (r % 64) < 32 ? cc : half + cc;
-}
 
 // An operand whose contraction index runs along memory rows: LDS holds kRows
 // rows of 128 bytes.  A direct load fills 1 KiB (8 rows) of LDS in lane order,
@@ -245,6 +260,7 @@ __device__ inline int gated_row(int r, int col0, int half)
 template <int kRows, int kWaves>
 struct StraightTile {
     static constexpr int kBytes = kRows * kStepBytes;
+    static constexpr int kReads = 1;  // LDS reads of a fragment
     static constexpr int kLoads = kRows / 8 / kWaves;
     static_assert(kRows % (8 * kWaves) == 0, "whole loads per wave");
     uint32_t off[kLoads];
@@ -263,6 +279,7 @@ struct StraightTile {
                      (uint32_t)chunk * 16;
     }
     // step: which 128 bytes of the rows; left: contraction bytes from there on
+    // (none left: zeros, and no traffic)
     template <int kCount = kLoads>
     __device__ inline void load(uint8_t *lds, int step, int left, int wave)
     {
@@ -270,9 +287,7 @@ struct StraightTile {
         const bool out = chunk * 16 >= left;
 #pragma unroll
         for (int d = 0; d < kCount; ++d)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                rs, (lds_byte *)(lds + (d * kWaves + wave) * 1024), 16, out ? kNowhere : off[d], 0,
-                0, 0);
+            load_direct(rs, out ? kNowhere : off[d], lds + (d * kWaves + wave) * 1024);
     }
     // 16 rows from row0; half 0 or 1 of the step.  Lane l: row l % 16, 16 bytes.
     __device__ static inline i32x4 frag(const uint8_t *lds, int row0, int half, int lane)
@@ -292,6 +307,7 @@ template <int kCols, int kWaves>
 struct CrossTile {
     static constexpr int kRowBytes = kCols * 2;
     static constexpr int kBytes = 64 * kRowBytes;
+    static constexpr int kReads = 2;
     static constexpr int kChunks = kRowBytes / 16;
     static constexpr int kRowsPerLoad = 64 / kChunks;
     static constexpr int kLoads = kBytes / 1024 / kWaves;
@@ -321,13 +337,12 @@ struct CrossTile {
     __device__ inline void load(uint8_t *lds, int step, int left, int wave)
     {
         static_assert(kCount == kLoads, "all columns of the tile");
-        const uint32_t rows = left < 64 ? left : 64;
+        const uint32_t rows = left < 64 ? (left > 0 ? left : 0) : 64;
         const __amdgpu_buffer_rsrc_t rs =
             buffer_at(base + (size_t)step * 64 * row_bytes, rows * (uint32_t)row_bytes);
 #pragma unroll
         for (int d = 0; d < kLoads; ++d)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                rs, (lds_byte *)(lds + (d * kWaves + wave) * 1024), 16, off[d], 0, 0, 0);
+            load_direct(rs, off[d], lds + (d * kWaves + wave) * 1024);
     }
     // 16 columns from col0, contraction rows half*32 + (lane/16)*8 ... +7
     __device__ static inline i32x4 frag(const uint8_t *lds, int col0, int half, int lane)
@@ -381,12 +396,33 @@ struct Count {
     static constexpr int value = kN;
 };
 
-// Every direct load and LDS read of this wave is done, and so are the other
-// waves' at the same point.  Unlike __syncthreads this is also a point no LDS
-// access may be moved across by the compiler.
-__device__ inline void wait_and_meet()
+// All but the kYoungest youngest direct loads and every LDS read of this wave
+// are done, and so are the other waves' at the same point; the compiler may
+// move no LDS access across it.
+template <int kYoungest>
+__device__ __forceinline__ void wait_and_meet()
 {
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kYoungest) : "memory");
+}
+
+// Spread LDS reads and direct loads between the multiplications of the code
+// before it: left to itself the compiler gathers the reads and then waits.
+template <int kReads, int kMuls, int kLoads, int kAt = 0>
+__device__ __forceinline__ void weave()
+{
+    constexpr int kGroups = kReads < kMuls ? kReads : kMuls;
+    if constexpr (kAt < kGroups) {
+        constexpr int kR = (kAt + 1) * kReads / kGroups - kAt * kReads / kGroups;
+        constexpr int kM = (kAt + 1) * kMuls / kGroups - kAt * kMuls / kGroups;
+        constexpr int kL = (kAt + 1) * kLoads / kGroups - kAt * kLoads / kGroups;
+        __builtin_amdgcn_sched_group_barrier(0x100, kR, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, kM, 0);
+        if constexpr (kL > 0)
+            __builtin_amdgcn_sched_group_barrier(0x020, kL, 0);
+        weave<kReads, kMuls, kLoads, kAt + 1>();
+    } else {
+        __builtin_amdgcn_sched_barrier(0);
+    }
 }
 
 // Four consecutive output columns of one row: bias, activation and residual in
@@ -428,23 +464,47 @@ __device__ inline void finish_forward(const ProductArgs &a, int expert, int row,
 // ---------------------------------------------------------------------------
 // The tile kernel
 // ---------------------------------------------------------------------------
+//
+// A tile is kGroups * 64 P rows by 256 Q columns, worked on by eight waves, two
+// along P and four along Q; the two of a SIMD share its columns and take the
+// 16-row blocks in turn, so a ragged tile of g groups costs each of them
+// g / kGroups of the work.  A step is 128 bytes of contraction.  Its operands
+// arrive as four units: P0 and P1, the first and second half of the rows, Q0
+// and Q1, 128 columns each (gated: Q0 gate rows, Q1 the up rows of the same
+// columns, so that a lane ends with both factors of its outputs).
+//
+// A step runs in two halves, one barrier each:
+//   A: P0 x Q0, P0 x Q1, while Q1 and P1 are read from LDS
+//   B: P1 x Q0, P1 x Q1, while P0 and Q0 of the next step are read
+// Each unit is read once, into registers; by the barrier after that every wave
+// has it, and its LDS takes the unit of two steps on.  So of the two steps that
+// LDS holds all but the pair being read is in flight: the loads of a pair have
+// one and a half steps to land.  (With whole steps as the unit, loads drain
+// at every barrier: loads alone took 1483 us for 32768 x 7168 x 4096 where these
+// take 1188, and the multiplications alone 1344.)
 
-template <int kProduct, bool kE4m3, int kBM, int kBN, int kWavesM, int kWavesN>
-__global__ __launch_bounds__(kWavesM *kWavesN *kWave) void k_product_tile(const ProductArgs a)
+constexpr int kTileWaves = 8, kTileWavesM = 2, kTileWavesN = 4, kTileCols = 256;
+
+template <int kProduct, bool kE4m3, int kGroups>
+__global__ __launch_bounds__(kTileWaves *kWave) void k_product_tile(const ProductArgs a)
 {
 #ifdef __HIP_DEVICE_COMPILE__  // the host pass needs the launch stub only
-    constexpr int kWaves = kWavesM * kWavesN;
-    constexpr int kMI = kBM / kWavesM / 16, kNJ = kBN / kWavesN / 16;
-    static_assert(kProduct != kForward || kBN / kWavesN == 64, "gated columns pair inside 64");
+    constexpr int kBM = kGroups * 64;
+    constexpr int kG0 = (kGroups + 1) / 2, kG1 = kGroups / 2;  // groups of P0, P1
+    typedef typename PickTile<kProduct == kGradWeight, kG0 * 64, kTileWaves>::type PTile0;
+    typedef typename PickTile<kProduct == kGradWeight, (kG1 ? kG1 : 1) * 64, kTileWaves>::type
+        PTile1;
+    typedef typename PickTile<kProduct != kForward, 128, kTileWaves>::type QTile;
+    constexpr int kP1At = PTile0::kBytes, kQ0At = kP1At + (kG1 ? PTile1::kBytes : 0);
+    constexpr int kQ1At = kQ0At + QTile::kBytes, kScaleAt = kQ1At + QTile::kBytes;
+    // e4m3: per half of a step 128 row and 128 column scales
+    constexpr int kStage = kScaleAt + (kE4m3 ? 2048 : 0);
     constexpr int kStep = kE4m3 ? 128 : 64;  // contraction elements per step
     constexpr int kElem = kE4m3 ? 1 : 2;
-    typedef typename PickTile<kProduct == kGradWeight, kBM, kWaves>::type PTile;
-    typedef typename PickTile<kProduct != kForward, kBN, kWaves>::type QTile;
-    constexpr int kStage = PTile::kBytes + QTile::kBytes;
     __shared__ __align__(1024) uint8_t lds[2 * kStage];
 
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x / kWave);
-    const int wm = wave / kWavesN, wn = wave % kWavesN;
+    const int wm = wave / kTileWavesN, wn = wave % kTileWavesN;
 
     Tile t;
     int contract = a.contract;  // elements
@@ -460,159 +520,212 @@ __global__ __launch_bounds__(kWavesM *kWavesN *kWave) void k_product_tile(const 
         t.rows = a.out_rows - t.row_tile * kBM;
         t.rows = t.rows < kBM ? t.rows : kBM;
     } else {
-        if (!find_tile<kWaves * kWave>(a, kBM, reinterpret_cast<int *>(lds), t))
+        if (!find_tile<kTileWaves * kWave>(a, kBM, reinterpret_cast<int *>(lds), t))
             return;
         __syncthreads();  // the scan's LDS becomes the operands'
     }
     const bool gated = kProduct == kForward && act_gated(a.act);
-    const int col0 = t.col_tile * (gated ? kBN / 2 : kBN);
+    const int col0 = t.col_tile * (gated ? kTileCols / 2 : kTileCols);
+    // weight row of column c of unit h (forward)
+    const auto weight_row = [&](int h, int c) {
+        const int n = gated ? a.weight_rows / 2 : a.weight_rows;
+        const int r = col0 + c + (gated ? 0 : h * 128);
+        return (r < n ? r : n - 1) + (gated ? h * n : 0);
+    };
 
-    PTile pt;
-    QTile qt;
-    if constexpr (kProduct == kGradWeight)
-        pt.init(a.p + (size_t)t.row0 * a.p_bytes, a.p_bytes, (uint32_t)(t.row_tile * kBM) * 2,
-                wave, lane);
-    else
-        pt.init(a.p + (size_t)t.row0 * a.p_bytes, a.p_bytes, wave, lane,
-                [&](int r) { return r < t.rows ? r : t.rows - 1; });
+    QTile q0, q1;
     if constexpr (kProduct == kForward) {
-        const int n = a.weight_rows;
-        qt.init(a.q + (size_t)t.expert * n * a.q_bytes, a.q_bytes, wave, lane, [&](int r) {
-            if (gated)
-                return gated_row(r, col0, n / 2);
-            return col0 + r < n ? col0 + r : n - 1;
-        });
-    } else if constexpr (kProduct == kGradInput) {
-        qt.init(a.q + (size_t)t.expert * a.weight_rows * a.q_bytes, a.q_bytes, (uint32_t)col0 * 2,
-                wave, lane);
+        const uint8_t *w = a.q + (size_t)t.expert * a.weight_rows * a.q_bytes;
+        q0.init(w, a.q_bytes, wave, lane, [&](int r) { return weight_row(0, r); });
+        q1.init(w, a.q_bytes, wave, lane, [&](int r) { return weight_row(1, r); });
     } else {
-        qt.init(a.q + (size_t)t.row0 * a.q_bytes, a.q_bytes, (uint32_t)col0 * 2, wave, lane);
+        const uint8_t *q = a.q + (kProduct == kGradInput
+                                      ? (size_t)t.expert * a.weight_rows * a.q_bytes
+                                      : (size_t)t.row0 * a.q_bytes);
+        q0.init(q, a.q_bytes, (uint32_t)col0 * 2, wave, lane);
+        q1.init(q, a.q_bytes, (uint32_t)col0 * 2 + 256, wave, lane);
     }
 
-    f32x4 acc[kMI][kNJ];
+    constexpr int kMI = kGroups * 2;
+    f32x4 acc[kMI][4];
 #pragma unroll
     for (int i = 0; i < kMI; ++i)
 #pragma unroll
-        for (int j = 0; j < kNJ; ++j)
+        for (int j = 0; j < 4; ++j)
             acc[i][j] = f32x4{0, 0, 0, 0};
 
-    const int qrow = wn * (kNJ * 16);
     const int steps = (contract + kStep - 1) / kStep;
-    // Row blocks of 16 go to the kWavesM waves of a SIMD in turn, so a ragged tile
-    // of g 64-row groups costs each of them g / kGroups of the work.
     auto sweep = [&](auto groups) {
-        constexpr int kA = decltype(groups)::value;          // 64-row groups with rows
-        constexpr int kI = kA * 4 / kWavesM;                 // row blocks of this wave
-        constexpr int kPLoads = kProduct == kGradWeight ? PTile::kLoads : kA * 8 / kWaves;
-        auto load = [&](int s) {
-            uint8_t *stage = lds + (s & 1) * kStage;
-            const int left = contract - s * kStep;
-            pt.template load<kPLoads>(stage, s, kProduct == kGradWeight ? left : left * kElem,
-                                      wave);
-            qt.load(stage + PTile::kBytes, s, kProduct == kForward ? left * kElem : left, wave);
-        };
+        constexpr int kA = decltype(groups)::value;  // 64-row groups that hold rows
+        constexpr int kA0 = (kA + 1) / 2, kA1 = kA / 2;
+        constexpr int kI0 = 2 * kA0, kI1 = 2 * kA1;  // row blocks of a wave
+        constexpr int kN0 = kI0, kN1 = kI1 ? kI1 : 1;
+        PTile0 p0;
+        PTile1 p1;
+        const uint8_t *p = a.p + (size_t)t.row0 * a.p_bytes;
+        if constexpr (kProduct == kGradWeight) {
+            p0.init(p, a.p_bytes, (uint32_t)(t.row_tile * kBM) * 2, wave, lane);
+            p1.init(p, a.p_bytes, (uint32_t)(t.row_tile * kBM) * 2 + 256, wave, lane);
+        } else {
+            const auto row = [&](int r) { return r < t.rows ? r : t.rows - 1; };
+            p0.init(p, a.p_bytes, wave, lane, row);
+            if constexpr (kA1 > 0)
+                p1.init(p, a.p_bytes, wave, lane, [&](int r) { return row(kA0 * 64 + r); });
+        }
+        constexpr bool kPCross = kProduct == kGradWeight;
+        constexpr int kL0 = kPCross ? PTile0::kLoads : kA0, kL1 = kPCross ? PTile1::kLoads : kA1;
+        // e4m3: waves 0 and 1 (of 4) bring the rows' scales, 2 and 3 the columns'
+        const int at4 = (wave & 1) * 64 + lane;
+        const uint8_t *scale_base[2] = {nullptr, nullptr};
         if constexpr (kE4m3) {
-            if (steps > 0)
-                load(0);
-            // the rows' scales and the columns' block scales
-            const float *sx[kI], *sw[kNJ];
             const int blocks = contract / 128;
 #pragma unroll
-            for (int i = 0; i < kI; ++i) {
-                int r = (i * kWavesM + wm) * 16 + (lane & 15);
+            for (int h = 0; h < 2; ++h) {
+                int r = h * kA0 * 64 + at4;
                 r = r < t.rows ? r : t.rows - 1;
-                sx[i] = a.scales + (size_t)(t.row0 + r) * blocks;
+                const size_t at = wave & 2 ? (size_t)t.expert * ((a.weight_rows + 127) / 128) +
+                                                 weight_row(h, at4) / 128
+                                           : (size_t)(t.row0 + r);
+                scale_base[h] = reinterpret_cast<const uint8_t *>(
+                    (wave & 2 ? a.weight_scales : a.scales) + at * blocks);
             }
+        }
+        const auto load_scales = [&](int s, int h) {
+            // past the end: any scale in bounds, its products are zero
+            const int b = s < steps ? s : 0;
+            load_direct4(scale_base[h] + b * 4, lds + (s & 1) * kStage + kScaleAt + h * 1024 +
+                                                    (wave & 3) * 256);
+        };
+        const auto load0 = [&](int s) {
+            uint8_t *st = lds + (s & 1) * kStage;
+            const int left = contract - s * kStep;
+            p0.template load<kL0>(st, s, kPCross ? left : left * kElem, wave);
+            q0.load(st + kQ0At, s, kProduct == kForward ? left * kElem : left, wave);
+            if constexpr (kE4m3)
+                load_scales(s, 0);
+        };
+        const auto load1 = [&](int s) {
+            uint8_t *st = lds + (s & 1) * kStage;
+            const int left = contract - s * kStep;
+            q1.load(st + kQ1At, s, kProduct == kForward ? left * kElem : left, wave);
+            if constexpr (kA1 > 0)
+                p1.template load<kL1>(st + kP1At, s, kPCross ? left : left * kElem, wave);
+            if constexpr (kE4m3)
+                load_scales(s, 1);
+        };
+        constexpr int kAll0 = kL0 + QTile::kLoads + (kE4m3 ? 1 : 0);
+        constexpr int kAll1 = (kA1 ? kL1 : 0) + QTile::kLoads + (kE4m3 ? 1 : 0);
+
+        i32x4 fp0[kN0][2], fp1[kN1][2], fq0[2][2], fq1[2][2];
+        float sp0[kN0], sp1[kN1], sq0[2], sq1[2];
+        const auto read_p0 = [&](int s) {
+            const uint8_t *st = lds + (s & 1) * kStage;
 #pragma unroll
-            for (int j = 0; j < kNJ; ++j) {
-                const int r = qrow + j * 16 + (lane >> 4) * 4;
-                int c = gated ? gated_row(r, col0, a.weight_rows / 2) : col0 + r;
-                c = c < a.weight_rows ? c : a.weight_rows - 1;
-                sw[j] = a.weight_scales +
-                        ((size_t)t.expert * ((a.weight_rows + 127) / 128) + c / 128) * blocks;
+            for (int i = 0; i < kI0; ++i) {
+                const int r = (i * kTileWavesM + wm) * 16;
+                fp0[i][0] = PTile0::frag(st, r, 0, lane);
+                fp0[i][1] = PTile0::frag(st, r, 1, lane);
+                if constexpr (kE4m3)
+                    sp0[i] = reinterpret_cast<const float *>(st + kScaleAt)[r + (lane & 15)];
             }
-            for (int s = 0; s < steps; ++s) {
-                __syncthreads();  // step s has landed, and every wave is done with step s - 1
-                if (s + 1 < steps)
-                    load(s + 1);
-                const uint8_t *ps = lds + (s & 1) * kStage, *qs = ps + PTile::kBytes;
-                i32x8 q[kNJ];
-                float fw[kNJ];
+        };
+        const auto read_p1 = [&](int s) {
+            const uint8_t *st = lds + (s & 1) * kStage;
 #pragma unroll
-                for (int j = 0; j < kNJ; ++j) {
-                    q[j] = join(QTile::frag(qs, qrow + j * 16, 0, lane),
-                                QTile::frag(qs, qrow + j * 16, 1, lane));
-                    fw[j] = sw[j][s];
-                }
+            for (int i = 0; i < kI1; ++i) {
+                const int r = (i * kTileWavesM + wm) * 16;
+                fp1[i][0] = PTile1::frag(st + kP1At, r, 0, lane);
+                fp1[i][1] = PTile1::frag(st + kP1At, r, 1, lane);
+                if constexpr (kE4m3)
+                    sp1[i] = reinterpret_cast<const float *>(st + kScaleAt + 1024)[r + (lane & 15)];
+            }
+        };
+        const auto read_q = [&](int s, int h, i32x4 (&f)[2][2], float (&sc)[2]) {
+            const uint8_t *st = lds + (s & 1) * kStage;
 #pragma unroll
-                for (int i = 0; i < kI; ++i) {
-                    const int row = (i * kWavesM + wm) * 16;
-                    const i32x8 p = join(PTile::frag(ps, row, 0, lane),
-                                         PTile::frag(ps, row, 1, lane));
-                    const float fx = sx[i][s];
+            for (int j = 0; j < 2; ++j) {
+                const int c = wn * 32 + j * 16;
+                f[j][0] = QTile::frag(st + (h ? kQ1At : kQ0At), c, 0, lane);
+                f[j][1] = QTile::frag(st + (h ? kQ1At : kQ0At), c, 1, lane);
+                if constexpr (kE4m3)
+                    sc[j] = reinterpret_cast<const float *>(
+                        st + kScaleAt + h * 1024 + 512)[c + (lane >> 4) * 4];
+            }
+        };
+        // row blocks i0 ... of acc by columns j0, j0 + 1
+        const auto multiply = [&](auto count, int i0, int j0, const auto &p, const auto &ps,
+                                  const auto &q, const auto &qs) {
+            constexpr int kI = decltype(count)::value;
+            if constexpr (kE4m3) {
 #pragma unroll
-                    for (int j = 0; j < kNJ; ++j) {
-                        const f32x4 d = mfma_e4m3(q[j], p, f32x4{0, 0, 0, 0});
-                        const float f = fx * fw[j];
+                for (int i = 0; i < kI; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const f32x4 d = mfma_e4m3(join(q[j][0], q[j][1]), join(p[i][0], p[i][1]),
+                                                  f32x4{0, 0, 0, 0});
+                        const float f = ps[i] * qs[j];
 #pragma unroll
                         for (int v = 0; v < 4; ++v)
-                            acc[i][j][v] = __builtin_fmaf(d[v], f, acc[i][j][v]);
+                            acc[i0 + i][j0 + j][v] =
+                                __builtin_fmaf(d[v], f, acc[i0 + i][j0 + j][v]);
                     }
-                }
+            } else {
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+#pragma unroll
+                    for (int i = 0; i < kI; ++i)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+                            acc[i0 + i][j0 + j] =
+                                mfma_bf16(q[j][half], p[i][half], acc[i0 + i][j0 + j]);
             }
-        } else {
-            // Fragments run half a step ahead of the matrix cores: while half 0 of
-            // step s is multiplied half 1 is read, and while half 1 is multiplied
-            // half 0 of step s + 1.  The one barrier of a step stands between: by
-            // then every wave has the rest of step s in registers, so its buffer
-            // takes step s + 2, whose loads have a whole step to land.
-            i32x4 p0[kI], q0[kNJ], p1[kI], q1[kNJ];
-            auto frags = [&](int s, int half, i32x4 (&p)[kI], i32x4 (&q)[kNJ]) {
-                const uint8_t *ps = lds + (s & 1) * kStage, *qs = ps + PTile::kBytes;
-#pragma unroll
-                for (int j = 0; j < kNJ; ++j)
-                    q[j] = QTile::frag(qs, qrow + j * 16, half, lane);
-#pragma unroll
-                for (int i = 0; i < kI; ++i)
-                    p[i] = PTile::frag(ps, (i * kWavesM + wm) * 16, half, lane);
-            };
-            auto multiply = [&](const i32x4 (&p)[kI], const i32x4 (&q)[kNJ]) {
-#pragma unroll
-                for (int i = 0; i < kI; ++i)
-#pragma unroll
-                    for (int j = 0; j < kNJ; ++j)
-                        acc[i][j] = mfma_bf16(q[j], p[i], acc[i][j]);
-            };
-            if (steps > 0) {
-                load(0);
-                if (steps > 1)
-                    load(1);
-                // wait for step 0 alone would need the load count; once per tile
-                wait_and_meet();
-                frags(0, 0, p0, q0);
-            }
-            for (int s = 0; s < steps; ++s) {
-                frags(s, 1, p1, q1);
-                multiply(p0, q0);
-                wait_and_meet();
-                if (s + 2 < steps)
-                    load(s + 2);
-                frags(s + 1, 0, p0, q0);  // after the last step: read, never used
-                multiply(p1, q1);
-            }
+        };
+        constexpr int kEach = kE4m3 ? 2 : 4;  // multiplications of a row block by two columns
+        constexpr int kScaleReads = kE4m3 ? 1 : 0;
+        constexpr int kReadP0 = kI0 * (2 * PTile0::kReads + kScaleReads);
+        constexpr int kReadP1 = kI1 * (2 * PTile1::kReads + kScaleReads);
+        constexpr int kReadQ = 2 * (2 * QTile::kReads + kScaleReads);
+
+        load0(0);
+        load1(0);
+        load0(1);
+        load1(1);
+        wait_and_meet<kAll0 + kAll1>();
+        read_p0(0);
+        read_q(0, 0, fq0, sq0);
+        wait_and_meet<kAll0 + kAll1>();
+        for (int s = 0; s < steps; ++s) {
+            load0(s + 2);
+            read_q(s, 1, fq1, sq1);
+            read_p1(s);
+            multiply(Count<kI0>(), 0, 0, fp0, sp0, fq0, sq0);
+            weave<kReadQ + kReadP1, kI0 * kEach, kAll0>();
+            multiply(Count<kI0>(), 0, 2, fp0, sp0, fq1, sq1);
+            wait_and_meet<kAll0 + kAll1>();
+            load1(s + 2);
+            read_p0(s + 1);  // after the last step: zeros, never used
+            multiply(Count<kI1>(), kI0, 0, fp1, sp1, fq0, sq0);
+            weave<kReadP0, (kI1 ? kI1 : 1) * kEach, kAll1>();
+            read_q(s + 1, 0, fq0, sq0);
+            multiply(Count<kI1>(), kI0, 2, fp1, sp1, fq1, sq1);
+            weave<kReadQ, (kI1 ? kI1 : 1) * kEach, 0>();
+            wait_and_meet<kAll0 + kAll1>();
         }
+        wait_and_meet<0>();  // no load may outlive the block
     };
     if constexpr (kProduct == kGradWeight) {
-        sweep(Count<kBM / 64>());
+        sweep(Count<kGroups>());
     } else {
         const int groups = (t.rows + 63) / 64;
-        if constexpr (kBM >= 256) {
+        if constexpr (kGroups >= 4) {
             if (groups >= 4)
                 sweep(Count<4>());
-            else if (groups == 3)
+        }
+        if constexpr (kGroups >= 3) {
+            if (groups == 3)
                 sweep(Count<3>());
         }
-        if constexpr (kBM >= 128) {
+        if constexpr (kGroups >= 2) {
             if (groups == 2)
                 sweep(Count<2>());
         }
@@ -623,23 +736,23 @@ __global__ __launch_bounds__(kWavesM *kWavesN *kWave) void k_product_tile(const 
     // lane: row l % 16 of each P block, columns 4 * (l / 16) ... +3 of each Q block
 #pragma unroll
     for (int i = 0; i < kMI; ++i) {
-        const int r = (i * kWavesM + wm) * 16 + (lane & 15);
+        const int r = (i * kTileWavesM + wm) * 16 + (lane & 15);
         if (r >= t.rows)
             continue;
         if constexpr (kProduct == kForward) {
             if (gated) {
 #pragma unroll
-                for (int j = 0; j < kNJ / 2; ++j) {
+                for (int j = 0; j < 2; ++j) {
                     const int c = col0 + wn * 32 + j * 16 + (lane >> 4) * 4;
                     if (c < a.out_cols)
-                        finish_forward(a, t.expert, t.row0 + r, c, acc[i][j], acc[i][j + kNJ / 2]);
+                        finish_forward(a, t.expert, t.row0 + r, c, acc[i][j], acc[i][j + 2]);
                 }
                 continue;
             }
         }
 #pragma unroll
-        for (int j = 0; j < kNJ; ++j) {
-            const int c = col0 + qrow + j * 16 + (lane >> 4) * 4;
+        for (int j = 0; j < 4; ++j) {
+            const int c = col0 + (j >> 1) * 128 + wn * 32 + (j & 1) * 16 + (lane >> 4) * 4;
             if (c >= a.out_cols)
                 continue;
             if constexpr (kProduct == kForward) {
