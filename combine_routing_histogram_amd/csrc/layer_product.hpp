@@ -241,14 +241,6 @@ __device__ __forceinline__ void load_direct(__amdgpu_buffer_rsrc_t at, uint32_t 
                  "v"(off), "s"(at));
 }
 
-// The same with 4 bytes per lane, from each lane's own address.
-__device__ __forceinline__ void load_direct4(const uint8_t *from, uint8_t *lds)
-{
-    const int to = uniform((int)(uint32_t)(uintptr_t)(lds_byte *)lds);
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(to),
-                 "v"(from));
-}
-
 constexpr uint32_t kNowhere = 0x80000000u;  // past every buffer below: the load gives zeros
 constexpr uint32_t kOpen = 0x7fffffffu;
 
@@ -396,6 +388,15 @@ struct Count {
     static constexpr int value = kN;
 };
 
+template <int kN, int kAt = 0, typename F>
+__device__ __forceinline__ void unrolled(F &&f)
+{
+    if constexpr (kAt < kN) {
+        f(Count<kAt>());
+        unrolled<kN, kAt + 1>(f);
+    }
+}
+
 // All but the kYoungest youngest direct loads and every LDS read of this wave
 // are done, and so are the other waves' at the same point; the compiler may
 // move no LDS access across it.
@@ -496,12 +497,14 @@ __global__ __launch_bounds__(kTileWaves *kWave) void k_product_tile(const Produc
         PTile1;
     typedef typename PickTile<kProduct != kForward, 128, kTileWaves>::type QTile;
     constexpr int kP1At = PTile0::kBytes, kQ0At = kP1At + (kG1 ? PTile1::kBytes : 0);
-    constexpr int kQ1At = kQ0At + QTile::kBytes, kScaleAt = kQ1At + QTile::kBytes;
-    // e4m3: per half of a step 128 row and 128 column scales
-    constexpr int kStage = kScaleAt + (kE4m3 ? 2048 : 0);
+    constexpr int kQ1At = kQ0At + QTile::kBytes;
+    constexpr int kStage = kQ1At + QTile::kBytes;
+    // e4m3: the scales of four steps, 16 bytes for every row and every four
+    // columns, also twice
+    constexpr int kScaleBytes = kGroups * 1024 + 1024, kScaleAt = 2 * kStage;
     constexpr int kStep = kE4m3 ? 128 : 64;  // contraction elements per step
     constexpr int kElem = kE4m3 ? 1 : 2;
-    __shared__ __align__(1024) uint8_t lds[2 * kStage];
+    __shared__ __align__(1024) uint8_t lds[2 * kStage + (kE4m3 ? 2 * kScaleBytes : 0)];
 
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x / kWave);
     const int wm = wave / kTileWavesN, wn = wave % kTileWavesN;
@@ -574,35 +577,44 @@ __global__ __launch_bounds__(kTileWaves *kWave) void k_product_tile(const Produc
         }
         constexpr bool kPCross = kProduct == kGradWeight;
         constexpr int kL0 = kPCross ? PTile0::kLoads : kA0, kL1 = kPCross ? PTile1::kLoads : kA1;
-        // e4m3: waves 0 and 1 (of 4) bring the rows' scales, 2 and 3 the columns'
-        const int at4 = (wave & 1) * 64 + lane;
-        const uint8_t *scale_base[2] = {nullptr, nullptr};
+        // e4m3: the first waves bring the rows' scales, 64 rows each, the fifth the
+        // columns', once every four steps; 16 bytes at a time because a row's
+        // scales lie in a line of their own
+        const bool scaler = kE4m3 && (wave < kA || wave == 4);
+        const uint8_t *scale_base = nullptr;
+        uint32_t scale_off = 0, scale_end = 0;
         if constexpr (kE4m3) {
             const int blocks = contract / 128;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                int r = h * kA0 * 64 + at4;
+            if (wave == 4) {
+                const int nb = (a.weight_rows + 127) / 128;
+                scale_base = reinterpret_cast<const uint8_t *>(a.weight_scales +
+                                                               (size_t)t.expert * nb * blocks);
+                scale_end = (uint32_t)nb * blocks * 4;
+                scale_off = (uint32_t)(weight_row(lane / 32, lane % 32 * 4) / 128) * blocks * 4;
+            } else {
+                int r = wave * 64 + lane;
                 r = r < t.rows ? r : t.rows - 1;
-                const size_t at = wave & 2 ? (size_t)t.expert * ((a.weight_rows + 127) / 128) +
-                                                 weight_row(h, at4) / 128
-                                           : (size_t)(t.row0 + r);
-                scale_base[h] = reinterpret_cast<const uint8_t *>(
-                    (wave & 2 ? a.weight_scales : a.scales) + at * blocks);
+                scale_base = reinterpret_cast<const uint8_t *>(a.scales + (size_t)t.row0 * blocks);
+                scale_end = (uint32_t)t.rows * blocks * 4;
+                scale_off = (uint32_t)r * blocks * 4;
             }
         }
-        const auto load_scales = [&](int s, int h) {
-            // past the end: any scale in bounds, its products are zero
-            const int b = s < steps ? s : 0;
-            load_direct4(scale_base[h] + b * 4, lds + (s & 1) * kStage + kScaleAt + h * 1024 +
-                                                    (wave & 3) * 256);
+        const auto load_scales = [&](int group) {
+            if (scaler)
+                load_direct(buffer_at(scale_base, scale_end), scale_off + group * 16,
+                            lds + kScaleAt + (group & 1) * kScaleBytes +
+                                (wave == 4 ? kGroups : wave) * 1024);
+        };
+        // scale of row r (column group: row kGroups * 64 + c / 4) in step s
+        const auto scale = [&](int s, int r) {
+            return reinterpret_cast<const float *>(lds + kScaleAt +
+                                                   (s >> 2 & 1) * kScaleBytes)[r * 4 + (s & 3)];
         };
         const auto load0 = [&](int s) {
             uint8_t *st = lds + (s & 1) * kStage;
             const int left = contract - s * kStep;
             p0.template load<kL0>(st, s, kPCross ? left : left * kElem, wave);
             q0.load(st + kQ0At, s, kProduct == kForward ? left * kElem : left, wave);
-            if constexpr (kE4m3)
-                load_scales(s, 0);
         };
         const auto load1 = [&](int s) {
             uint8_t *st = lds + (s & 1) * kStage;
@@ -610,11 +622,10 @@ __global__ __launch_bounds__(kTileWaves *kWave) void k_product_tile(const Produc
             q1.load(st + kQ1At, s, kProduct == kForward ? left * kElem : left, wave);
             if constexpr (kA1 > 0)
                 p1.template load<kL1>(st + kP1At, s, kPCross ? left : left * kElem, wave);
-            if constexpr (kE4m3)
-                load_scales(s, 1);
         };
-        constexpr int kAll0 = kL0 + QTile::kLoads + (kE4m3 ? 1 : 0);
-        constexpr int kAll1 = (kA1 ? kL1 : 0) + QTile::kLoads + (kE4m3 ? 1 : 0);
+        // loads of a pair; the few of scales are not counted, so now and then a
+        // wave waits for one load more than it needs
+        constexpr int kAll0 = kL0 + QTile::kLoads, kAll1 = (kA1 ? kL1 : 0) + QTile::kLoads;
 
         i32x4 fp0[kN0][2], fp1[kN1][2], fq0[2][2], fq1[2][2];
         float sp0[kN0], sp1[kN1], sq0[2], sq1[2];
@@ -626,7 +637,7 @@ __global__ __launch_bounds__(kTileWaves *kWave) void k_product_tile(const Produc
                 fp0[i][0] = PTile0::frag(st, r, 0, lane);
                 fp0[i][1] = PTile0::frag(st, r, 1, lane);
                 if constexpr (kE4m3)
-                    sp0[i] = reinterpret_cast<const float *>(st + kScaleAt)[r + (lane & 15)];
+                    sp0[i] = scale(s, r + (lane & 15));
             }
         };
         const auto read_p1 = [&](int s) {
@@ -637,7 +648,7 @@ __global__ __launch_bounds__(kTileWaves *kWave) void k_product_tile(const Produc
                 fp1[i][0] = PTile1::frag(st + kP1At, r, 0, lane);
                 fp1[i][1] = PTile1::frag(st + kP1At, r, 1, lane);
                 if constexpr (kE4m3)
-                    sp1[i] = reinterpret_cast<const float *>(st + kScaleAt + 1024)[r + (lane & 15)];
+                    sp1[i] = scale(s, kA0 * 64 + r + (lane & 15));
             }
         };
         const auto read_q = [&](int s, int h, i32x4 (&f)[2][2], float (&sc)[2]) {
@@ -648,44 +659,73 @@ __global__ __launch_bounds__(kTileWaves *kWave) void k_product_tile(const Produc
                 f[j][0] = QTile::frag(st + (h ? kQ1At : kQ0At), c, 0, lane);
                 f[j][1] = QTile::frag(st + (h ? kQ1At : kQ0At), c, 1, lane);
                 if constexpr (kE4m3)
-                    sc[j] = reinterpret_cast<const float *>(
-                        st + kScaleAt + h * 1024 + 512)[c + (lane >> 4) * 4];
+                    sc[j] = scale(s, kGroups * 64 + h * 32 + c / 4 + (lane >> 4));
             }
         };
-        // row blocks i0 ... of acc by columns j0, j0 + 1
-        const auto multiply = [&](auto count, int i0, int j0, const auto &p, const auto &ps,
-                                  const auto &q, const auto &qs) {
+        // bf16: row blocks i0 ... of acc by columns j0, j0 + 1
+        const auto multiply = [&](auto count, int i0, int j0, const auto &p, const auto &q) {
             constexpr int kI = decltype(count)::value;
-            if constexpr (kE4m3) {
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
 #pragma unroll
                 for (int i = 0; i < kI; ++i)
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const f32x4 d = mfma_e4m3(join(q[j][0], q[j][1]), join(p[i][0], p[i][1]),
-                                                  f32x4{0, 0, 0, 0});
-                        const float f = ps[i] * qs[j];
+                    for (int j = 0; j < 2; ++j)
+                        acc[i0 + i][j0 + j] =
+                            mfma_bf16(q[j][half], p[i][half], acc[i0 + i][j0 + j]);
+        };
+        // e4m3: the products of a step's 128 features are scaled as they are added
+        // to acc, four multiply-adds per matrix instruction.  They follow kLag
+        // instructions later, in its shadow: at once they would wait for it.
+        constexpr int kLag = 3;
+        f32x4 late[kLag];
+        float late_scale[kLag];
 #pragma unroll
-                        for (int v = 0; v < 4; ++v)
-                            acc[i0 + i][j0 + j][v] =
-                                __builtin_fmaf(d[v], f, acc[i0 + i][j0 + j][v]);
-                    }
-            } else {
+        for (int k = 0; k < kLag; ++k) {
+            late[k] = f32x4{0, 0, 0, 0};
+            late_scale[k] = 0.0f;
+        }
+        const auto add_late = [&](auto row, auto col) {
+            f32x4 &to = acc[decltype(row)::value][decltype(col)::value];
 #pragma unroll
-                for (int half = 0; half < 2; ++half)
+            for (int v = 0; v < 4; ++v)
+                to[v] = __builtin_fmaf(late[0][v], late_scale[0], to[v]);
 #pragma unroll
-                    for (int i = 0; i < kI; ++i)
-#pragma unroll
-                        for (int j = 0; j < 2; ++j)
-                            acc[i0 + i][j0 + j] =
-                                mfma_bf16(q[j][half], p[i][half], acc[i0 + i][j0 + j]);
+            for (int k = 0; k + 1 < kLag; ++k) {
+                late[k] = late[k + 1];
+                late_scale[k] = late_scale[k + 1];
             }
         };
-        constexpr int kEach = kE4m3 ? 2 : 4;  // multiplications of a row block by two columns
+        // row blocks kAt ... kAt + kI - 1 by all four column blocks; before them
+        // the last ones of the phase over kPrevI blocks from kPrevAt
+        const auto multiply_scaled = [&](auto ci, auto cat, auto cprev, auto cprev_at,
+                                         const auto &p, const auto &ps) {
+            constexpr int kI = decltype(ci)::value, kAt = decltype(cat)::value;
+            constexpr int kPrevI = decltype(cprev)::value, kPrevAt = decltype(cprev_at)::value;
+            unrolled<4 * kI>([&](auto cn) {
+                constexpr int n = decltype(cn)::value;
+                constexpr int h = n / (2 * kI), i = n / 2 % kI, j = n % 2;
+                const i32x4(&q)[2] = h ? fq1[j] : fq0[j];
+                const f32x4 d = mfma_e4m3(join(q[0], q[1]), join(p[i][0], p[i][1]),
+                                          f32x4{0, 0, 0, 0});
+                const float scale = ps[i] * (h ? sq1[j] : sq0[j]);
+                constexpr int m = n >= kLag ? n - kLag : 4 * kPrevI + n - kLag;
+                constexpr int mi = n >= kLag ? kI : kPrevI, ma = n >= kLag ? kAt : kPrevAt;
+                add_late(Count<ma + m / 2 % mi>(), Count<m / (2 * mi) * 2 + m % 2>());
+                late[kLag - 1] = d;
+                late_scale[kLag - 1] = scale;
+                // vector arithmetic stays where it is; memory and scalar code may pass
+                __builtin_amdgcn_sched_barrier(0x0004 | 0x0010 | 0x0080);
+            });
+        };
+        constexpr int kEach = 4;  // bf16 multiplications of a row block by two columns
         constexpr int kScaleReads = kE4m3 ? 1 : 0;
         constexpr int kReadP0 = kI0 * (2 * PTile0::kReads + kScaleReads);
         constexpr int kReadP1 = kI1 * (2 * PTile1::kReads + kScaleReads);
         constexpr int kReadQ = 2 * (2 * QTile::kReads + kScaleReads);
 
+        if constexpr (kE4m3)
+            load_scales(0);
         load0(0);
         load1(0);
         load0(1);
@@ -695,21 +735,43 @@ __global__ __launch_bounds__(kTileWaves *kWave) void k_product_tile(const Produc
         read_q(0, 0, fq0, sq0);
         wait_and_meet<kAll0 + kAll1>();
         for (int s = 0; s < steps; ++s) {
+            if constexpr (kE4m3) {
+                // the group before has been read; this one is needed from step s + 4
+                if ((s & 3) == 0)
+                    load_scales((s >> 2) + 1);
+            }
             load0(s + 2);
             read_q(s, 1, fq1, sq1);
             read_p1(s);
-            multiply(Count<kI0>(), 0, 0, fp0, sp0, fq0, sq0);
-            weave<kReadQ + kReadP1, kI0 * kEach, kAll0>();
-            multiply(Count<kI0>(), 0, 2, fp0, sp0, fq1, sq1);
+            if constexpr (kE4m3) {
+                multiply_scaled(Count<kI0>(), Count<0>(), Count<kI1 ? kI1 : kI0>(),
+                                Count<kI1 ? kI0 : 0>(), fp0, sp0);
+            } else {
+                multiply(Count<kI0>(), 0, 0, fp0, fq0);
+                weave<kReadQ + kReadP1, kI0 * kEach, kAll0>();
+                multiply(Count<kI0>(), 0, 2, fp0, fq1);
+            }
             wait_and_meet<kAll0 + kAll1>();
             load1(s + 2);
             read_p0(s + 1);  // after the last step: zeros, never used
-            multiply(Count<kI1>(), kI0, 0, fp1, sp1, fq0, sq0);
-            weave<kReadP0, (kI1 ? kI1 : 1) * kEach, kAll1>();
-            read_q(s + 1, 0, fq0, sq0);
-            multiply(Count<kI1>(), kI0, 2, fp1, sp1, fq1, sq1);
-            weave<kReadQ, (kI1 ? kI1 : 1) * kEach, 0>();
+            if constexpr (kE4m3) {
+                multiply_scaled(Count<kI1>(), Count<kI0>(), Count<kI0>(), Count<0>(), fp1, sp1);
+                read_q(s + 1, 0, fq0, sq0);
+            } else {
+                multiply(Count<kI1>(), kI0, 0, fp1, fq0);
+                weave<kReadP0, (kI1 ? kI1 : 1) * kEach, kAll1>();
+                read_q(s + 1, 0, fq0, sq0);
+                multiply(Count<kI1>(), kI0, 2, fp1, fq1);
+                weave<kReadQ, (kI1 ? kI1 : 1) * kEach, 0>();
+            }
             wait_and_meet<kAll0 + kAll1>();
+        }
+        if constexpr (kE4m3) {
+            constexpr int kLast = kI1 ? kI1 : kI0, kLastAt = kI1 ? kI0 : 0;
+            unrolled<kLag>([&](auto cn) {
+                constexpr int m = 4 * kLast + decltype(cn)::value - kLag;
+                add_late(Count<kLastAt + m / 2 % kLast>(), Count<m / (2 * kLast) * 2 + m % 2>());
+            });
         }
         wait_and_meet<0>();  // no load may outlive the block
     };
