@@ -149,10 +149,10 @@ epdc_status check_product(const epdc_product_args *p)
         return fail(EPDC_ERR_INVALID_ARGS, "one expert's weight must be smaller than 2 GiB");
     if (!p->expert_off)
         return fail(EPDC_ERR_INVALID_ARGS, "expert_off is required");
-    if (!aligned(p->expert_off, 4) || !aligned(p->bias, 4) || !aligned(p->scales, 4) ||
+    if (!aligned(p->expert_off, 4) || !aligned(p->bias, 16) || !aligned(p->scales, 4) ||
         !aligned(p->weight_scales, 4) || !aligned(p->input, 16) || !aligned(p->weight, 16))
-        return fail(EPDC_ERR_INVALID_ARGS,
-                    "input and weight must be 16-byte aligned, the other arrays 4-byte aligned");
+        return fail(EPDC_ERR_INVALID_ARGS, "input, weight and bias must be 16-byte aligned, the "
+                                           "other arrays 4-byte aligned");
     return EPDC_SUCCESS;
 }
 

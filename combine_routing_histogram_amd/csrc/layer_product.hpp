@@ -462,6 +462,75 @@ __device__ inline void finish_forward(const ProductArgs &a, int expert, int row,
     *reinterpret_cast<bf16x4 *>(a.out + at * 2) = to_bf16(y);
 }
 
+// Eight consecutive output columns of one row, as finish_forward; res: the
+// residual's, loaded beforehand.
+__device__ inline void finish_forward8(const ProductArgs &a, int expert, int row, int col,
+                                       float (&z)[8], float (&up)[8], bf16x8 res)
+{
+    const bool gated = act_gated(a.act);
+    if (a.bias) {
+        const f32x4 *b =
+            reinterpret_cast<const f32x4 *>(a.bias + (size_t)expert * a.weight_rows + col);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            z[i] += b[i / 4][i % 4];
+        if (gated) {
+            b = reinterpret_cast<const f32x4 *>(a.bias + (size_t)expert * a.weight_rows +
+                                                a.out_cols + col);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                up[i] += b[i / 4][i % 4];
+        }
+    }
+    bf16x8 o;
+    if (a.preact) {
+        uint16_t *z0 = a.preact + (size_t)row * a.weight_rows + col;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            o[i] = (__bf16)z[i];
+        *reinterpret_cast<bf16x8 *>(z0) = o;
+        if (gated) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                o[i] = (__bf16)up[i];
+            *reinterpret_cast<bf16x8 *>(z0 + a.out_cols) = o;
+        }
+    }
+    switch (a.act) {
+    case kActRelu:
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            z[i] = act_one(kActRelu, z[i]);
+        break;
+    case kActGelu:
+    case kActGeglu:
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            z[i] = act_gelu(z[i]);
+        break;
+    case kActSilu:
+    case kActSwiglu:
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            z[i] = act_silu(z[i]);
+        break;
+    }
+    if (gated) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            z[i] *= up[i];
+    }
+    if (a.residual) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            z[i] += (float)res[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        o[i] = (__bf16)z[i];
+    *reinterpret_cast<bf16x8 *>(a.out + ((size_t)row * a.out_cols + col) * 2) = o;
+}
+
 // ---------------------------------------------------------------------------
 // The tile kernel
 // ---------------------------------------------------------------------------
@@ -795,39 +864,76 @@ __global__ __launch_bounds__(kTileWaves *kWave) void k_product_tile(const Produc
             sweep(Count<1>());
     }
 
-    // lane: row l % 16 of each P block, columns 4 * (l / 16) ... +3 of each Q block
+    // The accumulators leave through LDS, 64 rows at a time: a lane holds 4 columns
+    // of 16 rows, and memory wants whole lines.  Written from the registers
+    // (8 bytes per lane, a residual load before each store) 1021 x 8 rows of
+    // 2048 x 7168 with bias and residual took 425 us of which 113 were this.
+    constexpr int kRowFloats = kTileCols, kChunkBytes = 64 * kRowFloats * 4;
+    constexpr int kTurns = sizeof lds >= 2 * kChunkBytes ? 2 : 1;
+    const int vecs = gated ? kTileCols / 16 : kTileCols / 8;  // of 8 output columns, per row
+    const int per = 64 * vecs / (kTileWaves * kWave);
+    const auto slot = [](int row, int quad) { return row * (kRowFloats / 4) + (quad ^ (row & 15)); };
 #pragma unroll
-    for (int i = 0; i < kMI; ++i) {
-        const int r = (i * kTileWavesM + wm) * 16 + (lane & 15);
-        if (r >= t.rows)
-            continue;
-        if constexpr (kProduct == kForward) {
-            if (gated) {
+    for (int c = 0; c < kGroups; ++c) {
+        if (c * 64 >= t.rows)
+            break;
+        f32x4 *chunk = reinterpret_cast<f32x4 *>(lds + (kTurns == 2 ? c & 1 : 0) * kChunkBytes);
+        if (kTurns == 1 && c > 0)
+            __syncthreads();
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int c = col0 + wn * 32 + j * 16 + (lane >> 4) * 4;
-                    if (c < a.out_cols)
-                        finish_forward(a, t.expert, t.row0 + r, c, acc[i][j], acc[i][j + 2]);
-                }
-                continue;
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                chunk[slot((i * kTileWavesM + wm) * 16 + (lane & 15),
+                           (j >> 1) * 32 + wn * 8 + (j & 1) * 4 + (lane >> 4))] =
+                    acc[c * 2 + i][j];
+        bf16x8 res[4];
+        if (kProduct == kForward && a.residual) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int at = k * kTileWaves * kWave + (int)threadIdx.x;
+                const int r = c * 64 + at / vecs, col = col0 + at % vecs * 8;
+                if (k < per && r < t.rows && col < a.out_cols)
+                    res[k] = *reinterpret_cast<const bf16x8 *>(
+                        a.residual + (size_t)(t.row0 + r) * a.out_cols + col);
             }
         }
+        __syncthreads();
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int c = col0 + (j >> 1) * 128 + wn * 32 + (j & 1) * 16 + (lane >> 4) * 4;
-            if (c >= a.out_cols)
+        for (int k = 0; k < 4; ++k) {
+            const int at = k * kTileWaves * kWave + (int)threadIdx.x;
+            const int lr = at / vecs, v = at % vecs, r = c * 64 + lr, col = col0 + v * 8;
+            if (k >= per || r >= t.rows || col >= a.out_cols)
                 continue;
+            float z[8], up[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                z[i] = chunk[slot(lr, v * 2 + i / 4)][i % 4];
+                up[i] = 0.0f;
+            }
+            if (gated) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    up[i] = chunk[slot(lr, 32 + v * 2 + i / 4)][i % 4];
+            }
             if constexpr (kProduct == kForward) {
-                finish_forward(a, t.expert, t.row0 + r, c, acc[i][j], f32x4{0, 0, 0, 0});
+                finish_forward8(a, t.expert, t.row0 + r, col, z, up, res[k]);
             } else {
                 const size_t row = kProduct == kGradInput
                                        ? (size_t)(t.row0 + r)
                                        : (size_t)t.expert * a.out_rows + t.row_tile * kBM + r;
-                const size_t at = row * a.out_cols + c;
-                if (kProduct == kGradWeight && a.out_fp32)
-                    *reinterpret_cast<f32x4 *>(a.out + at * 4) = acc[i][j];
-                else
-                    *reinterpret_cast<bf16x4 *>(a.out + at * 2) = to_bf16(acc[i][j]);
+                const size_t to = row * a.out_cols + col;
+                if (kProduct == kGradWeight && a.out_fp32) {
+                    f32x4 *o = reinterpret_cast<f32x4 *>(a.out + to * 4);
+                    o[0] = f32x4{z[0], z[1], z[2], z[3]};
+                    o[1] = f32x4{z[4], z[5], z[6], z[7]};
+                } else {
+                    bf16x8 o;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        o[i] = (__bf16)z[i];
+                    *reinterpret_cast<bf16x8 *>(a.out + to * 2) = o;
+                }
             }
         }
     }

@@ -22,9 +22,9 @@
  *  - `stream` is a hipStream_t passed as void*; NULL is the null stream.  The
  *    work is enqueued on it and the call returns without waiting.  No call
  *    records a memset node, so every one can be captured into a HIP graph.
- *  - Row-major layouts, no padding between rows.  Payload rows (input, weight,
- *    residual, preact, out and gradients of them) start 16-byte aligned, every
- *    other array 4-byte aligned.
+ *  - Row-major layouts, no padding between rows.  Logits, payload rows (input,
+ *    weight, residual, preact, out), gradients of them and the products' bias
+ *    start 16-byte aligned, every other array 4-byte aligned.
  *  - A call with no rows or tokens enqueues what its outputs need (zeroed
  *    losses and counts, zero weight gradients) and nothing else.
  *  - Sums, softmax statistics and losses are kept in fp32 (the matrix products
