@@ -53,7 +53,7 @@ constexpr int64_t kMaxExpertBytes = (int64_t)0x7fff0000;
 
 int gate_blocks(int64_t tokens, int limit)
 {
-    const int64_t b = (tokens + kGateTokens - 1) / kGateTokens;
+    const int64_t per = kGateThreads / gate_lanes(tokens), b = (tokens + per - 1) / per;
     return (int)(b < 1 ? 1 : (b < limit ? b : limit));
 }
 
@@ -97,29 +97,43 @@ GateArgs gate_args(const epdc_gate_args *g)
     return a;
 }
 
+// f(lanes, slots) with the lanes of a token and the logits of a lane
+template <typename F>
+void gate_form(int64_t tokens, int experts, F &&f)
+{
+    const int step = experts <= 64 ? 0 : experts <= 128 ? 1 : experts <= 256 ? 2 : 3;
+    if (gate_lanes(tokens) == 64) {
+        switch (step) {
+        case 0: f(Count<64>(), Count<1>()); break;
+        case 1: f(Count<64>(), Count<2>()); break;
+        case 2: f(Count<64>(), Count<4>()); break;
+        default: f(Count<64>(), Count<8>()); break;
+        }
+    } else {
+        switch (step) {
+        case 0: f(Count<16>(), Count<4>()); break;
+        case 1: f(Count<16>(), Count<8>()); break;
+        case 2: f(Count<16>(), Count<16>()); break;
+        default: f(Count<16>(), Count<32>()); break;
+        }
+    }
+}
+
 template <bool kBalance>
 void launch_gate(int grid, size_t lds, hipStream_t st, const GateArgs &a)
 {
-    if (a.experts <= 64)
-        k_gate<4, kBalance><<<grid, kGateThreads, lds, st>>>(a);
-    else if (a.experts <= 128)
-        k_gate<8, kBalance><<<grid, kGateThreads, lds, st>>>(a);
-    else if (a.experts <= 256)
-        k_gate<16, kBalance><<<grid, kGateThreads, lds, st>>>(a);
-    else
-        k_gate<32, kBalance><<<grid, kGateThreads, lds, st>>>(a);
+    gate_form(a.tokens, a.experts, [&](auto lanes, auto slots) {
+        k_gate<decltype(lanes)::value, decltype(slots)::value, kBalance>
+            <<<grid, kGateThreads, lds, st>>>(a);
+    });
 }
 
-void launch_gate_backward(int grid, size_t lds, hipStream_t st, const GateArgs &a)
+void launch_gate_backward(int grid, hipStream_t st, const GateArgs &a)
 {
-    if (a.experts <= 64)
-        k_gate_backward<4><<<grid, kGateThreads, lds, st>>>(a);
-    else if (a.experts <= 128)
-        k_gate_backward<8><<<grid, kGateThreads, lds, st>>>(a);
-    else if (a.experts <= 256)
-        k_gate_backward<16><<<grid, kGateThreads, lds, st>>>(a);
-    else
-        k_gate_backward<32><<<grid, kGateThreads, lds, st>>>(a);
+    gate_form(a.tokens, a.experts, [&](auto lanes, auto slots) {
+        k_gate_backward<decltype(lanes)::value, decltype(slots)::value>
+            <<<grid, kGateThreads, 0, st>>>(a);
+    });
 }
 
 // ---- products -----------------------------------------------------------------
@@ -233,7 +247,11 @@ epdc_status epdc_gate_scratch_bytes(int32_t max_tokens, int32_t num_experts, siz
     if (max_tokens < 0 || num_experts < 1 || num_experts > kMaxExperts || !bytes)
         return fail(EPDC_ERR_INVALID_ARGS, "max_tokens >= 0, num_experts in [1, %d] and bytes "
                                            "are required", kMaxExperts);
-    *bytes = 256 + sizeof(float) * (size_t)gate_blocks(max_tokens, kGateMaxBlocks) *
+    // the most blocks a call of up to max_tokens tokens takes: a wave per token
+    // needs more of them than 16 lanes
+    const int small = max_tokens < kGateWaveTokens ? max_tokens : kGateWaveTokens;
+    const int a = gate_blocks(small, kGateMaxBlocks), b = gate_blocks(max_tokens, kGateMaxBlocks);
+    *bytes = 256 + sizeof(float) * (size_t)((a > b ? a : b) + kGateFan) *
                        (size_t)gate_partial_words(num_experts);
     return ok();
 }
@@ -267,7 +285,8 @@ epdc_status epdc_gate(const epdc_gate_args *args, void *stream, float *weights, 
         a.partial = reinterpret_cast<float *>(static_cast<uint8_t *>(scratch) + 256);
         const int grid = gate_blocks(a.tokens, kGateMaxBlocks);
         const size_t lds = sizeof(float) * ((size_t)a.experts + 1 +
-                                            kGateThreads / 64 * (size_t)a.experts + kGateTokens);
+                                            kGateThreads / 64 * (size_t)a.experts +
+                                            kGateThreads / gate_lanes(a.tokens));
         s = launch("k_gate", [&] { launch_gate<true>(grid, lds, st, a); });
     } else {
         s = launch("k_gate",
@@ -300,10 +319,8 @@ epdc_status epdc_gate_backward(const epdc_gate_args *args, void *stream, const i
     a.in_counts = counts;
     a.grad_losses = grad_losses;
     a.grad_logits = grad_logits;
-    const size_t lds = sizeof(float) * (size_t)a.experts;
     s = launch("k_gate_backward", [&] {
-        launch_gate_backward(gate_blocks(a.tokens, 1 << 20), lds, static_cast<hipStream_t>(stream),
-                             a);
+        launch_gate_backward(gate_blocks(a.tokens, 1 << 20), static_cast<hipStream_t>(stream), a);
     });
     return s == EPDC_SUCCESS ? ok() : s;
 }

@@ -2,11 +2,11 @@
 // per-expert counts, balance and z losses), its gradient, and combine's
 // gradient.
 //
-// Sixteen lanes own one token, four tokens to a wave: lane j of the group
-// holds elements 64 c + 4 j ... +3 of the row (16-byte loads), and every
-// reduction over a row is four DPP steps inside the 16 lanes, which cost no
-// LDS and serve four tokens at once.  The steps pair lanes symmetrically, so
-// that all 16 lanes end with the same bits.
+// A group of kLanes lanes owns one token: 16, four tokens to a wave, when there
+// are tokens enough to fill the chip, else the whole wave.  Every reduction over
+// a row is four DPP steps inside 16 lanes (and two row swaps for 64), which cost
+// no LDS; the steps pair lanes symmetrically, so that all lanes of the group end
+// with the same bits.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -16,8 +16,17 @@
 namespace epdc_layer {
 
 constexpr int kGateThreads = 512;
-constexpr int kGateTokens = kGateThreads / 16;  // of a block's pass
-constexpr int kGateMaxBlocks = 256;
+constexpr int kGateFan = 32;  // rows of partial sums one block adds
+constexpr int kGateMaxBlocks = 512;  // two of 8 waves per CU
+static_assert(kGateMaxBlocks <= kGateFan * kGateFan, "two levels of sums");
+// Up to this many tokens a whole wave takes one: with 16 lanes 4096 tokens are
+// only one wave per SIMD, and a wave's chain of top-k steps is the time.
+constexpr int kGateWaveTokens = 8192;
+
+__host__ __device__ inline int gate_lanes(int64_t tokens)
+{
+    return tokens <= kGateWaveTokens ? 64 : 16;
+}
 constexpr int kMaxTopk = 16;
 
 enum { kScoreSoftmax = 0, kScoreSigmoid = 1 };
@@ -31,8 +40,9 @@ struct GateArgs {
     const uint8_t *mask;
     float *weights;
     int32_t *indices;
-    // balance: counts [E+1], losses [2] and scratch (ticket, then one row of
-    // partials per block: E + 1 counts, E probability sums, the z sum)
+    // balance: counts [E+1], losses [2] and scratch (tickets, then a row of
+    // partials per block and per kGateFan blocks: E + 1 counts, E probability
+    // sums, the z sum)
     int32_t *counts;
     float *losses;
     uint32_t *ticket;
@@ -70,7 +80,46 @@ __device__ inline double dpp_d(double v)
 // lane ^ 1, lane ^ 2, then the mirrors inside 8 and inside 16 lanes
 constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kMirror8 = 0x141, kMirror16 = 0x140;
 
+// The other operand of a reduction across rows of 16 lanes (kRows 1: lane ^ 16,
+// 2: lane ^ 32): a swap of rows between two copies leaves in one of them the
+// lane's own value and in the other its partner's.
+template <int kRows>
+__device__ inline void row_swap(uint32_t v, uint32_t &a, uint32_t &b)
+{
+    const auto r = kRows == 1 ? __builtin_amdgcn_permlane16_swap(v, v, false, false)
+                              : __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    a = r[0];
+    b = r[1];
+}
+template <int kRows>
+__device__ inline void across(float v, float &a, float &b)
+{
+    uint32_t x, y;
+    row_swap<kRows>(__float_as_uint(v), x, y);
+    a = __uint_as_float(x);
+    b = __uint_as_float(y);
+}
+template <int kRows>
+__device__ inline void across(int v, int &a, int &b)
+{
+    uint32_t x, y;
+    row_swap<kRows>((uint32_t)v, x, y);
+    a = (int)x;
+    b = (int)y;
+}
+template <int kRows>
+__device__ inline void across(double v, double &a, double &b)
+{
+    const uint64_t u = (uint64_t)__double_as_longlong(v);
+    uint32_t lx, ly, hx, hy;
+    row_swap<kRows>((uint32_t)u, lx, ly);
+    row_swap<kRows>((uint32_t)(u >> 32), hx, hy);
+    a = __longlong_as_double((long long)(((uint64_t)hx << 32) | lx));
+    b = __longlong_as_double((long long)(((uint64_t)hy << 32) | ly));
+}
+
 #define EPDC_GROUP_REDUCE(name, T, dpp, expr)      \
+    template <int kLanes>                          \
     __device__ inline T name(T a)                  \
     {                                              \
         T b = dpp<kXor1>(a);                       \
@@ -80,13 +129,20 @@ constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kMirror8 = 0x141, kMirror16 = 0x140;
         b = dpp<kMirror8>(a);                      \
         a = expr;                                  \
         b = dpp<kMirror16>(a);                     \
-        return expr;                               \
+        a = expr;                                  \
+        if constexpr (kLanes == 64) {              \
+            across<1>(a, a, b);                    \
+            a = expr;                              \
+            across<2>(a, a, b);                    \
+            a = expr;                              \
+        }                                          \
+        return a;                                  \
     }
-EPDC_GROUP_REDUCE(group_max, float, dpp_f, (a > b ? a : b))
+EPDC_GROUP_REDUCE(group_max, float, dpp_f, fmaxf(a, b))
 EPDC_GROUP_REDUCE(group_sum, float, dpp_f, (a + b))
 EPDC_GROUP_REDUCE(group_min, int, dpp_i, (a < b ? a : b))
 EPDC_GROUP_REDUCE(group_or, int, dpp_i, (a | b))
-EPDC_GROUP_REDUCE(group_max, double, dpp_d, (a > b ? a : b))
+EPDC_GROUP_REDUCE(group_max, double, dpp_d, fmax(a, b))
 EPDC_GROUP_REDUCE(group_sum, double, dpp_d, (a + b))
 #undef EPDC_GROUP_REDUCE
 
@@ -97,50 +153,56 @@ __device__ inline float lowest<float>() { return -__builtin_inff(); }
 template <>
 __device__ inline double lowest<double>() { return -__builtin_inf(); }
 
-// Element of this lane's slot v: 64 (v / 4) + 4 j + v % 4.
-__device__ inline int slot_expert(int v, int j) { return (v >> 2) * 64 + j * 4 + (v & 3); }
+// Element of lane j's slot v: a lane holds kW consecutive elements of every
+// kLanes * kW (16-byte loads of fp32 where kW is 4).
+template <int kLanes, int kV>
+__device__ inline int slot_expert(int v, int j)
+{
+    constexpr int kW = kV < 4 ? kV : 4;
+    return v / kW * (kLanes * kW) + j * kW + v % kW;
+}
 
-template <int kV>
+__device__ inline float logit_at(const GateArgs &a, size_t at)
+{
+    return a.bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t *>(a.logits)[at] << 16)
+                  : static_cast<const float *>(a.logits)[at];
+}
+
+template <int kLanes, int kV>
 __device__ inline void load_logits(const GateArgs &a, int64_t token, int j, float (&l)[kV])
 {
-    const float none = lowest<float>();
+    constexpr int kW = kV < 4 ? kV : 4;
     const int E = a.experts;
-    const bool wide = (E & 3) == 0;  // rows of whole 4-element vectors stay aligned
+    const bool wide = kW == 4 && (E & 3) == 0;  // rows of whole vectors stay aligned
     const size_t row = (size_t)token * E;
 #pragma unroll
-    for (int c = 0; c < kV / 4; ++c) {
-        const int e = c * 64 + j * 4;
+    for (int c = 0; c < kV / kW; ++c) {
+        const int e = slot_expert<kLanes, kV>(c * kW, j);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            l[c * 4 + i] = none;
-        if (a.bf16) {
-            const uint16_t *p = static_cast<const uint16_t *>(a.logits) + row + e;
-            if (wide && e < E) {
-                const uint2 w = *reinterpret_cast<const uint2 *>(p);
-                l[c * 4 + 0] = __uint_as_float(w.x << 16);
-                l[c * 4 + 1] = __uint_as_float(w.x & 0xFFFF0000u);
-                l[c * 4 + 2] = __uint_as_float(w.y << 16);
-                l[c * 4 + 3] = __uint_as_float(w.y & 0xFFFF0000u);
+        for (int i = 0; i < kW; ++i)
+            l[c * kW + i] = lowest<float>();
+        if (wide) {
+            if (e >= E)
+                continue;
+            if (a.bf16) {
+                const uint2 w = *reinterpret_cast<const uint2 *>(
+                    static_cast<const uint16_t *>(a.logits) + row + e);
+                const uint32_t u[4] = {w.x << 16, w.x & 0xFFFF0000u, w.y << 16, w.y & 0xFFFF0000u};
+#pragma unroll
+                for (int i = 0; i < kW; ++i)
+                    l[c * kW + i] = __uint_as_float(u[i]);
             } else {
+                const f32x4 w = *reinterpret_cast<const f32x4 *>(
+                    static_cast<const float *>(a.logits) + row + e);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (e + i < E)
-                        l[c * 4 + i] = __uint_as_float((uint32_t)p[i] << 16);
+                for (int i = 0; i < kW; ++i)
+                    l[c * kW + i] = w[i];
             }
         } else {
-            const float *p = static_cast<const float *>(a.logits) + row + e;
-            if (wide && e < E) {
-                const float4 w = *reinterpret_cast<const float4 *>(p);
-                l[c * 4 + 0] = w.x;
-                l[c * 4 + 1] = w.y;
-                l[c * 4 + 2] = w.z;
-                l[c * 4 + 3] = w.w;
-            } else {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (e + i < E)
-                        l[c * 4 + i] = p[i];
-            }
+            for (int i = 0; i < kW; ++i)
+                if (e + i < E)
+                    l[c * kW + i] = logit_at(a, row + e + i);
         }
     }
 }
@@ -148,51 +210,66 @@ __device__ inline void load_logits(const GateArgs &a, int64_t token, int j, floa
 // What a token's logits make of it.
 enum { kTokenOut = 0, kTokenIn = 1, kTokenBad = 2 };
 
-template <int kV>
-__device__ inline int classify(const GateArgs &a, int64_t token, const float (&l)[kV], float &m)
+template <int kLanes, int kV>
+__device__ inline int classify(const GateArgs &a, bool masked, const float (&l)[kV], float &m)
 {
     float top = lowest<float>();
     int bad = 0;
 #pragma unroll
     for (int v = 0; v < kV; ++v) {
         bad |= !(l[v] < __builtin_inff());  // NaN or +inf
-        top = l[v] > top ? l[v] : top;
+        top = fmaxf(top, l[v]);
     }
-    m = group_max(top);
-    bad = group_or(bad);
-    if (a.mask && a.mask[token] == 0)
+    m = group_max<kLanes>(top);
+    bad = group_or<kLanes>(bad);
+    if (masked)
         return kTokenOut;
     if (bad)
         return kTokenBad;
     return m == lowest<float>() ? kTokenOut : kTokenIn;
 }
 
-// The largest key of the group and its expert (lowest index among equals);
-// expert -1 when nothing is left.
-template <int kV, typename T>
-__device__ inline void group_top(const T (&key)[kV], int j, T &best, int &expert)
+// Take the group's largest key and its expert (lowest index among equals) out
+// of the keys; expert -1 when nothing is left.
+template <int kLanes, int kV, typename T>
+__device__ inline void take_top(T (&key)[kV], int j, T &best, int &expert)
 {
     T top = lowest<T>();
-    int at = INT_MAX;
 #pragma unroll
     for (int v = 0; v < kV; ++v)
-        if (key[v] > top) {  // slots ascend in expert order
-            top = key[v];
-            at = slot_expert(v, j);
-        }
-    best = group_max(top);
-    expert = group_min(top == best ? at : INT_MAX);
-    if (expert == INT_MAX)
+        top = key[v] > top ? key[v] : top;
+    best = group_max<kLanes>(top);
+    int at = INT_MAX;
+#pragma unroll
+    for (int v = kV - 1; v >= 0; --v)
+        at = key[v] == best ? slot_expert<kLanes, kV>(v, j) : at;
+    expert = group_min<kLanes>(at);
+    // this lane's slot of that expert, if it has it
+    const int mine = expert == at ? at : -1;
+#pragma unroll
+    for (int v = 0; v < kV; ++v)
+        key[v] = mine == slot_expert<kLanes, kV>(v, j) ? lowest<T>() : key[v];
+    if (best == lowest<T>())
         expert = -1;
 }
 
-template <int kV, typename T>
-__device__ inline void drop(T (&key)[kV], int j, int expert)
+// exp in fp32 to about an ulp in six instructions: the hardware's 2^x of
+// x log2(e), and the part of that product that fp32 does not hold as a factor.
+// Arguments below -150 give 0.
+__device__ inline float exp_near(float x)
 {
-#pragma unroll
-    for (int v = 0; v < kV; ++v)
-        if (slot_expert(v, j) == expert)
-            key[v] = lowest<T>();
+    x = fmaxf(x, -150.0f);
+    const float h = x * 1.44269502f;
+    const float r = __builtin_fmaf(x, 1.92596303e-8f, __builtin_fmaf(x, 1.44269502f, -h));
+    const float p = __builtin_amdgcn_exp2f(h);
+    return __builtin_fmaf(p, r * 0.693147181f, p);
+}
+
+// 1 / x to about an ulp: the hardware's reciprocal and one Newton step
+__device__ inline float recip_near(float x)
+{
+    const float r = __builtin_amdgcn_rcpf(x);
+    return __builtin_fmaf(__builtin_fmaf(-x, r, 1.0f), r, r);
 }
 
 // log of a chosen score up to a constant of the row, without underflow:
@@ -204,7 +281,11 @@ __device__ inline float log_score(int score, float l)
     return fminf(l, 0.0f) - log1pf(expf(-fabsf(l)));
 }
 
-__device__ inline float sigmoid(float l) { return 1.0f / (1.0f + expf(-l)); }
+// exp(-l) is kept finite: past 80 the score is 0 to within e^-80
+__device__ inline float sigmoid(float l)
+{
+    return recip_near(1.0f + exp_near(fminf(-l, 80.0f)));
+}
 
 // Keys with a bias, s + b, are rounded sums of rounded scores.  In fp32 s is
 // off by a few ulp of at most 1 and the sum by half an ulp of the key, so two
@@ -224,85 +305,83 @@ __device__ inline float load_agent(const float *p)
 // has choice k).  With a balance, each lane sums its experts' probabilities
 // over its tokens; waves, then blocks, are added in a fixed order, the blocks
 // by the last one to finish.
-template <int kV, bool kBalance>
-__global__ __launch_bounds__(kGateThreads) void k_gate(const GateArgs a)
+template <int kLanes, int kV, bool kBalance>
+__global__ __launch_bounds__(kGateThreads, kV < 32 ? 4 : 2) void k_gate(const GateArgs a)
 {
-    constexpr int kWaves = kGateThreads / 64;
+    constexpr int kWaves = kGateThreads / 64, kTokens = kGateThreads / kLanes;
     extern __shared__ __align__(16) uint8_t dyn[];
     int *cnt = reinterpret_cast<int *>(dyn);                       // [E + 1]
     float *sum = reinterpret_cast<float *>(dyn) + a.experts + 1;   // [waves][E]
-    float *zsum = sum + kWaves * a.experts;                        // [kGateTokens]
+    float *zsum = sum + kWaves * a.experts;                        // [kTokens]
     __shared__ int last;
 
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid / 64, j = tid & 15;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid / 64, j = tid & (kLanes - 1);
     const int E = a.experts, K = a.topk;
     if (kBalance) {
         for (int e = tid; e <= E; e += kGateThreads)
             cnt[e] = 0;
         __syncthreads();
     }
-    float bias[kV], prob[kV], z = 0.0f;
+    float prob[kV], z = 0.0f;
 #pragma unroll
-    for (int v = 0; v < kV; ++v) {
-        const int e = slot_expert(v, j);
-        bias[v] = a.bias && e < E ? a.bias[e] : 0.0f;
+    for (int v = 0; v < kV; ++v)
         prob[v] = 0.0f;
-    }
     const bool softmax = a.score == kScoreSoftmax;
     const bool scores = kBalance || a.bias != nullptr || (softmax && !a.renorm);
 
-    for (int64_t t0 = (int64_t)blockIdx.x * kGateTokens; t0 < a.tokens;
-         t0 += (int64_t)gridDim.x * kGateTokens) {
-        const int64_t t = t0 + tid / 16;
+    for (int64_t t0 = (int64_t)blockIdx.x * kTokens; t0 < a.tokens;
+         t0 += (int64_t)gridDim.x * kTokens) {
+        const int64_t t = t0 + tid / kLanes;
         if (t >= a.tokens)
             continue;
-        float l[kV], s[kV], m;
-        load_logits<kV>(a, t, j, l);
-        const int kind = classify<kV>(a, t, l, m);
+        float l[kV], m;
+        load_logits<kLanes, kV>(a, t, j, l);
+        const int kind = classify<kLanes, kV>(a, a.mask && a.mask[t] == 0, l, m);
         int chosen = -1;      // lane k: choice k
-        float total = 1.0f, lse = 0.0f;
+        float inv = 1.0f, lse = 0.0f;
         if (kind == kTokenIn) {
+            float key[kV];
+#pragma unroll
+            for (int v = 0; v < kV; ++v)
+                key[v] = l[v];
             if (scores) {
-                float part = 0.0f, esum = 0.0f;
+                float s[kV], part = 0.0f, esum = 0.0f;
 #pragma unroll
                 for (int v = 0; v < kV; ++v) {
-                    const float x = expf(l[v] - m);
+                    const float x = softmax || kBalance ? exp_near(l[v] - m) : 0.0f;
                     s[v] = softmax ? x : sigmoid(l[v]);
                     part += s[v];
                     esum += x;
                 }
-                total = group_sum(part);
+                if (softmax || kBalance)
+                    inv = 1.0f / group_sum<kLanes>(part);
                 if (kBalance)
-                    lse = m + logf(group_sum(esum));
-                const float r = 1.0f / total;
+                    lse = m + logf(softmax ? 1.0f / inv : group_sum<kLanes>(esum));
 #pragma unroll
                 for (int v = 0; v < kV; ++v) {
                     if (kBalance)
-                        prob[v] += s[v] * r;
-                    if (softmax)
-                        s[v] *= r;
+                        prob[v] += s[v] * inv;
+                    if (a.bias) {
+                        const int e = slot_expert<kLanes, kV>(v, j);
+                        if (l[v] > lowest<float>())
+                            key[v] = (softmax ? s[v] * inv : s[v]) + a.bias[e];
+                    }
                 }
             }
-            float key[kV];
-#pragma unroll
-            for (int v = 0; v < kV; ++v)
-                key[v] = a.bias && l[v] > lowest<float>() ? s[v] + bias[v] : l[v];
             float before = __builtin_inff();
             bool close = false;
-            for (int k = 0; k <= K; ++k) {  // with a bias one more, to see the border
-                if (k == K && !a.bias)
-                    break;
+            const int rounds = a.bias ? K + 1 : K;  // with a bias one more, to see the border
+            for (int k = 0; k < rounds; ++k) {
                 float best;
                 int e;
-                group_top<kV>(key, j, best, e);
-                if (a.bias && e >= 0)
+                take_top<kLanes, kV>(key, j, best, e);
+                if (e >= 0)
                     close |= before - best <= key_slack(best);
                 before = best;
                 if (k < K && j == k)
                     chosen = e;
-                drop<kV>(key, j, e);
             }
-            if (close) {  // the same in 64 bits
+            if (close && a.bias) {  // the same in 64 bits
                 double key64[kV], part = 0.0, sum64 = 1.0;
 #pragma unroll
                 for (int v = 0; v < kV; ++v) {
@@ -311,35 +390,33 @@ __global__ __launch_bounds__(kGateThreads) void k_gate(const GateArgs a)
                     part += key64[v];
                 }
                 if (softmax)
-                    sum64 = group_sum(part);
+                    sum64 = group_sum<kLanes>(part);
 #pragma unroll
                 for (int v = 0; v < kV; ++v)
-                    key64[v] = l[v] > lowest<float>() ? key64[v] / sum64 + (double)bias[v]
-                                                      : lowest<double>();
+                    key64[v] = l[v] > lowest<float>()
+                                   ? key64[v] / sum64 +
+                                         (double)a.bias[slot_expert<kLanes, kV>(v, j)]
+                                   : lowest<double>();
                 for (int k = 0; k < K; ++k) {
                     double best;
                     int e;
-                    group_top<kV>(key64, j, best, e);
+                    take_top<kLanes, kV>(key64, j, best, e);
                     if (j == k)
                         chosen = e;
-                    drop<kV>(key64, j, e);
                 }
             }
         }
         const bool have = chosen >= 0;
         float x = lowest<float>(), w = 0.0f;
-        if (have) {
-            const size_t at = (size_t)t * E + chosen;
-            x = a.bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t *>(a.logits)[at] << 16)
-                       : static_cast<const float *>(a.logits)[at];
-        }
+        if (have)
+            x = logit_at(a, (size_t)t * E + chosen);
         if (a.renorm) {
             const float ls = have ? log_score(a.score, x) : lowest<float>();
-            const float top = group_max(ls);
+            const float top = group_max<kLanes>(ls);
             const float p = have ? expf(ls - top) : 0.0f;
-            w = a.scale * (p / group_sum(p));
+            w = a.scale * (p / group_sum<kLanes>(p));
         } else if (have) {
-            w = a.scale * (softmax ? expf(x - m) / total : sigmoid(x));
+            w = a.scale * (softmax ? expf(x - m) * inv : 1.0f / (1.0f + expf(-x)));
         }
         if (!have)
             w = kind == kTokenBad ? __builtin_nanf("") : 0.0f;
@@ -361,18 +438,20 @@ __global__ __launch_bounds__(kGateThreads) void k_gate(const GateArgs a)
     if (!kBalance)
         return;
 
-    // the wave's four groups, then the block's waves
+    // the wave's groups, then the block's waves
 #pragma unroll
     for (int v = 0; v < kV; ++v) {
         float p = prob[v];
-        p += __shfl_xor(p, 16, 64);
-        p += __shfl_xor(p, 32, 64);
-        const int e = slot_expert(v, j);
-        if (lane < 16 && e < E)
+        if (kLanes == 16) {
+            p += __shfl_xor(p, 16, 64);
+            p += __shfl_xor(p, 32, 64);
+        }
+        const int e = slot_expert<kLanes, kV>(v, j);
+        if (lane < kLanes && e < E)
             sum[wave * E + e] = p;
     }
     if (j == 0)
-        zsum[tid / 16] = z;
+        zsum[tid / kLanes] = z;
     __syncthreads();
     const int words = gate_partial_words(E);
     float *mine = a.partial + (size_t)blockIdx.x * words;
@@ -386,36 +465,61 @@ __global__ __launch_bounds__(kGateThreads) void k_gate(const GateArgs a)
     }
     if (tid == 0) {
         float zz = 0.0f;
-        for (int i = 0; i < kGateTokens; ++i)
+        for (int i = 0; i < kTokens; ++i)
             zz += zsum[i];
         store_agent(mine + E, __int_as_float(cnt[E]));
         store_agent(mine + 2 * E + 1, zz);
     }
-    // every store of the block is at the device's point of coherence before
-    // the ticket is taken
-    __builtin_amdgcn_s_waitcnt(0);
-    __syncthreads();
-    if (tid == 0)
-        last = __hip_atomic_fetch_add(a.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
-               gridDim.x - 1;
-    __syncthreads();
-    if (!last)
-        return;
-    const int nb = gridDim.x;
-    for (int i = tid; i <= E; i += kGateThreads) {  // counts, and the token count
+    // Every block's stores are at the device's point of coherence before it takes
+    // a ticket.  The last of each kGateFan blocks adds their rows, the last of
+    // those the sums: with one level its last block alone read 256 rows, 40 us more.
+    const auto done = [&](uint32_t *ticket, uint32_t count) {
+        __builtin_amdgcn_s_waitcnt(0);
+        __syncthreads();
+        if (tid == 0) {
+            last = __hip_atomic_fetch_add(ticket, 1u, __ATOMIC_RELAXED,
+                                          __HIP_MEMORY_SCOPE_AGENT) == count - 1;
+            if (last)  // ready for the next call, which the stream orders after this one
+                __hip_atomic_store(ticket, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+        __syncthreads();
+        return last != 0;
+    };
+    const auto add_rows = [&](const float *from, int rows, int i) {  // word i
         int c = 0;
-#pragma unroll 16
-        for (int b = 0; b < nb; ++b)
-            c += __float_as_int(load_agent(a.partial + (size_t)b * words + i));
-        cnt[i] = c;
-        a.counts[i] = c;
-    }
-    for (int i = tid; i <= E; i += kGateThreads) {  // probabilities, and the z sum
         float p = 0.0f;
-#pragma unroll 16
-        for (int b = 0; b < nb; ++b)
-            p += load_agent(a.partial + (size_t)b * words + E + 1 + i);
-        sum[i] = p;
+        if (i <= E) {
+#pragma unroll
+            for (int b = 0; b < kGateFan; ++b)
+                c += b < rows ? __float_as_int(load_agent(from + (size_t)b * words + i)) : 0;
+            return __int_as_float(c);
+        }
+#pragma unroll
+        for (int b = 0; b < kGateFan; ++b)
+            p += b < rows ? load_agent(from + (size_t)b * words + i) : 0.0f;
+        return p;
+    };
+    const int nb = gridDim.x, groups = (nb + kGateFan - 1) / kGateFan;
+    const int group = blockIdx.x / kGateFan, first = group * kGateFan;
+    const int in_group = nb - first < kGateFan ? nb - first : kGateFan;
+    if (!done(a.ticket + 1 + group, in_group))
+        return;
+    float *tops = a.partial + (size_t)nb * words;
+    if (groups > 1) {
+        for (int i = tid; i < words; i += kGateThreads)
+            store_agent(tops + (size_t)group * words + i,
+                        add_rows(a.partial + (size_t)first * words, in_group, i));
+        if (!done(a.ticket, groups))
+            return;
+    }
+    for (int i = tid; i < words; i += kGateThreads) {
+        const float v = groups > 1 ? add_rows(tops, groups, i) : add_rows(a.partial, nb, i);
+        if (i <= E) {
+            cnt[i] = __float_as_int(v);
+            a.counts[i] = __float_as_int(v);
+        } else {
+            sum[i - E - 1] = v;
+        }
     }
     __syncthreads();
     if (wave == 0) {
@@ -429,18 +533,17 @@ __global__ __launch_bounds__(kGateThreads) void k_gate(const GateArgs a)
         if (lane == 0) {
             a.losses[0] = (float)E * (d / n / (n * (float)K));
             a.losses[1] = sum[E] / n;
-            *a.ticket = 0;  // ready for the next call, which the stream orders after this one
         }
     }
 }
 
 // One pass over the logits: with p the scores' softmax (sigmoid: s / sum s),
 //   d/dl_j of scale * r(chosen)  and of  E/n sum_e f_e p_e  and of  lse^2 / n.
-template <int kV>
-__global__ __launch_bounds__(kGateThreads) void k_gate_backward(const GateArgs a)
+template <int kLanes, int kV>
+__global__ __launch_bounds__(kGateThreads, kV < 32 ? 4 : 2) void k_gate_backward(const GateArgs a)
 {
-    extern __shared__ __align__(16) float f[];  // [E]: an expert's share of the choices
-    const int tid = threadIdx.x, j = tid & 15;
+    constexpr int kTokens = kGateThreads / kLanes, kW = kV < 4 ? kV : 4;
+    const int tid = threadIdx.x, j = tid & (kLanes - 1);
     const int E = a.experts, K = a.topk;
     const bool softmax = a.score == kScoreSoftmax, balance = a.in_counts != nullptr;
     float gb = 0.0f, gz = 0.0f;
@@ -450,25 +553,32 @@ __global__ __launch_bounds__(kGateThreads) void k_gate_backward(const GateArgs a
         share[v] = 0.0f;
     if (balance) {
         const int n = a.in_counts[E] > 1 ? a.in_counts[E] : 1;
-        for (int e = tid; e < E; e += kGateThreads)
-            f[e] = (float)a.in_counts[e] / ((float)n * (float)K);
+        const float per = 1.0f / ((float)n * (float)K);
         gb = a.grad_losses[0] * (float)E / (float)n;
         gz = a.grad_losses[1] * 2.0f / (float)n;
-        __syncthreads();
 #pragma unroll
         for (int v = 0; v < kV; ++v) {
-            const int e = slot_expert(v, j);
-            share[v] = e < E ? f[e] : 0.0f;
+            const int e = slot_expert<kLanes, kV>(v, j);
+            share[v] = e < E ? (float)a.in_counts[e] * per : 0.0f;
         }
     }
-    for (int64_t t0 = (int64_t)blockIdx.x * kGateTokens; t0 < a.tokens;
-         t0 += (int64_t)gridDim.x * kGateTokens) {
-        const int64_t t = t0 + tid / 16;
+    for (int64_t t0 = (int64_t)blockIdx.x * kTokens; t0 < a.tokens;
+         t0 += (int64_t)gridDim.x * kTokens) {
+        const int64_t t = t0 + tid / kLanes;
         if (t >= a.tokens)
             continue;
         float l[kV], m;
-        load_logits<kV>(a, t, j, l);
-        const int kind = classify<kV>(a, t, l, m);
+        load_logits<kLanes, kV>(a, t, j, l);
+        // the chosen: lane k holds choice k
+        int e = -1;
+        float g = 0.0f;
+        if (j < K && a.grad_weights) {
+            e = a.in_indices[t * K + j];
+            e = e >= 0 && e < E ? e : -1;
+            if (e >= 0)
+                g = a.grad_weights[t * K + j] * a.scale;
+        }
+        const int kind = classify<kLanes, kV>(a, a.mask && a.mask[t] == 0, l, m);
         float d[kV];
 #pragma unroll
         for (int v = 0; v < kV; ++v)
@@ -478,43 +588,30 @@ __global__ __launch_bounds__(kGateThreads) void k_gate_backward(const GateArgs a
             float x[kV], s[kV], xs = 0.0f, ss = 0.0f, fp = 0.0f;
 #pragma unroll
             for (int v = 0; v < kV; ++v) {
-                x[v] = expf(l[v] - m);
+                x[v] = exp_near(l[v] - m);
                 xs += x[v];
                 s[v] = softmax ? x[v] : sigmoid(l[v]);
                 ss += s[v];
                 fp += share[v] * s[v];
             }
-            xs = group_sum(xs);
-            ss = group_sum(ss);
-            fp = group_sum(fp) / ss;
-            // the chosen: lane k holds choice k, its gradient and its share r
-            int e = -1;
-            float g = 0.0f, le = lowest<float>();
-            if (j < K && a.grad_weights) {
-                e = a.in_indices[t * K + j];
-                e = e >= 0 && e < E ? e : -1;
-                if (e >= 0) {
-                    g = a.grad_weights[t * K + j] * a.scale;
-                    const size_t at = (size_t)t * E + e;
-                    le = a.bf16 ? __uint_as_float(
-                                      (uint32_t)static_cast<const uint16_t *>(a.logits)[at] << 16)
-                                : static_cast<const float *>(a.logits)[at];
-                }
-            }
+            xs = group_sum<kLanes>(xs);
+            ss = softmax ? xs : group_sum<kLanes>(ss);
+            fp = group_sum<kLanes>(fp) / ss;
+            const float le = e >= 0 ? logit_at(a, (size_t)t * E + e) : lowest<float>();
             float r = 0.0f, dc = 0.0f, all = 0.0f;  // all: taken from every p of a softmax
             if (a.renorm) {
                 const float ls = e >= 0 ? log_score(a.score, le) : lowest<float>();
-                const float top = group_max(ls);
+                const float top = group_max<kLanes>(ls);
                 r = e >= 0 ? expf(ls - top) : 0.0f;
-                const float rs = group_sum(r);
+                const float rs = group_sum<kLanes>(r);
                 r = rs > 0.0f ? r / rs : 0.0f;
-                dc = r * (g - group_sum(g * r));
+                dc = r * (g - group_sum<kLanes>(g * r));
                 if (!softmax)
                     dc *= e >= 0 ? 1.0f - sigmoid(le) : 0.0f;
             } else if (softmax) {
                 r = e >= 0 ? expf(le - m) / xs : 0.0f;
                 dc = g * r;
-                all = group_sum(dc);
+                all = group_sum<kLanes>(dc);
             } else {
                 r = e >= 0 ? sigmoid(le) : 0.0f;
                 dc = g * r * (1.0f - r);
@@ -528,45 +625,44 @@ __global__ __launch_bounds__(kGateThreads) void k_gate_backward(const GateArgs a
                     b *= 1.0f - s[v];
                 d[v] = b + (gz * lse - all) * q;
             }
-            for (int k = 0; k < K; ++k) {
-                const int ek = __shfl(e, k, 16);
-                const float dk = __shfl(dc, k, 16);
+            if (a.grad_weights)
+                for (int k = 0; k < K; ++k) {
+                    const int ek = __shfl(e, k, kLanes);
+                    const float dk = __shfl(dc, k, kLanes);
 #pragma unroll
-                for (int v = 0; v < kV; ++v)
-                    d[v] += slot_expert(v, j) == ek ? dk : 0.0f;
-            }
+                    for (int v = 0; v < kV; ++v)
+                        d[v] += slot_expert<kLanes, kV>(v, j) == ek ? dk : 0.0f;
+                }
 #pragma unroll
             for (int v = 0; v < kV; ++v)
                 if (l[v] == lowest<float>())
                     d[v] = 0.0f;
         }
         const size_t row = (size_t)t * E;
-        const bool wide = (E & 3) == 0;
+        const bool wide = kW == 4 && (E & 3) == 0;
 #pragma unroll
-        for (int c = 0; c < kV / 4; ++c) {
-            const int e = c * 64 + j * 4;
-            if (a.bf16) {
-                __bf16 *p = static_cast<__bf16 *>(a.grad_logits) + row + e;
-                if (wide && e < E) {
-                    *reinterpret_cast<bf16x4 *>(p) =
-                        to_bf16(f32x4{d[c * 4], d[c * 4 + 1], d[c * 4 + 2], d[c * 4 + 3]});
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (e + i < E)
-                            p[i] = (__bf16)d[c * 4 + i];
-                }
+        for (int c = 0; c < kV / kW; ++c) {
+            const int at = slot_expert<kLanes, kV>(c * kW, j);
+            if (wide) {
+                if (at >= E)
+                    continue;
+                const f32x4 o{d[c * kW], d[c * kW + 1 % kW], d[c * kW + 2 % kW],
+                              d[c * kW + 3 % kW]};
+                if (a.bf16)
+                    *reinterpret_cast<bf16x4 *>(static_cast<__bf16 *>(a.grad_logits) + row + at) =
+                        to_bf16(o);
+                else
+                    *reinterpret_cast<f32x4 *>(static_cast<float *>(a.grad_logits) + row + at) = o;
             } else {
-                float *p = static_cast<float *>(a.grad_logits) + row + e;
-                if (wide && e < E) {
-                    *reinterpret_cast<f32x4 *>(p) =
-                        f32x4{d[c * 4], d[c * 4 + 1], d[c * 4 + 2], d[c * 4 + 3]};
-                } else {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (e + i < E)
-                            p[i] = d[c * 4 + i];
-                }
+                for (int i = 0; i < kW; ++i)
+                    if (at + i < E) {
+                        if (a.bf16)
+                            static_cast<__bf16 *>(a.grad_logits)[row + at + i] =
+                                (__bf16)d[c * kW + i];
+                        else
+                            static_cast<float *>(a.grad_logits)[row + at + i] = d[c * kW + i];
+                    }
             }
         }
     }
