@@ -57,6 +57,13 @@ int gate_blocks(int64_t tokens, int limit)
     return (int)(b < 1 ? 1 : (b < limit ? b : limit));
 }
 
+// Blocks of a balance: in small batches half as many, whose sums take half as
+// long to add (4093 x 128: 17.9 us for the forward, with 512 blocks 18.9).
+int balance_blocks(int64_t tokens)
+{
+    return gate_blocks(tokens, tokens <= kGateWaveTokens ? kGateMaxBlocks / 2 : kGateMaxBlocks);
+}
+
 epdc_status check_gate(const epdc_gate_args *g)
 {
     if (!g)
@@ -250,8 +257,8 @@ epdc_status epdc_gate_scratch_bytes(int32_t max_tokens, int32_t num_experts, siz
     // the most blocks a call of up to max_tokens tokens takes: a wave per token
     // needs more of them than 16 lanes
     const int small = max_tokens < kGateWaveTokens ? max_tokens : kGateWaveTokens;
-    const int a = gate_blocks(small, kGateMaxBlocks), b = gate_blocks(max_tokens, kGateMaxBlocks);
-    *bytes = 256 + sizeof(float) * (size_t)((a > b ? a : b) + kGateFan) *
+    const int a = balance_blocks(small), b = balance_blocks(max_tokens);
+    *bytes = 256 + sizeof(float) * (size_t)((a > b ? a : b) + kGateMaxFan) *
                        (size_t)gate_partial_words(num_experts);
     return ok();
 }
@@ -283,7 +290,7 @@ epdc_status epdc_gate(const epdc_gate_args *args, void *stream, float *weights, 
     if (balance) {
         a.ticket = static_cast<uint32_t *>(scratch);
         a.partial = reinterpret_cast<float *>(static_cast<uint8_t *>(scratch) + 256);
-        const int grid = gate_blocks(a.tokens, kGateMaxBlocks);
+        const int grid = balance_blocks(a.tokens);
         const size_t lds = sizeof(float) * ((size_t)a.experts + 1 +
                                             kGateThreads / 64 * (size_t)a.experts +
                                             kGateThreads / gate_lanes(a.tokens));

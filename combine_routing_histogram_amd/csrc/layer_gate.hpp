@@ -16,9 +16,12 @@
 namespace epdc_layer {
 
 constexpr int kGateThreads = 512;
-constexpr int kGateFan = 32;  // rows of partial sums one block adds
 constexpr int kGateMaxBlocks = 512;  // two of 8 waves per CU
-static_assert(kGateMaxBlocks <= kGateFan * kGateFan, "two levels of sums");
+constexpr int kGateMaxFan = 32;
+
+// Rows of partial sums one block adds; two levels of them hold every block.
+__host__ __device__ inline int gate_fan(int blocks) { return blocks <= 256 ? 16 : kGateMaxFan; }
+static_assert(kGateMaxBlocks <= kGateMaxFan * kGateMaxFan, "two levels of sums");
 // Up to this many tokens a whole wave takes one: with 16 lanes 4096 tokens are
 // only one wave per SIMD, and a wave's chain of top-k steps is the time.
 constexpr int kGateWaveTokens = 8192;
@@ -41,8 +44,7 @@ struct GateArgs {
     float *weights;
     int32_t *indices;
     // balance: counts [E+1], losses [2] and scratch (tickets, then a row of
-    // partials per block and per kGateFan blocks: E + 1 counts, E probability
-    // sums, the z sum)
+    // partials per block and per fan of blocks)
     int32_t *counts;
     float *losses;
     uint32_t *ticket;
@@ -296,9 +298,91 @@ __device__ inline void store_agent(float *p, float v)
 {
     __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
-__device__ inline float load_agent(const float *p)
+
+// exp in 64 bits for x <= 0 or so, rolled up: it is hardly ever called, and the
+// library's, inlined, fills the scalar registers of the whole kernel with its
+// constants.  x = n ln 2 + r, and the series of e^r to r^14 / 14! (|r| < 0.35).
+__device__ inline double exp_rolled(double x)
 {
-    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    x = x < -800.0 ? -800.0 : (x > 700.0 ? 700.0 : x);
+    const double n = rint(x * 1.4426950408889634);
+    // ln 2 in two parts, the first with zeros enough that n times it is exact
+    const double r = fma(n, -1.9082149292705877e-10, fma(n, -0.6931471803691238, x));
+    double p = 1.0, k = 14.0;
+#pragma unroll 1
+    for (; k > 0.5; k -= 1.0)
+        p = fma(p * r, 1.0 / k, 1.0);
+    return ldexp(p, (int)n);
+}
+
+// The key of expert e in 64 bits; -inf if it is unavailable.
+__device__ inline double key64(const GateArgs &a, int64_t t, int e, double m, double inv_sum)
+{
+    const double l = (double)logit_at(a, (size_t)t * a.experts + e);
+    if (!(l > lowest<double>()))
+        return lowest<double>();
+    const double x = exp_rolled(a.score == kScoreSoftmax ? l - m : -l);
+    return (a.score == kScoreSoftmax ? x * inv_sum : 1.0 / (1.0 + x)) + (double)a.bias[e];
+}
+
+// The choice in 64 bits, for a token whose keys fp32 cannot put in order.
+// `cand`: its first fp32 candidates, one per lane, which hold the true choice
+// unless `more` follow as closely (equal logits and biases, say); then every
+// expert is compared, key by key, without any array of keys: this code must not
+// cost the common path registers.
+template <int kLanes>
+__device__ inline int choose64(const GateArgs &a, int64_t t, int j, float m, int cand, bool more)
+{
+    double inv = 1.0;
+    if (a.score == kScoreSoftmax) {
+        double part = 0.0;
+#pragma unroll 1
+        for (int e = j; e < a.experts; e += kLanes)
+            part += exp_rolled((double)logit_at(a, (size_t)t * a.experts + e) - (double)m);
+        inv = 1.0 / group_sum<kLanes>(part);
+    }
+    int chosen = -1;
+    if (!more) {
+        const double key = cand >= 0 ? key64(a, t, cand, m, inv) : lowest<double>();
+        int rank = cand >= 0 ? 0 : -1;
+#pragma unroll 1
+        for (int i = 0; i < kMaxTopk; ++i) {
+            const double k2 = __shfl(key, i, kLanes);
+            const int e2 = __shfl(cand, i, kLanes);
+            if (cand >= 0 && e2 >= 0 && (k2 > key || (k2 == key && e2 < cand)))
+                ++rank;
+        }
+#pragma unroll 1
+        for (int i = 0; i < kMaxTopk; ++i) {
+            const int e2 = __shfl(cand, i, kLanes);
+            if (__shfl(rank, i, kLanes) == j)
+                chosen = e2;
+        }
+        return j < a.topk ? chosen : -1;
+    }
+    double last = -lowest<double>();
+    int last_e = -1;
+#pragma unroll 1
+    for (int k = 0; k < a.topk; ++k) {
+        double best = lowest<double>();
+        int at = INT_MAX;
+#pragma unroll 1
+        for (int e = j; e < a.experts; e += kLanes) {
+            const double key = key64(a, t, e, m, inv);
+            if (key > best && (key < last || (key == last && e > last_e))) {
+                best = key;
+                at = e;
+            }
+        }
+        const double top = group_max<kLanes>(best);
+        if (!(top > lowest<double>()))
+            break;
+        last_e = group_min<kLanes>(best == top ? at : INT_MAX);
+        last = top;
+        if (j == k)
+            chosen = last_e;
+    }
+    return chosen;
 }
 
 // Reads the logits once; a token's choice is kept by its group's lanes (lane k
@@ -314,14 +398,17 @@ __global__ __launch_bounds__(kGateThreads, kV < 32 ? 4 : 2) void k_gate(const Ga
     float *sum = reinterpret_cast<float *>(dyn) + a.experts + 1;   // [waves][E]
     float *zsum = sum + kWaves * a.experts;                        // [kTokens]
     __shared__ int last;
+    __shared__ __align__(16) float bias[kGateThreads];  // as many as experts at most
 
     const int tid = threadIdx.x, lane = tid & 63, wave = tid / 64, j = tid & (kLanes - 1);
     const int E = a.experts, K = a.topk;
-    if (kBalance) {
+    if (a.bias)
+        bias[tid] = tid < E ? a.bias[tid] : 0.0f;
+    if (kBalance)
         for (int e = tid; e <= E; e += kGateThreads)
             cnt[e] = 0;
+    if (kBalance || a.bias)
         __syncthreads();
-    }
     float prob[kV], z = 0.0f;
 #pragma unroll
     for (int v = 0; v < kV; ++v)
@@ -361,50 +448,36 @@ __global__ __launch_bounds__(kGateThreads, kV < 32 ? 4 : 2) void k_gate(const Ga
                 for (int v = 0; v < kV; ++v) {
                     if (kBalance)
                         prob[v] += s[v] * inv;
-                    if (a.bias) {
-                        const int e = slot_expert<kLanes, kV>(v, j);
-                        if (l[v] > lowest<float>())
-                            key[v] = (softmax ? s[v] * inv : s[v]) + a.bias[e];
-                    }
+                    if (a.bias && l[v] > lowest<float>())
+                        key[v] = (softmax ? s[v] * inv : s[v]) +
+                                 bias[slot_expert<kLanes, kV>(v, j)];
                 }
             }
+            // with a bias on to the first clear gap behind the choice, 16 at most
             float before = __builtin_inff();
-            bool close = false;
-            const int rounds = a.bias ? K + 1 : K;  // with a bias one more, to see the border
-            for (int k = 0; k < rounds; ++k) {
+            bool close = false, more = false;
+            for (int k = 0; k < K || a.bias; ++k) {
                 float best;
                 int e;
                 take_top<kLanes, kV>(key, j, best, e);
-                if (e >= 0)
-                    close |= before - best <= key_slack(best);
+                if (e < 0)
+                    break;
+                const bool near = before - best <= key_slack(best);
+                if (k >= K && !near)
+                    break;
+                close |= near;
+                if (k == kMaxTopk) {
+                    more = true;
+                    break;
+                }
                 before = best;
-                if (k < K && j == k)
+                if (j == k)
                     chosen = e;
             }
-            if (close && a.bias) {  // the same in 64 bits
-                double key64[kV], part = 0.0, sum64 = 1.0;
-#pragma unroll
-                for (int v = 0; v < kV; ++v) {
-                    const double x = (double)l[v];
-                    key64[v] = softmax ? exp(x - (double)m) : 1.0 / (1.0 + exp(-x));
-                    part += key64[v];
-                }
-                if (softmax)
-                    sum64 = group_sum<kLanes>(part);
-#pragma unroll
-                for (int v = 0; v < kV; ++v)
-                    key64[v] = l[v] > lowest<float>()
-                                   ? key64[v] / sum64 +
-                                         (double)a.bias[slot_expert<kLanes, kV>(v, j)]
-                                   : lowest<double>();
-                for (int k = 0; k < K; ++k) {
-                    double best;
-                    int e;
-                    take_top<kLanes, kV>(key64, j, best, e);
-                    if (j == k)
-                        chosen = e;
-                }
-            }
+            if (close && a.bias)
+                chosen = choose64<kLanes>(a, t, j, m, chosen, more);
+            else if (j >= K)
+                chosen = -1;
         }
         const bool have = chosen >= 0;
         float x = lowest<float>(), w = 0.0f;
@@ -453,6 +526,7 @@ __global__ __launch_bounds__(kGateThreads, kV < 32 ? 4 : 2) void k_gate(const Ga
     if (j == 0)
         zsum[tid / kLanes] = z;
     __syncthreads();
+    // a row of partials: E counts, E probability sums, the token count, the z sum
     const int words = gate_partial_words(E);
     float *mine = a.partial + (size_t)blockIdx.x * words;
     for (int e = tid; e < E; e += kGateThreads) {
@@ -461,17 +535,20 @@ __global__ __launch_bounds__(kGateThreads, kV < 32 ? 4 : 2) void k_gate(const Ga
         for (int w = 0; w < kWaves; ++w)
             p += sum[w * E + e];
         store_agent(mine + e, __int_as_float(cnt[e]));
-        store_agent(mine + E + 1 + e, p);
+        store_agent(mine + E + e, p);
     }
-    if (tid == 0) {
-        float zz = 0.0f;
-        for (int i = 0; i < kTokens; ++i)
-            zz += zsum[i];
-        store_agent(mine + E, __int_as_float(cnt[E]));
-        store_agent(mine + 2 * E + 1, zz);
+    if (wave == 0) {
+        float zz = lane < kTokens ? zsum[lane] : 0.0f;
+#pragma unroll
+        for (int x = 1; x < 64; x <<= 1)
+            zz += __shfl_xor(zz, x, 64);
+        if (lane == 0) {
+            store_agent(mine + 2 * E, __int_as_float(cnt[E]));
+            store_agent(mine + 2 * E + 1, zz);
+        }
     }
     // Every block's stores are at the device's point of coherence before it takes
-    // a ticket.  The last of each kGateFan blocks adds their rows, the last of
+    // a ticket.  The last of each `fan` blocks adds their rows, the last of
     // those the sums: with one level its last block alone read 256 rows, 40 us more.
     const auto done = [&](uint32_t *ticket, uint32_t count) {
         __builtin_amdgcn_s_waitcnt(0);
@@ -485,41 +562,58 @@ __global__ __launch_bounds__(kGateThreads, kV < 32 ? 4 : 2) void k_gate(const Ga
         __syncthreads();
         return last != 0;
     };
-    const auto add_rows = [&](const float *from, int rows, int i) {  // word i
-        int c = 0;
-        float p = 0.0f;
-        if (i <= E) {
+    // words 2 i and 2 i + 1 added over rows; every load is in flight at once
+    const auto add_rows = [&](const float *from, int rows, int i, float &x, float &y) {
+        uint64_t w[kGateMaxFan];
 #pragma unroll
-            for (int b = 0; b < kGateFan; ++b)
-                c += b < rows ? __float_as_int(load_agent(from + (size_t)b * words + i)) : 0;
-            return __int_as_float(c);
-        }
+        for (int b = 0; b < kGateMaxFan; ++b)
+            w[b] = b < rows ? __hip_atomic_load(
+                                  reinterpret_cast<const uint64_t *>(from + (size_t)b * words) + i,
+                                  __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)
+                            : 0;
+        const auto word = [&](int at, int shift) {
+            int c = 0;
+            float p = 0.0f;
 #pragma unroll
-        for (int b = 0; b < kGateFan; ++b)
-            p += b < rows ? load_agent(from + (size_t)b * words + i) : 0.0f;
-        return p;
+            for (int b = 0; b < kGateMaxFan; ++b) {
+                c += (int)(uint32_t)(w[b] >> shift);
+                p += __uint_as_float((uint32_t)(w[b] >> shift));
+            }
+            return at < E || at == 2 * E ? __int_as_float(c) : p;
+        };
+        x = word(2 * i, 0);
+        y = word(2 * i + 1, 32);
     };
-    const int nb = gridDim.x, groups = (nb + kGateFan - 1) / kGateFan;
-    const int group = blockIdx.x / kGateFan, first = group * kGateFan;
-    const int in_group = nb - first < kGateFan ? nb - first : kGateFan;
+    const int nb = gridDim.x, fan = gate_fan(nb), groups = (nb + fan - 1) / fan;
+    const int group = blockIdx.x / fan, first = group * fan;
+    const int in_group = nb - first < fan ? nb - first : fan;
     if (!done(a.ticket + 1 + group, in_group))
         return;
     float *tops = a.partial + (size_t)nb * words;
     if (groups > 1) {
-        for (int i = tid; i < words; i += kGateThreads)
-            store_agent(tops + (size_t)group * words + i,
-                        add_rows(a.partial + (size_t)first * words, in_group, i));
+        for (int i = tid; i < words / 2; i += kGateThreads) {
+            float x, y;
+            add_rows(a.partial + (size_t)first * words, in_group, i, x, y);
+            store_agent(tops + (size_t)group * words + 2 * i, x);
+            store_agent(tops + (size_t)group * words + 2 * i + 1, y);
+        }
         if (!done(a.ticket, groups))
             return;
     }
-    for (int i = tid; i < words; i += kGateThreads) {
-        const float v = groups > 1 ? add_rows(tops, groups, i) : add_rows(a.partial, nb, i);
-        if (i <= E) {
-            cnt[i] = __float_as_int(v);
-            a.counts[i] = __float_as_int(v);
+    const auto take = [&](int at, float v) {
+        if (at < E || at == 2 * E) {
+            const int e = at < E ? at : E;
+            cnt[e] = __float_as_int(v);
+            a.counts[e] = __float_as_int(v);
         } else {
-            sum[i - E - 1] = v;
+            sum[at < 2 * E ? at - E : E] = v;
         }
+    };
+    for (int i = tid; i < words / 2; i += kGateThreads) {
+        float x, y;
+        add_rows(groups > 1 ? tops : a.partial, groups > 1 ? groups : nb, i, x, y);
+        take(2 * i, x);
+        take(2 * i + 1, y);
     }
     __syncthreads();
     if (wave == 0) {

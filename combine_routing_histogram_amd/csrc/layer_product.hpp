@@ -948,8 +948,8 @@ __global__ __launch_bounds__(kTileWaves *kWave) void k_product_tile(const Produc
 // used once, so they go straight to registers.  A block owns 16 output columns
 // (gated: 16 gate and 16 up rows) of one row tile; its four waves take the
 // contraction's 128-byte steps in turn, so a block reads 512 contiguous bytes
-// of each weight row per round, and add up through LDS at the end.  A lane
-// takes 32 contiguous bytes of a row per step; the contraction index is thus
+// of each weight row per round, and add up through LDS at the end.  A load
+// takes 64 contiguous bytes of each of 16 rows; the contraction index is thus
 // permuted inside a step, alike for both operands.
 
 constexpr int kStreamWaves = 4;
@@ -965,7 +965,7 @@ __global__ __launch_bounds__(kStreamWaves *kWave) void k_product_stream(const Pr
         return;
     __syncthreads();
     const int col0 = t.col_tile * 16;
-    const int at = (lane >> 4) * 32;  // this lane's bytes of a step
+    const int at = (lane >> 4) * 16;  // this lane's bytes of each half step
     const uint8_t *qp[kQ], *pp[kMI];
     const float *sx[kMI], *sw[kQ];
     const int bytes = a.contract * (kE4m3 ? 1 : 2), blocks = a.contract / 128;
@@ -1027,11 +1027,10 @@ __global__ __launch_bounds__(kStreamWaves *kWave) void k_product_stream(const Pr
             for (int h = 0; h < 2; ++h) {
 #pragma unroll
                 for (int q = 0; q < kQ; ++q)
-                    w[b][q][h] = __builtin_nontemporal_load(
-                        reinterpret_cast<const i32x4 *>(qp[q] + o + h * 16));
+                    w[b][q][h] = *reinterpret_cast<const i32x4 *>(qp[q] + o + h * 64);
 #pragma unroll
                 for (int i = 0; i < kMI; ++i)
-                    x[b][i][h] = *reinterpret_cast<const i32x4 *>(pp[i] + o + h * 16);
+                    x[b][i][h] = *reinterpret_cast<const i32x4 *>(pp[i] + o + h * 64);
             }
         }
 #pragma unroll
@@ -1043,14 +1042,14 @@ __global__ __launch_bounds__(kStreamWaves *kWave) void k_product_stream(const Pr
         const size_t o = (size_t)s * kStepBytes;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const bool in = s * kStepBytes + at + h * 16 < bytes;  // past the row: zeros
+            const bool in = s * kStepBytes + at + h * 64 < bytes;  // past the row: zeros
 #pragma unroll
             for (int q = 0; q < kQ; ++q)
-                w[q][h] = in ? *reinterpret_cast<const i32x4 *>(qp[q] + o + h * 16)
+                w[q][h] = in ? *reinterpret_cast<const i32x4 *>(qp[q] + o + h * 64)
                              : i32x4{0, 0, 0, 0};
 #pragma unroll
             for (int i = 0; i < kMI; ++i)
-                x[i][h] = in ? *reinterpret_cast<const i32x4 *>(pp[i] + o + h * 16)
+                x[i][h] = in ? *reinterpret_cast<const i32x4 *>(pp[i] + o + h * 64)
                              : i32x4{0, 0, 0, 0};
         }
         one(w, x, s);
