@@ -195,26 +195,32 @@ epdc_status grid_of(int64_t tiles, int *grid)
     return EPDC_SUCCESS;
 }
 
-template <int kProduct, bool kE4m3, int kGroups>
-epdc_status launch_tile(hipStream_t st, ProductArgs &a)
+// Column tiles of a product, and the blocks of its grid.
+template <int kProduct, int kGroups>
+epdc_status plan_tiles(ProductArgs &a, int *grid)
 {
-    constexpr int kBM = kGroups * 64;
     const int cols_per_tile =
         kProduct == kForward && act_gated(a.act) ? kTileCols / 2 : kTileCols;
     a.col_tiles = (a.out_cols + cols_per_tile - 1) / cols_per_tile;
     int64_t tiles;
     if (kProduct == kGradWeight) {
-        a.row_tiles = (a.out_rows + kBM - 1) / kBM;
+        a.row_tiles = (a.out_rows + kGroups * 64 - 1) / (kGroups * 64);
         tiles = (int64_t)a.experts * a.row_tiles * a.col_tiles;
     } else {
-        tiles = row_tile_bound(a.rows, a.experts, kBM) * a.col_tiles;
+        tiles = row_tile_bound(a.rows, a.experts, kGroups * 64) * a.col_tiles;
     }
+    return grid_of(tiles, grid);
+}
+
+template <bool kE4m3, int kGroups>
+epdc_status launch_tile(hipStream_t st, ProductArgs &a)
+{
     int grid;
-    const epdc_status s = grid_of(tiles, &grid);
+    const epdc_status s = plan_tiles<kForward, kGroups>(a, &grid);
     if (s != EPDC_SUCCESS)
         return s;
     return launch("k_product_tile", [&] {
-        k_product_tile<kProduct, kE4m3, kGroups><<<grid, kTileWaves * kWave, 0, st>>>(a);
+        k_product_tile<kE4m3, kGroups><<<grid, kTileWaves * kWave, 0, st>>>(a);
     });
 }
 
@@ -241,8 +247,8 @@ epdc_status launch_forward(hipStream_t st, ProductArgs &a)
     if (mean <= 8)
         return launch_stream<kE4m3, 1>(st, a);
     if (mean <= 64)
-        return launch_tile<kForward, kE4m3, 1>(st, a);
-    return launch_tile<kForward, kE4m3, kE4m3 ? 3 : 4>(st, a);
+        return launch_tile<kE4m3, 1>(st, a);
+    return launch_tile<kE4m3, kE4m3 ? 3 : 4>(st, a);
 }
 
 }  // namespace
@@ -424,38 +430,52 @@ epdc_status epdc_expert_backward(const epdc_product_args *args, void *stream,
     a.q_bytes = in * 2;
     a.out_cols = in;
     a.expert_off = args->expert_off;
-    if (grad_input && args->rows > 0) {
-        ProductArgs g = a;
-        g.contract = of;
-        g.q = static_cast<const uint8_t *>(args->weight);
-        g.out = static_cast<uint8_t *>(grad_input);
-        s = launch_tile<kGradInput, false, 4>(st, g);
-        if (s != EPDC_SUCCESS)
-            return s;
-    }
+    GradArgs g = {};
+    g.weight = g.input = a;
+    // few rows per expert: 64-row tiles for the rows' gradient, as in the forward
+    const bool few = args->rows / args->num_experts <= 64;
+    int64_t blocks = 0;
     if (grad_weight) {
-        ProductArgs g = a;
-        g.out_rows = of;
-        g.out_fp32 = grad_weight_dtype == EPDC_DT_FP32;
-        g.q = static_cast<const uint8_t *>(args->input);
-        g.out = static_cast<uint8_t *>(grad_weight);
-        s = launch_tile<kGradWeight, false, 4>(st, g);
+        g.weight.out_rows = of;
+        g.weight.out_fp32 = grad_weight_dtype == EPDC_DT_FP32;
+        g.weight.q = static_cast<const uint8_t *>(args->input);
+        g.weight.out = static_cast<uint8_t *>(grad_weight);
+        s = plan_tiles<kGradWeight, 4>(g.weight, &g.weight_blocks);
         if (s != EPDC_SUCCESS)
             return s;
+        blocks += g.weight_blocks;
+    }
+    if (grad_input && args->rows > 0) {
+        g.input.contract = of;
+        g.input.q = static_cast<const uint8_t *>(args->weight);
+        g.input.out = static_cast<uint8_t *>(grad_input);
+        s = few ? plan_tiles<kGradInput, 1>(g.input, &g.input_blocks)
+                : plan_tiles<kGradInput, 4>(g.input, &g.input_blocks);
+        if (s != EPDC_SUCCESS)
+            return s;
+        blocks += g.input_blocks;
     }
     if (grad_bias) {
-        BiasGradArgs b = {};
-        b.rows = args->rows;
-        b.experts = args->num_experts;
-        b.cols = of;
-        b.expert_off = args->expert_off;
-        b.act = args->activation;
-        b.grad_out = static_cast<const uint16_t *>(grad_out);
-        b.preact = static_cast<const uint16_t *>(preact);
-        b.grad_bias = grad_bias;
-        const dim3 grid(args->num_experts, (of + kWave * 8 - 1) / (kWave * 8));
-        s = launch("k_bias_grad",
-                   [&] { k_bias_grad<<<grid, dim3(kWave, kBiasSlices), 0, st>>>(b); });
+        g.bias.rows = args->rows;
+        g.bias.experts = args->num_experts;
+        g.bias.cols = of;
+        g.bias.expert_off = args->expert_off;
+        g.bias.act = args->activation;
+        g.bias.grad_out = static_cast<const uint16_t *>(grad_out);
+        g.bias.preact = static_cast<const uint16_t *>(preact);
+        g.bias.grad_bias = grad_bias;
+        g.bias_cols = (of + kWave * 8 - 1) / (kWave * 8);
+        blocks += (int64_t)args->num_experts * g.bias_cols;
+    }
+    if (blocks > 0x7fffffff)
+        return fail(EPDC_ERR_INVALID_ARGS, "more tiles than a launch can hold");
+    if (blocks > 0) {
+        s = launch("k_product_grads", [&] {
+            if (few)
+                k_product_grads<1><<<(int)blocks, kTileWaves * kWave, 0, st>>>(g);
+            else
+                k_product_grads<4><<<(int)blocks, kTileWaves * kWave, 0, st>>>(g);
+        });
         if (s != EPDC_SUCCESS)
             return s;
     }

@@ -126,10 +126,10 @@ struct Tile {
 
 constexpr int kBandRows = 8, kRun = 32;
 
-__device__ inline int tile_number()
+__device__ inline int tile_number(int block)
 {
-    const int slot = blockIdx.x / kXcds;
-    return (slot / kRun * kXcds + (int)(blockIdx.x % kXcds)) * kRun + slot % kRun;
+    const int slot = block / kXcds;
+    return (slot / kRun * kXcds + block % kXcds) * kRun + slot % kRun;
 }
 
 // Tile `local` of an expert of mt x nt tiles.
@@ -150,7 +150,7 @@ __device__ inline int clamp_row(const int32_t *off, int i, int rows)
 
 // lds: int[kThreads / 64 + 4].  Returns false (in the whole block) past the total.
 template <int kThreads>
-__device__ inline bool find_tile(const ProductArgs &a, int bm, int *lds, Tile &t)
+__device__ inline bool find_tile(const ProductArgs &a, int block, int bm, int *lds, Tile &t)
 {
     constexpr int kEach = (kMaxExperts + kThreads - 1) / kThreads;
     constexpr int kWaves = kThreads / kWave;
@@ -185,7 +185,7 @@ __device__ inline bool find_tile(const ProductArgs &a, int bm, int *lds, Tile &t
         before += w < wave ? v : 0;
         total += v;
     }
-    const int id = tile_number();
+    const int id = tile_number(block);
     if (id >= total)
         return false;
     int first = before + incl - cnt;
@@ -555,25 +555,32 @@ __device__ inline void finish_forward8(const ProductArgs &a, int expert, int row
 
 constexpr int kTileWaves = 8, kTileWavesM = 2, kTileWavesN = 4, kTileCols = 256;
 
+// LDS of a tile: P0, P1, Q0 and Q1 of two steps; e4m3: also the scales of four
+// steps, 16 bytes for every row and every four columns, twice.
+template <bool kE4m3, int kGroups>
+struct TileLds {
+    static constexpr int kP1 = (kGroups + 1) / 2 * 64 * kStepBytes;
+    static constexpr int kQ0 = kGroups * 64 * kStepBytes, kQ1 = kQ0 + 128 * kStepBytes;
+    static constexpr int kStage = kQ1 + 128 * kStepBytes;
+    static constexpr int kScales = 2 * kStage, kScaleBytes = kGroups * 1024 + 1024;
+    static constexpr int kBytes = kScales + (kE4m3 ? 2 * kScaleBytes : 0);
+};
+
+#ifdef __HIP_DEVICE_COMPILE__  // the host pass needs the launch stubs only
 template <int kProduct, bool kE4m3, int kGroups>
-__global__ __launch_bounds__(kTileWaves *kWave) void k_product_tile(const ProductArgs a)
+__device__ __forceinline__ void product_tile(const ProductArgs &a, int block, uint8_t *lds)
 {
-#ifdef __HIP_DEVICE_COMPILE__  // the host pass needs the launch stub only
+    typedef TileLds<kE4m3, kGroups> Lds;
     constexpr int kBM = kGroups * 64;
     constexpr int kG0 = (kGroups + 1) / 2, kG1 = kGroups / 2;  // groups of P0, P1
     typedef typename PickTile<kProduct == kGradWeight, kG0 * 64, kTileWaves>::type PTile0;
     typedef typename PickTile<kProduct == kGradWeight, (kG1 ? kG1 : 1) * 64, kTileWaves>::type
         PTile1;
     typedef typename PickTile<kProduct != kForward, 128, kTileWaves>::type QTile;
-    constexpr int kP1At = PTile0::kBytes, kQ0At = kP1At + (kG1 ? PTile1::kBytes : 0);
-    constexpr int kQ1At = kQ0At + QTile::kBytes;
-    constexpr int kStage = kQ1At + QTile::kBytes;
-    // e4m3: the scales of four steps, 16 bytes for every row and every four
-    // columns, also twice
-    constexpr int kScaleBytes = kGroups * 1024 + 1024, kScaleAt = 2 * kStage;
+    constexpr int kP1At = Lds::kP1, kQ0At = Lds::kQ0, kQ1At = Lds::kQ1, kStage = Lds::kStage;
+    constexpr int kScaleAt = Lds::kScales, kScaleBytes = Lds::kScaleBytes;
     constexpr int kStep = kE4m3 ? 128 : 64;  // contraction elements per step
     constexpr int kElem = kE4m3 ? 1 : 2;
-    __shared__ __align__(1024) uint8_t lds[2 * kStage + (kE4m3 ? 2 * kScaleBytes : 0)];
 
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x / kWave);
     const int wm = wave / kTileWavesN, wn = wave % kTileWavesN;
@@ -581,7 +588,7 @@ __global__ __launch_bounds__(kTileWaves *kWave) void k_product_tile(const Produc
     Tile t;
     int contract = a.contract;  // elements
     if (kProduct == kGradWeight) {
-        const int per = a.row_tiles * a.col_tiles, id = tile_number();
+        const int per = a.row_tiles * a.col_tiles, id = tile_number(block);
         t.expert = id / per;
         if (t.expert >= a.experts)
             return;
@@ -592,7 +599,7 @@ __global__ __launch_bounds__(kTileWaves *kWave) void k_product_tile(const Produc
         t.rows = a.out_rows - t.row_tile * kBM;
         t.rows = t.rows < kBM ? t.rows : kBM;
     } else {
-        if (!find_tile<kTileWaves * kWave>(a, kBM, reinterpret_cast<int *>(lds), t))
+        if (!find_tile<kTileWaves * kWave>(a, block, kBM, reinterpret_cast<int *>(lds), t))
             return;
         __syncthreads();  // the scan's LDS becomes the operands'
     }
@@ -869,7 +876,7 @@ __global__ __launch_bounds__(kTileWaves *kWave) void k_product_tile(const Produc
     // (8 bytes per lane, a residual load before each store) 1021 x 8 rows of
     // 2048 x 7168 with bias and residual took 425 us of which 113 were this.
     constexpr int kRowFloats = kTileCols, kChunkBytes = 64 * kRowFloats * 4;
-    constexpr int kTurns = sizeof lds >= 2 * kChunkBytes ? 2 : 1;
+    constexpr int kTurns = Lds::kBytes >= 2 * kChunkBytes ? 2 : 1;
     const int vecs = gated ? kTileCols / 16 : kTileCols / 8;  // of 8 output columns, per row
     const int per = 64 * vecs / (kTileWaves * kWave);
     const auto slot = [](int row, int quad) { return row * (kRowFloats / 4) + (quad ^ (row & 15)); };
@@ -937,8 +944,18 @@ __global__ __launch_bounds__(kTileWaves *kWave) void k_product_tile(const Produc
             }
         }
     }
+}
+#endif
+
+template <bool kE4m3, int kGroups>
+__global__ __launch_bounds__(kTileWaves *kWave) void k_product_tile(const ProductArgs a)
+{
+#ifdef __HIP_DEVICE_COMPILE__
+    __shared__ __align__(1024) uint8_t lds[TileLds<kE4m3, kGroups>::kBytes];
+    product_tile<kForward, kE4m3, kGroups>(a, blockIdx.x, lds);
 #endif
 }
+
 
 // ---------------------------------------------------------------------------
 // Few rows per expert: the weights stream past them
@@ -961,7 +978,7 @@ __global__ __launch_bounds__(kStreamWaves *kWave) void k_product_stream(const Pr
     __shared__ __align__(16) f32x4 part[kStreamWaves][kMI * kQ][kWave];
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x / kWave);
     Tile t;
-    if (!find_tile<kStreamWaves * kWave>(a, kMI * 16, reinterpret_cast<int *>(part), t))
+    if (!find_tile<kStreamWaves * kWave>(a, blockIdx.x, kMI * 16, reinterpret_cast<int *>(part), t))
         return;
     __syncthreads();
     const int col0 = t.col_tile * 16;
@@ -1131,15 +1148,16 @@ struct BiasGradArgs {
     float *grad_bias;                   // [experts, cols]
 };
 
-constexpr int kBiasSlices = 8;
+constexpr int kBiasSlices = kTileWaves, kBiasLds = kBiasSlices * (kWave * 8 + 8) * 4;
 
 // Column sums of an expert's dz in fp32, from its factors rather than the rounded
 // dz: a block takes 512 columns, its eight waves every eighth row; the waves'
 // sums are added in order, so the result does not vary.
-__global__ __launch_bounds__(kBiasSlices *kWave) void k_bias_grad(const BiasGradArgs a)
+__device__ inline void bias_grad(const BiasGradArgs &a, int e, int col_block, uint8_t *lds)
 {
-    __shared__ float part[kBiasSlices][kWave * 8 + 8];
-    const int e = blockIdx.x, c = blockIdx.y * kWave * 8 + threadIdx.x * 8;
+    float(*part)[kWave * 8 + 8] = reinterpret_cast<float(*)[kWave * 8 + 8]>(lds);
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x / kWave);
+    const int c = col_block * kWave * 8 + lane * 8;
     const int r0 = clamp_row(a.expert_off, e, a.rows), r1 = clamp_row(a.expert_off, e + 1, a.rows);
     const bool gated = act_gated(a.act);
     const int gcols = gated ? a.cols / 2 : a.cols;
@@ -1148,7 +1166,7 @@ __global__ __launch_bounds__(kBiasSlices *kWave) void k_bias_grad(const BiasGrad
     float s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     if (c < a.cols) {
 #pragma unroll 4
-        for (int r = r0 + (int)threadIdx.y; r < r1; r += kBiasSlices) {
+        for (int r = r0 + wave; r < r1; r += kBiasSlices) {
             const bf16x8 g =
                 *reinterpret_cast<const bf16x8 *>(a.grad_out + (size_t)r * gcols + gc);
             if (a.act == kActNone) {
@@ -1172,16 +1190,50 @@ __global__ __launch_bounds__(kBiasSlices *kWave) void k_bias_grad(const BiasGrad
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        part[threadIdx.y][threadIdx.x * 8 + i] = s[i];
+        part[wave][lane * 8 + i] = s[i];
     __syncthreads();
-    const int col = threadIdx.y * kWave + threadIdx.x;
-    if (blockIdx.y * kWave * 8 + col >= a.cols)
+    const int col = threadIdx.x;
+    if (col_block * kWave * 8 + col >= a.cols)
         return;
     float sum = 0.0f;
 #pragma unroll
     for (int w = 0; w < kBiasSlices; ++w)
         sum += part[w][col];
-    a.grad_bias[(size_t)e * a.cols + blockIdx.y * kWave * 8 + col] = sum;
+    a.grad_bias[(size_t)e * a.cols + col_block * kWave * 8 + col] = sum;
+}
+
+// The gradients that follow from dz in one launch: first the blocks of the weights'
+// tiles, then the rows', then the biases' column blocks, any of them none.  Each
+// XCD's run of a part starts afresh, so a part holds a multiple of 8 blocks
+// unless it is the last.  (One after the other, 122 rows of 256 x 520 over 8
+// experts took 36 us, of which each launch was 6 to 10.)
+struct GradArgs {
+    ProductArgs weight, input;
+    BiasGradArgs bias;
+    int32_t weight_blocks, input_blocks, bias_cols;  // bias_cols: column blocks of an expert
+};
+
+template <int kInputGroups>
+__global__ __launch_bounds__(kTileWaves *kWave) void k_product_grads(const GradArgs a)
+{
+#ifdef __HIP_DEVICE_COMPILE__
+    constexpr int kBytes = TileLds<false, 4>::kBytes;
+    static_assert(kBytes >= kBiasLds, "the smaller parts fit");
+    __shared__ __align__(1024) uint8_t lds[kBytes];
+    int block = blockIdx.x;
+    if (block < a.weight_blocks) {
+        product_tile<kGradWeight, false, 4>(a.weight, block, lds);
+        return;
+    }
+    block -= a.weight_blocks;
+    if (block < a.input_blocks) {
+        product_tile<kGradInput, false, kInputGroups>(a.input, block, lds);
+        return;
+    }
+    block -= a.input_blocks;
+    const int e = block / a.bias_cols;
+    bias_grad(a.bias, e, block - e * a.bias_cols, lds);
+#endif
 }
 
 }  // namespace epdc_layer
