@@ -248,7 +248,7 @@ epdc_status launch_forward(hipStream_t st, ProductArgs &a)
         return launch_stream<kE4m3, 1>(st, a);
     if (mean <= 64)
         return launch_tile<kE4m3, 1>(st, a);
-    return launch_tile<kE4m3, kE4m3 ? 3 : 4>(st, a);
+    return launch_tile<kE4m3, 4>(st, a);
 }
 
 }  // namespace

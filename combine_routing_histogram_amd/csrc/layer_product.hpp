@@ -249,7 +249,8 @@ constexpr uint32_t kOpen = 0x7fffffffu;
 // so the bank swizzle -- 16-byte chunk c of row r sits at chunk c ^ (r & 7) --
 // is applied to the address a lane loads from.  Fragment reads of 16 rows x 16
 // bytes then touch every bank evenly.
-template <int kRows, int kWaves>
+// kWhole: the contraction is whole steps, so only steps past the end are cut.
+template <int kRows, int kWaves, bool kWhole>
 struct StraightTile {
     static constexpr int kBytes = kRows * kStepBytes;
     static constexpr int kReads = 1;  // LDS reads of a fragment
@@ -275,8 +276,9 @@ struct StraightTile {
     template <int kCount = kLoads>
     __device__ inline void load(uint8_t *lds, int step, int left, int wave)
     {
-        const __amdgpu_buffer_rsrc_t rs = buffer_at(base + (size_t)step * kStepBytes, kOpen);
-        const bool out = chunk * 16 >= left;
+        const __amdgpu_buffer_rsrc_t rs =
+            buffer_at(base + (size_t)step * kStepBytes, kWhole && left <= 0 ? 0 : kOpen);
+        const bool out = !kWhole && chunk * 16 >= left;
 #pragma unroll
         for (int d = 0; d < kCount; ++d)
             load_direct(rs, out ? kNowhere : off[d], lds + (d * kWaves + wave) * 1024);
@@ -351,12 +353,12 @@ struct CrossTile {
     }
 };
 
-template <bool kCross, int kExtent, int kWaves>
+template <bool kCross, int kExtent, int kWaves, bool kWhole>
 struct PickTile {
-    typedef StraightTile<kExtent, kWaves> type;
+    typedef StraightTile<kExtent, kWaves, kWhole> type;
 };
-template <int kExtent, int kWaves>
-struct PickTile<true, kExtent, kWaves> {
+template <int kExtent, int kWaves, bool kWhole>
+struct PickTile<true, kExtent, kWaves, kWhole> {
     typedef CrossTile<kExtent, kWaves> type;
 };
 
@@ -573,10 +575,11 @@ __device__ __forceinline__ void product_tile(const ProductArgs &a, int block, ui
     typedef TileLds<kE4m3, kGroups> Lds;
     constexpr int kBM = kGroups * 64;
     constexpr int kG0 = (kGroups + 1) / 2, kG1 = kGroups / 2;  // groups of P0, P1
-    typedef typename PickTile<kProduct == kGradWeight, kG0 * 64, kTileWaves>::type PTile0;
-    typedef typename PickTile<kProduct == kGradWeight, (kG1 ? kG1 : 1) * 64, kTileWaves>::type
-        PTile1;
-    typedef typename PickTile<kProduct != kForward, 128, kTileWaves>::type QTile;
+    typedef typename PickTile<kProduct == kGradWeight, kG0 * 64, kTileWaves,
+                              kE4m3>::type PTile0;
+    typedef typename PickTile<kProduct == kGradWeight, (kG1 ? kG1 : 1) * 64, kTileWaves,
+                              kE4m3>::type PTile1;
+    typedef typename PickTile<kProduct != kForward, 128, kTileWaves, kE4m3>::type QTile;
     constexpr int kP1At = Lds::kP1, kQ0At = Lds::kQ0, kQ1At = Lds::kQ1, kStage = Lds::kStage;
     constexpr int kScaleAt = Lds::kScales, kScaleBytes = Lds::kScaleBytes;
     constexpr int kStep = kE4m3 ? 128 : 64;  // contraction elements per step
@@ -753,7 +756,7 @@ __device__ __forceinline__ void product_tile(const ProductArgs &a, int block, ui
         // e4m3: the products of a step's 128 features are scaled as they are added
         // to acc, four multiply-adds per matrix instruction.  They follow kLag
         // instructions later, in its shadow: at once they would wait for it.
-        constexpr int kLag = 3;
+        constexpr int kLag = kGroups < 4 ? 3 : 1;  // as registers allow
         f32x4 late[kLag];
         float late_scale[kLag];
 #pragma unroll
