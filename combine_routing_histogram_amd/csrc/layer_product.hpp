@@ -12,6 +12,7 @@
 #pragma once
 
 #include <hip/hip_runtime.h>
+#include <limits.h>
 #include <stdint.h>
 
 namespace epdc_layer {
@@ -118,7 +119,7 @@ __host__ __device__ inline bool act_gated(int act) { return act >= kActSwiglu; }
 // (One expert per XCD instead read 4.1 GB from HBM for 0.94 GB of operands:
 // 32768 x 7168 x 4096 over 8 experts 1944 us, now 1766.)  The counts per expert
 // are on the device only: every block scans the offsets (at most 513 ints, in
-// L2), and blocks past the total end.
+// L2) into an index of its own.
 
 struct Tile {
     int expert, row0, rows, row_tile, col_tile;
@@ -148,26 +149,36 @@ __device__ inline int clamp_row(const int32_t *off, int i, int rows)
     return v < 0 ? 0 : (v > rows ? rows : v);
 }
 
-// lds: int[kThreads / 64 + 4].  Returns false (in the whole block) past the total.
+// The experts' first tiles and rows, in LDS.
+struct TileIndex {
+    int first[kMaxExperts];      // INT_MAX behind the last expert
+    int start[kMaxExperts + 1];
+    int wave_sum[16];
+    int total;
+};
+
+// Fills the index, and ends with a barrier.
 template <int kThreads>
-__device__ inline bool find_tile(const ProductArgs &a, int block, int bm, int *lds, Tile &t)
+__device__ inline void build_index(const ProductArgs &a, int bm, TileIndex &x)
 {
-    constexpr int kEach = (kMaxExperts + kThreads - 1) / kThreads;
-    constexpr int kWaves = kThreads / kWave;
+    constexpr int kEach = kMaxExperts / kThreads, kWaves = kThreads / kWave;
+    static_assert(kMaxExperts % kThreads == 0 && kWaves <= 16, "whole experts per thread");
     const int tid = threadIdx.x, lane = tid & 63, wave = tid / kWave;
-    int r0[kEach], n[kEach], cnt = 0;
+    int n[kEach], cnt = 0;
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
         const int e = tid * kEach + i;
-        r0[i] = n[i] = 0;
+        n[i] = 0;
         if (e < a.experts) {
-            r0[i] = clamp_row(a.expert_off, e, a.rows);
+            const int r0 = clamp_row(a.expert_off, e, a.rows);
             const int r1 = clamp_row(a.expert_off, e + 1, a.rows);
-            n[i] = r1 > r0[i] ? r1 - r0[i] : 0;
+            x.start[e] = r0;
+            if (e == a.experts - 1)
+                x.start[a.experts] = r1;
+            n[i] = r1 > r0 ? (r1 - r0 + bm - 1) / bm * a.col_tiles : 0;
         }
-        cnt += (n[i] + bm - 1) / bm;
+        cnt += n[i];
     }
-    cnt *= a.col_tiles;
     int incl = cnt;
 #pragma unroll
     for (int d = 1; d < kWave; d <<= 1) {
@@ -176,37 +187,41 @@ __device__ inline bool find_tile(const ProductArgs &a, int block, int bm, int *l
             incl += u;
     }
     if (lane == kWave - 1)
-        lds[wave] = incl;
+        x.wave_sum[wave] = incl;
     __syncthreads();
-    int total = 0, before = 0;
+    int total = 0, first = incl - cnt;
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) {
-        const int v = lds[w];
-        before += w < wave ? v : 0;
+        const int v = x.wave_sum[w];
+        first += w < wave ? v : 0;
         total += v;
     }
-    const int id = tile_number(block);
-    if (id >= total)
-        return false;
-    int first = before + incl - cnt;
-    if (id >= first && id < first + cnt) {
 #pragma unroll
-        for (int i = 0; i < kEach; ++i) {
-            const int c = (n[i] + bm - 1) / bm * a.col_tiles;
-            if (id >= first && id < first + c) {
-                lds[kWaves] = tid * kEach + i;
-                lds[kWaves + 1] = id - first;
-                lds[kWaves + 2] = r0[i];
-                lds[kWaves + 3] = n[i];
-            }
-            first += c;
-        }
+    for (int i = 0; i < kEach; ++i) {
+        const int e = tid * kEach + i;
+        x.first[e] = e < a.experts ? first : INT_MAX;
+        first += n[i];
     }
+    if (tid == 0)
+        x.total = total;
     __syncthreads();
-    t.expert = uniform(lds[kWaves]);
-    const int local = uniform(lds[kWaves + 1]);
-    const int start = uniform(lds[kWaves + 2]), have = uniform(lds[kWaves + 3]);
-    place(local, (have + bm - 1) / bm, a.col_tiles, t);
+}
+
+// Tile `id` of all; false past the total.  Every wave finds it for itself: the
+// expert is the last whose first tile is not behind it.
+__device__ inline bool find_tile(const ProductArgs &a, const TileIndex &x, int id, int bm, Tile &t)
+{
+    if (id >= uniform(x.total))
+        return false;
+    const int lane = threadIdx.x & 63;
+    int upto = 0;
+#pragma unroll
+    for (int k = 0; k < kMaxExperts / kWave; ++k)
+        upto += __popcll(__ballot(x.first[k * kWave + lane] <= id));
+    t.expert = uniform(upto - 1);
+    const int start = uniform(x.start[t.expert]);
+    const int have = uniform(x.start[t.expert + 1]) - start;
+    place(id - uniform(x.first[t.expert]), (have + bm - 1) / bm, a.col_tiles, t);
     t.row0 = start + t.row_tile * bm;
     const int left = have - t.row_tile * bm;
     t.rows = left < bm ? left : bm;
@@ -464,24 +479,18 @@ __device__ inline void finish_forward(const ProductArgs &a, int expert, int row,
     *reinterpret_cast<bf16x4 *>(a.out + at * 2) = to_bf16(y);
 }
 
-// Eight consecutive output columns of one row, as finish_forward; res: the
-// residual's, loaded beforehand.
-__device__ inline void finish_forward8(const ProductArgs &a, int expert, int row, int col,
-                                       float (&z)[8], float (&up)[8], bf16x8 res)
+// Eight consecutive output columns of one row, as finish_forward; the biases (0
+// for none) and the residual are loaded beforehand.
+__device__ inline void finish_forward8(const ProductArgs &a, int row, int col, float (&z)[8],
+                                       float (&up)[8], const float (&bz)[8], const float (&bu)[8],
+                                       bf16x8 res)
 {
     const bool gated = act_gated(a.act);
     if (a.bias) {
-        const f32x4 *b =
-            reinterpret_cast<const f32x4 *>(a.bias + (size_t)expert * a.weight_rows + col);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            z[i] += b[i / 4][i % 4];
-        if (gated) {
-            b = reinterpret_cast<const f32x4 *>(a.bias + (size_t)expert * a.weight_rows +
-                                                a.out_cols + col);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                up[i] += b[i / 4][i % 4];
+        for (int i = 0; i < 8; ++i) {
+            z[i] += bz[i];
+            up[i] += bu[i];
         }
     }
     bf16x8 o;
@@ -557,8 +566,11 @@ __device__ inline void finish_forward8(const ProductArgs &a, int expert, int row
 
 constexpr int kTileWaves = 8, kTileWavesM = 2, kTileWavesN = 4, kTileCols = 256;
 
-// LDS of a tile: P0, P1, Q0 and Q1 of two steps; e4m3: also the scales of four
-// steps, 16 bytes for every row and every four columns, twice.
+// LDS of a block: P0, P1, Q0 and Q1 of two steps; e4m3: also the scales of four
+// steps, 16 bytes for every row and every four columns, twice.  The index before
+// them and the results behind use the operands' part.  (Blocks that stayed for
+// tile after tile, bringing in the next one's operands while results left,
+// gained 1 to 3% on even rows and lost 4% on skewed ones.)
 template <bool kE4m3, int kGroups>
 struct TileLds {
     static constexpr int kP1 = (kGroups + 1) / 2 * 64 * kStepBytes;
@@ -566,102 +578,84 @@ struct TileLds {
     static constexpr int kStage = kQ1 + 128 * kStepBytes;
     static constexpr int kScales = 2 * kStage, kScaleBytes = kGroups * 1024 + 1024;
     static constexpr int kBytes = kScales + (kE4m3 ? 2 * kScaleBytes : 0);
+    static constexpr int kOutWave = 16 * 32 * 4;  // 16 rows of 32 columns, fp32
+    static_assert(kTileWaves * kOutWave <= kBytes && sizeof(TileIndex) <= kBytes, "both fit");
+    static_assert(kBytes <= 160 * 1024, "LDS of a CU");
 };
 
 #ifdef __HIP_DEVICE_COMPILE__  // the host pass needs the launch stubs only
-template <int kProduct, bool kE4m3, int kGroups>
-__device__ __forceinline__ void product_tile(const ProductArgs &a, int block, uint8_t *lds)
-{
-    typedef TileLds<kE4m3, kGroups> Lds;
-    constexpr int kBM = kGroups * 64;
-    constexpr int kG0 = (kGroups + 1) / 2, kG1 = kGroups / 2;  // groups of P0, P1
-    typedef typename PickTile<kProduct == kGradWeight, kG0 * 64, kTileWaves,
-                              kE4m3>::type PTile0;
-    typedef typename PickTile<kProduct == kGradWeight, (kG1 ? kG1 : 1) * 64, kTileWaves,
-                              kE4m3>::type PTile1;
-    typedef typename PickTile<kProduct != kForward, 128, kTileWaves, kE4m3>::type QTile;
-    constexpr int kP1At = Lds::kP1, kQ0At = Lds::kQ0, kQ1At = Lds::kQ1, kStage = Lds::kStage;
-    constexpr int kScaleAt = Lds::kScales, kScaleBytes = Lds::kScaleBytes;
-    constexpr int kStep = kE4m3 ? 128 : 64;  // contraction elements per step
-    constexpr int kElem = kE4m3 ? 1 : 2;
-
-    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x / kWave);
-    const int wm = wave / kTileWavesN, wn = wave % kTileWavesN;
-
+// A tile of one product: which, and its contraction length in elements.
+struct TileWork {
     Tile t;
-    int contract = a.contract;  // elements
-    if (kProduct == kGradWeight) {
-        const int per = a.row_tiles * a.col_tiles, id = tile_number(block);
-        t.expert = id / per;
-        if (t.expert >= a.experts)
-            return;
-        place(id - t.expert * per, a.row_tiles, a.col_tiles, t);
-        t.row0 = uniform(clamp_row(a.expert_off, t.expert, a.rows));
-        contract = uniform(clamp_row(a.expert_off, t.expert + 1, a.rows)) - t.row0;
-        contract = contract < 0 ? 0 : contract;
-        t.rows = a.out_rows - t.row_tile * kBM;
-        t.rows = t.rows < kBM ? t.rows : kBM;
-    } else {
-        if (!find_tile<kTileWaves * kWave>(a, block, kBM, reinterpret_cast<int *>(lds), t))
-            return;
-        __syncthreads();  // the scan's LDS becomes the operands'
-    }
-    const bool gated = kProduct == kForward && act_gated(a.act);
-    const int col0 = t.col_tile * (gated ? kTileCols / 2 : kTileCols);
-    // weight row of column c of unit h (forward)
-    const auto weight_row = [&](int h, int c) {
-        const int n = gated ? a.weight_rows / 2 : a.weight_rows;
-        const int r = col0 + c + (gated ? 0 : h * 128);
-        return (r < n ? r : n - 1) + (gated ? h * n : 0);
-    };
+    int contract, col0;
+    bool gated;
+};
 
+// The operands of a tile with kA 64-row groups of rows, and their loads.
+template <int kProduct, bool kE4m3, int kGroups, int kA>
+struct TileOperands {
+    typedef TileLds<kE4m3, kGroups> Lds;
+    static constexpr int kG0 = (kGroups + 1) / 2, kG1 = kGroups / 2;  // groups of P0, P1
+    static constexpr int kA0 = (kA + 1) / 2, kA1 = kA / 2;            // those with rows
+    static constexpr bool kPCross = kProduct == kGradWeight, kQCross = kProduct != kForward;
+    typedef typename PickTile<kPCross, kG0 * 64, kTileWaves, kE4m3>::type PTile0;
+    typedef typename PickTile<kPCross, (kG1 ? kG1 : 1) * 64, kTileWaves, kE4m3>::type PTile1;
+    typedef typename PickTile<kQCross, 128, kTileWaves, kE4m3>::type QTile;
+    static constexpr int kL0 = kPCross ? PTile0::kLoads : kA0;
+    static constexpr int kL1 = kPCross ? PTile1::kLoads : kA1;
+    // loads of a pair of units; the few of scales are not counted, so now and
+    // then a wave waits for one load more than it needs
+    static constexpr int kAll0 = kL0 + QTile::kLoads, kAll1 = (kA1 ? kL1 : 0) + QTile::kLoads;
+    static constexpr int kStep = kE4m3 ? 128 : 64;  // contraction elements per step
+    static constexpr int kElem = kE4m3 ? 1 : 2;
+
+    PTile0 p0;
+    PTile1 p1;
     QTile q0, q1;
-    if constexpr (kProduct == kForward) {
-        const uint8_t *w = a.q + (size_t)t.expert * a.weight_rows * a.q_bytes;
-        q0.init(w, a.q_bytes, wave, lane, [&](int r) { return weight_row(0, r); });
-        q1.init(w, a.q_bytes, wave, lane, [&](int r) { return weight_row(1, r); });
-    } else {
-        const uint8_t *q = a.q + (kProduct == kGradInput
-                                      ? (size_t)t.expert * a.weight_rows * a.q_bytes
-                                      : (size_t)t.row0 * a.q_bytes);
-        q0.init(q, a.q_bytes, (uint32_t)col0 * 2, wave, lane);
-        q1.init(q, a.q_bytes, (uint32_t)col0 * 2 + 256, wave, lane);
-    }
+    uint8_t *lds;
+    int contract, wave;
+    bool scaler;
+    const uint8_t *scale_base;
+    uint32_t scale_off, scale_end;
 
-    constexpr int kMI = kGroups * 2;
-    f32x4 acc[kMI][4];
-#pragma unroll
-    for (int i = 0; i < kMI; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            acc[i][j] = f32x4{0, 0, 0, 0};
-
-    const int steps = (contract + kStep - 1) / kStep;
-    auto sweep = [&](auto groups) {
-        constexpr int kA = decltype(groups)::value;  // 64-row groups that hold rows
-        constexpr int kA0 = (kA + 1) / 2, kA1 = kA / 2;
-        constexpr int kI0 = 2 * kA0, kI1 = 2 * kA1;  // row blocks of a wave
-        constexpr int kN0 = kI0, kN1 = kI1 ? kI1 : 1;
-        PTile0 p0;
-        PTile1 p1;
+    __device__ inline void init(const ProductArgs &a, const TileWork &w, uint8_t *l, int wv,
+                                int lane)
+    {
+        const Tile &t = w.t;
+        lds = l;
+        contract = w.contract;
+        wave = wv;
+        // weight row of column c of unit h (forward)
+        const auto weight_row = [&](int h, int c) {
+            const int n = w.gated ? a.weight_rows / 2 : a.weight_rows;
+            const int r = w.col0 + c + (w.gated ? 0 : h * 128);
+            return (r < n ? r : n - 1) + (w.gated ? h * n : 0);
+        };
+        if constexpr (kProduct == kForward) {
+            const uint8_t *q = a.q + (size_t)t.expert * a.weight_rows * a.q_bytes;
+            q0.init(q, a.q_bytes, wave, lane, [&](int r) { return weight_row(0, r); });
+            q1.init(q, a.q_bytes, wave, lane, [&](int r) { return weight_row(1, r); });
+        } else {
+            const uint8_t *q = a.q + (kProduct == kGradInput
+                                          ? (size_t)t.expert * a.weight_rows * a.q_bytes
+                                          : (size_t)t.row0 * a.q_bytes);
+            q0.init(q, a.q_bytes, (uint32_t)w.col0 * 2, wave, lane);
+            q1.init(q, a.q_bytes, (uint32_t)w.col0 * 2 + 256, wave, lane);
+        }
         const uint8_t *p = a.p + (size_t)t.row0 * a.p_bytes;
-        if constexpr (kProduct == kGradWeight) {
-            p0.init(p, a.p_bytes, (uint32_t)(t.row_tile * kBM) * 2, wave, lane);
-            p1.init(p, a.p_bytes, (uint32_t)(t.row_tile * kBM) * 2 + 256, wave, lane);
+        if constexpr (kPCross) {
+            p0.init(p, a.p_bytes, (uint32_t)(t.row_tile * kGroups * 64) * 2, wave, lane);
+            p1.init(p, a.p_bytes, (uint32_t)(t.row_tile * kGroups * 64) * 2 + 256, wave, lane);
         } else {
             const auto row = [&](int r) { return r < t.rows ? r : t.rows - 1; };
             p0.init(p, a.p_bytes, wave, lane, row);
             if constexpr (kA1 > 0)
                 p1.init(p, a.p_bytes, wave, lane, [&](int r) { return row(kA0 * 64 + r); });
         }
-        constexpr bool kPCross = kProduct == kGradWeight;
-        constexpr int kL0 = kPCross ? PTile0::kLoads : kA0, kL1 = kPCross ? PTile1::kLoads : kA1;
         // e4m3: the first waves bring the rows' scales, 64 rows each, the fifth the
         // columns', once every four steps; 16 bytes at a time because a row's
         // scales lie in a line of their own
-        const bool scaler = kE4m3 && (wave < kA || wave == 4);
-        const uint8_t *scale_base = nullptr;
-        uint32_t scale_off = 0, scale_end = 0;
+        scaler = kE4m3 && (wave < kA || wave == 4);
         if constexpr (kE4m3) {
             const int blocks = contract / 128;
             if (wave == 4) {
@@ -678,33 +672,104 @@ __device__ __forceinline__ void product_tile(const ProductArgs &a, int block, ui
                 scale_off = (uint32_t)r * blocks * 4;
             }
         }
-        const auto load_scales = [&](int group) {
-            if (scaler)
-                load_direct(buffer_at(scale_base, scale_end), scale_off + group * 16,
-                            lds + kScaleAt + (group & 1) * kScaleBytes +
-                                (wave == 4 ? kGroups : wave) * 1024);
-        };
+    }
+    __device__ inline void load_scales(int group)
+    {
+        if (scaler)
+            load_direct(buffer_at(scale_base, scale_end), scale_off + group * 16,
+                        lds + Lds::kScales + (group & 1) * Lds::kScaleBytes +
+                            (wave == 4 ? kGroups : wave) * 1024);
+    }
+    __device__ inline void load0(int s)
+    {
+        uint8_t *st = lds + (s & 1) * Lds::kStage;
+        const int left = contract - s * kStep;
+        p0.template load<kL0>(st, s, kPCross ? left : left * kElem, wave);
+        q0.load(st + Lds::kQ0, s, kQCross ? left : left * kElem, wave);
+    }
+    __device__ inline void load1(int s)
+    {
+        uint8_t *st = lds + (s & 1) * Lds::kStage;
+        const int left = contract - s * kStep;
+        q1.load(st + Lds::kQ1, s, kQCross ? left : left * kElem, wave);
+        if constexpr (kA1 > 0)
+            p1.template load<kL1>(st + Lds::kP1, s, kPCross ? left : left * kElem, wave);
+    }
+    // the first two steps
+    __device__ inline void start()
+    {
+        if constexpr (kE4m3)
+            load_scales(0);
+        load0(0);
+        load1(0);
+        load0(1);
+        load1(1);
+    }
+};
+
+template <int kProduct, bool kE4m3, int kGroups>
+__device__ __forceinline__ void product_tile(const ProductArgs &a, int block, uint8_t *lds)
+{
+    typedef TileLds<kE4m3, kGroups> Lds;
+    constexpr int kBM = kGroups * 64;
+    constexpr int kP1At = Lds::kP1, kQ0At = Lds::kQ0, kQ1At = Lds::kQ1, kStage = Lds::kStage;
+    constexpr int kScaleAt = Lds::kScales, kScaleBytes = Lds::kScaleBytes;
+    constexpr int kStep = kE4m3 ? 128 : 64;
+
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x / kWave);
+    const int wm = wave / kTileWavesN, wn = wave % kTileWavesN;
+    const bool gated = kProduct == kForward && act_gated(a.act);
+
+    TileWork w;
+    Tile &t = w.t;
+    w.contract = a.contract;
+    w.gated = gated;
+    if constexpr (kProduct == kGradWeight) {
+        const int per = a.row_tiles * a.col_tiles, id = tile_number(block);
+        t.expert = id / per;
+        if (t.expert >= a.experts)
+            return;
+        place(id - t.expert * per, a.row_tiles, a.col_tiles, t);
+        t.row0 = uniform(clamp_row(a.expert_off, t.expert, a.rows));
+        const int n = uniform(clamp_row(a.expert_off, t.expert + 1, a.rows)) - t.row0;
+        w.contract = n < 0 ? 0 : n;
+        t.rows = a.out_rows - t.row_tile * kBM;
+        t.rows = t.rows < kBM ? t.rows : kBM;
+    } else {
+        TileIndex &index = *reinterpret_cast<TileIndex *>(lds);
+        build_index<kTileWaves * kWave>(a, kBM, index);
+        if (!find_tile(a, index, tile_number(block), kBM, t))
+            return;
+        __syncthreads();  // the index's LDS becomes the operands'
+    }
+    w.col0 = t.col_tile * (gated ? kTileCols / 2 : kTileCols);
+
+    constexpr int kMI = kGroups * 2;
+    f32x4 acc[kMI][4];
+    auto sweep = [&](auto groups) {
+        constexpr int kA = decltype(groups)::value;  // 64-row groups that hold rows
+        typedef TileOperands<kProduct, kE4m3, kGroups, kA> Operands;
+        typedef typename Operands::PTile0 PTile0;
+        typedef typename Operands::PTile1 PTile1;
+        typedef typename Operands::QTile QTile;
+        constexpr int kA0 = Operands::kA0, kA1 = Operands::kA1;
+        constexpr int kI0 = 2 * kA0, kI1 = 2 * kA1;  // row blocks of a wave
+        constexpr int kN0 = kI0, kN1 = kI1 ? kI1 : 1;
+        constexpr int kAll0 = Operands::kAll0, kAll1 = Operands::kAll1;
+        Operands o;
+        o.init(a, w, lds, wave, lane);
+        o.start();
+        const int steps = (w.contract + kStep - 1) / kStep;
+#pragma unroll
+        for (int i = 0; i < kMI; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                acc[i][j] = f32x4{0, 0, 0, 0};
         // scale of row r (column group: row kGroups * 64 + c / 4) in step s
         const auto scale = [&](int s, int r) {
             return reinterpret_cast<const float *>(lds + kScaleAt +
                                                    (s >> 2 & 1) * kScaleBytes)[r * 4 + (s & 3)];
         };
-        const auto load0 = [&](int s) {
-            uint8_t *st = lds + (s & 1) * kStage;
-            const int left = contract - s * kStep;
-            p0.template load<kL0>(st, s, kPCross ? left : left * kElem, wave);
-            q0.load(st + kQ0At, s, kProduct == kForward ? left * kElem : left, wave);
-        };
-        const auto load1 = [&](int s) {
-            uint8_t *st = lds + (s & 1) * kStage;
-            const int left = contract - s * kStep;
-            q1.load(st + kQ1At, s, kProduct == kForward ? left * kElem : left, wave);
-            if constexpr (kA1 > 0)
-                p1.template load<kL1>(st + kP1At, s, kPCross ? left : left * kElem, wave);
-        };
-        // loads of a pair; the few of scales are not counted, so now and then a
-        // wave waits for one load more than it needs
-        constexpr int kAll0 = kL0 + QTile::kLoads, kAll1 = (kA1 ? kL1 : 0) + QTile::kLoads;
 
         i32x4 fp0[kN0][2], fp1[kN1][2], fq0[2][2], fq1[2][2];
         float sp0[kN0], sp1[kN1], sq0[2], sq1[2];
@@ -803,12 +868,6 @@ __device__ __forceinline__ void product_tile(const ProductArgs &a, int block, ui
         constexpr int kReadP1 = kI1 * (2 * PTile1::kReads + kScaleReads);
         constexpr int kReadQ = 2 * (2 * QTile::kReads + kScaleReads);
 
-        if constexpr (kE4m3)
-            load_scales(0);
-        load0(0);
-        load1(0);
-        load0(1);
-        load1(1);
         wait_and_meet<kAll0 + kAll1>();
         read_p0(0);
         read_q(0, 0, fq0, sq0);
@@ -817,9 +876,9 @@ __device__ __forceinline__ void product_tile(const ProductArgs &a, int block, ui
             if constexpr (kE4m3) {
                 // the group before has been read; this one is needed from step s + 4
                 if ((s & 3) == 0)
-                    load_scales((s >> 2) + 1);
+                    o.load_scales((s >> 2) + 1);
             }
-            load0(s + 2);
+            o.load0(s + 2);
             read_q(s, 1, fq1, sq1);
             read_p1(s);
             if constexpr (kE4m3) {
@@ -831,7 +890,7 @@ __device__ __forceinline__ void product_tile(const ProductArgs &a, int block, ui
                 multiply(Count<kI0>(), 0, 2, fp0, fq1);
             }
             wait_and_meet<kAll0 + kAll1>();
-            load1(s + 2);
+            o.load1(s + 2);
             read_p0(s + 1);  // after the last step: zeros, never used
             if constexpr (kE4m3) {
                 multiply_scaled(Count<kI1>(), Count<kI0>(), Count<kI0>(), Count<0>(), fp1, sp1);
@@ -852,7 +911,7 @@ __device__ __forceinline__ void product_tile(const ProductArgs &a, int block, ui
                 add_late(Count<kLastAt + m / 2 % kLast>(), Count<m / (2 * kLast) * 2 + m % 2>());
             });
         }
-        wait_and_meet<0>();  // no load may outlive the block
+        wait_and_meet<0>();  // the operands' LDS is free, and no load outlives the block
     };
     if constexpr (kProduct == kGradWeight) {
         sweep(Count<kGroups>());
@@ -861,88 +920,108 @@ __device__ __forceinline__ void product_tile(const ProductArgs &a, int block, ui
         if constexpr (kGroups >= 4) {
             if (groups >= 4)
                 sweep(Count<4>());
-        }
-        if constexpr (kGroups >= 3) {
-            if (groups == 3)
+            else if (groups == 3)
                 sweep(Count<3>());
-        }
-        if constexpr (kGroups >= 2) {
-            if (groups == 2)
+            else if (groups == 2)
                 sweep(Count<2>());
         }
         if (groups == 1)
             sweep(Count<1>());
     }
 
-    // The accumulators leave through LDS, 64 rows at a time: a lane holds 4 columns
-    // of 16 rows, and memory wants whole lines.  Written from the registers
-    // (8 bytes per lane, a residual load before each store) 1021 x 8 rows of
-    // 2048 x 7168 with bias and residual took 425 us of which 113 were this.
-    constexpr int kRowFloats = kTileCols, kChunkBytes = 64 * kRowFloats * 4;
-    constexpr int kTurns = Lds::kBytes >= 2 * kChunkBytes ? 2 : 1;
-    const int vecs = gated ? kTileCols / 16 : kTileCols / 8;  // of 8 output columns, per row
-    const int per = 64 * vecs / (kTileWaves * kWave);
-    const auto slot = [](int row, int quad) { return row * (kRowFloats / 4) + (quad ^ (row & 15)); };
+    // The accumulators leave through LDS, 16 rows by 32 columns of a wave at a time
+    // and with no barrier: a lane holds 4 columns of 16 rows, and memory wants
+    // 16 bytes per lane of few rows.  (From the registers, 8 bytes per lane and a
+    // residual load before each store, 1021 x 8 rows of 2048 x 7168 with bias and
+    // residual took 425 us of which 113 were this.)
+    f32x4 *out = reinterpret_cast<f32x4 *>(lds + wave * Lds::kOutWave);
+    const int lr = lane >> 2, v = lane & 3;  // of 8 columns, when read back
+    const auto through = [&](const f32x4 &lo, const f32x4 &hi, float(&z)[8]) {
+        const int row = lane & 15, quad = lane >> 4;
+        out[row * 8 + (quad ^ (row & 7))] = lo;
+        out[row * 8 + ((quad + 4) ^ (row & 7))] = hi;
+        // lanes read what others wrote: a wave's LDS accesses keep their order,
+        // and here the compiler has to keep it too (it moved the writes of
+        // lanes with nothing to store under their condition)
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        const f32x4 x = out[lr * 8 + ((v * 2) ^ (lr & 7))];
+        const f32x4 y = out[lr * 8 + ((v * 2 + 1) ^ (lr & 7))];
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
 #pragma unroll
-    for (int c = 0; c < kGroups; ++c) {
-        if (c * 64 >= t.rows)
-            break;
-        f32x4 *chunk = reinterpret_cast<f32x4 *>(lds + (kTurns == 2 ? c & 1 : 0) * kChunkBytes);
-        if (kTurns == 1 && c > 0)
-            __syncthreads();
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                chunk[slot((i * kTileWavesM + wm) * 16 + (lane & 15),
-                           (j >> 1) * 32 + wn * 8 + (j & 1) * 4 + (lane >> 4))] =
-                    acc[c * 2 + i][j];
-        bf16x8 res[4];
-        if (kProduct == kForward && a.residual) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int at = k * kTileWaves * kWave + (int)threadIdx.x;
-                const int r = c * 64 + at / vecs, col = col0 + at % vecs * 8;
-                if (k < per && r < t.rows && col < a.out_cols)
-                    res[k] = *reinterpret_cast<const bf16x8 *>(
-                        a.residual + (size_t)(t.row0 + r) * a.out_cols + col);
-            }
+        for (int i = 0; i < 4; ++i) {
+            z[i] = x[i];
+            z[4 + i] = y[i];
         }
-        __syncthreads();
+    };
+    const int col[2] = {w.col0 + wn * 32 + v * 8, w.col0 + 128 + wn * 32 + v * 8};
+    float bias[2][8] = {};
+    if (kProduct == kForward && a.bias) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int at = k * kTileWaves * kWave + (int)threadIdx.x;
-            const int lr = at / vecs, v = at % vecs, r = c * 64 + lr, col = col0 + v * 8;
-            if (k >= per || r >= t.rows || col >= a.out_cols)
-                continue;
-            float z[8], up[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                z[i] = chunk[slot(lr, v * 2 + i / 4)][i % 4];
-                up[i] = 0.0f;
-            }
-            if (gated) {
+        for (int h = 0; h < 2; ++h) {
+            const int c = gated ? col[0] + h * a.out_cols : col[h];
+            if ((gated ? col[0] : col[h]) < a.out_cols) {
+                const f32x4 *b = reinterpret_cast<const f32x4 *>(
+                    a.bias + (size_t)t.expert * a.weight_rows + c);
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    up[i] = chunk[slot(lr, 32 + v * 2 + i / 4)][i % 4];
+                    bias[h][i] = b[i / 4][i % 4];
             }
-            if constexpr (kProduct == kForward) {
-                finish_forward8(a, t.expert, t.row0 + r, col, z, up, res[k]);
-            } else {
-                const size_t row = kProduct == kGradInput
-                                       ? (size_t)(t.row0 + r)
-                                       : (size_t)t.expert * a.out_rows + t.row_tile * kBM + r;
-                const size_t to = row * a.out_cols + col;
-                if (kProduct == kGradWeight && a.out_fp32) {
-                    f32x4 *o = reinterpret_cast<f32x4 *>(a.out + to * 4);
-                    o[0] = f32x4{z[0], z[1], z[2], z[3]};
-                    o[1] = f32x4{z[4], z[5], z[6], z[7]};
-                } else {
-                    bf16x8 o;
+        }
+    }
+    constexpr int kBatch = kMI < 4 ? kMI : 4;  // row blocks whose residuals are in flight
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        o[i] = (__bf16)z[i];
-                    *reinterpret_cast<bf16x8 *>(a.out + to * 2) = o;
+    for (int i0 = 0; i0 < kMI; i0 += kBatch) {
+        bf16x8 res[kBatch][2];
+        if (kProduct == kForward && a.residual) {
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int r = ((i0 + i) * kTileWavesM + wm) * 16 + lr;
+                    if (r < t.rows && col[h] < a.out_cols && !(gated && h))
+                        res[i][h] = *reinterpret_cast<const bf16x8 *>(
+                            a.residual + (size_t)(t.row0 + r) * a.out_cols + col[h]);
+                }
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int block_row = ((i0 + i) * kTileWavesM + wm) * 16;
+            if (block_row >= t.rows)
+                break;
+            const int r = block_row + lr;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float z[8], up[8] = {};
+                through(acc[i0 + i][h * 2], acc[i0 + i][h * 2 + 1], z);
+                if (gated) {
+                    if (h)
+                        break;
+                    through(acc[i0 + i][2], acc[i0 + i][3], up);
+                }
+                if (r >= t.rows || col[h] >= a.out_cols)
+                    continue;
+                if constexpr (kProduct == kForward) {
+                    finish_forward8(a, t.row0 + r, col[h], z, up, bias[h], bias[1],
+                                    res[i][h]);
+                } else {
+                    const size_t row =
+                        kProduct == kGradInput
+                            ? (size_t)(t.row0 + r)
+                            : (size_t)t.expert * a.out_rows + t.row_tile * kBM + r;
+                    const size_t to = row * a.out_cols + col[h];
+                    if (kProduct == kGradWeight && a.out_fp32) {
+                        f32x4 *o = reinterpret_cast<f32x4 *>(a.out + to * 4);
+                        o[0] = f32x4{z[0], z[1], z[2], z[3]};
+                        o[1] = f32x4{z[4], z[5], z[6], z[7]};
+                    } else {
+                        bf16x8 o;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            o[k] = (__bf16)z[k];
+                        *reinterpret_cast<bf16x8 *>(a.out + to * 2) = o;
+                    }
                 }
             }
         }
@@ -979,11 +1058,12 @@ __global__ __launch_bounds__(kStreamWaves *kWave) void k_product_stream(const Pr
 {
     constexpr int kQ = kGated ? 2 : 1;
     __shared__ __align__(16) f32x4 part[kStreamWaves][kMI * kQ][kWave];
+    __shared__ TileIndex index;
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x / kWave);
     Tile t;
-    if (!find_tile<kStreamWaves * kWave>(a, blockIdx.x, kMI * 16, reinterpret_cast<int *>(part), t))
+    build_index<kStreamWaves * kWave>(a, kMI * 16, index);
+    if (!find_tile(a, index, tile_number(blockIdx.x), kMI * 16, t))
         return;
-    __syncthreads();
     const int col0 = t.col_tile * 16;
     const int at = (lane >> 4) * 16;  // this lane's bytes of each half step
     const uint8_t *qp[kQ], *pp[kMI];
