@@ -243,9 +243,21 @@ epdc_status launch_stream(hipStream_t st, ProductArgs &a)
 template <bool kE4m3>
 epdc_status launch_forward(hipStream_t st, ProductArgs &a)
 {
+    // By mean rows per expert, what is known here of the experts' counts.  The
+    // streamed form reads the weights fastest but once per 16 (32) rows of an
+    // expert, the tiles once per 64 (256) at 85% of that rate.  Measured over 64
+    // experts of 4096 x 4096, streamed (16), streamed (32), 64-row tiles: bf16 mean
+    // 8: 327, 346, 393 us; 12: 355, 337, 394; 24: -, 366, 405; 32: -, 578, 409.
+    // e4m3: 12: 195, 239, 238; 16: 261, 253, 236 (with 32 rows its registers
+    // leave too few waves).  64- against 256-row tiles, bf16: 64 rows 421, 433; 96:
+    // 497, 466.
     const int64_t mean = (int64_t)a.rows / a.experts;
-    if (mean <= 8)
+    if (mean <= (kE4m3 ? 12 : 10))
         return launch_stream<kE4m3, 1>(st, a);
+    if constexpr (!kE4m3) {
+        if (mean <= 24)
+            return launch_stream<kE4m3, 2>(st, a);
+    }
     if (mean <= 64)
         return launch_tile<kE4m3, 1>(st, a);
     return launch_tile<kE4m3, 4>(st, a);

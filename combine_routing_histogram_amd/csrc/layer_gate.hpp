@@ -775,7 +775,7 @@ struct CombineGradArgs {
     float *grad_weights;
 };
 
-constexpr int kCombineGradThreads = 256;
+constexpr int kCombineGradThreads = 512;
 
 // A block per token: a thread reads a vector of the token's gradient once and
 // serves the K rows with it -- the row's vector for the dot product in, the

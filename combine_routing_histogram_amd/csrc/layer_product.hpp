@@ -1044,12 +1044,14 @@ __global__ __launch_bounds__(kTileWaves *kWave) void k_product_tile(const Produc
 // ---------------------------------------------------------------------------
 //
 // With at most kMI * 16 rows per tile the weights are the traffic, each element
-// used once, so they go straight to registers.  A block owns 16 output columns
-// (gated: 16 gate and 16 up rows) of one row tile; its four waves take the
-// contraction's 128-byte steps in turn, so a block reads 512 contiguous bytes
-// of each weight row per round, and add up through LDS at the end.  A load
-// takes 64 contiguous bytes of each of 16 rows; the contraction index is thus
-// permuted inside a step, alike for both operands.
+// used once.  A block owns 16 output columns (gated: 16 gate and 16 up rows) of
+// one row tile; its four waves take the contraction's 128-byte steps in turn, so
+// a block reads 512 contiguous bytes of each weight row per round, and add up
+// through LDS at the end.  A load takes whole 128-byte lines of 8 rows, past the
+// caches, and a wave turns them through 2 KiB of LDS of its own into fragments
+// of 16 rows.  (Loaded as fragments, 64 bytes of 16 rows, one token's eight
+// experts of 7168 x 4096 took 89 us, 5.3 TB/s; as lines 83, and past the caches
+// 72, 6.6 TB/s.)
 
 constexpr int kStreamWaves = 4;
 
@@ -1059,6 +1061,7 @@ __global__ __launch_bounds__(kStreamWaves *kWave) void k_product_stream(const Pr
     constexpr int kQ = kGated ? 2 : 1;
     __shared__ __align__(16) f32x4 part[kStreamWaves][kMI * kQ][kWave];
     __shared__ TileIndex index;
+    __shared__ __align__(16) uint8_t turn[kStreamWaves][2][kQ][16 * kStepBytes];
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x / kWave);
     Tile t;
     build_index<kStreamWaves * kWave>(a, kMI * 16, index);
@@ -1066,14 +1069,18 @@ __global__ __launch_bounds__(kStreamWaves *kWave) void k_product_stream(const Pr
         return;
     const int col0 = t.col_tile * 16;
     const int at = (lane >> 4) * 16;  // this lane's bytes of each half step
-    const uint8_t *qp[kQ], *pp[kMI];
+    const uint8_t *qp[kQ][2], *pp[kMI];
     const float *sx[kMI], *sw[kQ];
     const int bytes = a.contract * (kE4m3 ? 1 : 2), blocks = a.contract / 128;
 #pragma unroll
     for (int q = 0; q < kQ; ++q) {
-        int c = col0 + (lane & 15);
-        c = (c < a.out_cols ? c : a.out_cols - 1) + q * a.out_cols;
-        qp[q] = a.q + ((size_t)t.expert * a.weight_rows + c) * a.q_bytes + at;
+        int c;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            c = col0 + h * 8 + (lane >> 3);
+            c = (c < a.out_cols ? c : a.out_cols - 1) + q * a.out_cols;
+            qp[q][h] = a.q + ((size_t)t.expert * a.weight_rows + c) * a.q_bytes + (lane & 7) * 16;
+        }
         if constexpr (kE4m3) {
             c = col0 + (lane >> 4) * 4;
             c = (c < a.out_cols ? c : a.out_cols - 1) + q * a.out_cols;
@@ -1115,8 +1122,33 @@ __global__ __launch_bounds__(kStreamWaves *kWave) void k_product_stream(const Pr
             }
         }
     };
+    // lines of 8 + 8 rows to fragments of 16, in one of two turns' LDS; lanes read
+    // what others wrote, in the order in which the wave's LDS accesses run
+    const auto turned = [&](i32x4 (&w)[kQ][2], int buf) {
+        typedef StraightTile<16, 1, false> Turn;
+#pragma unroll
+        for (int q = 0; q < kQ; ++q)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int r = h * 8 + (lane >> 3);
+                *reinterpret_cast<i32x4 *>(turn[wave][buf][q] + r * kStepBytes +
+                                           ((lane & 7) ^ (r & 7)) * 16) = w[q][h];
+            }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int q = 0; q < kQ; ++q)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                w[q][h] = Turn::frag(turn[wave][buf][q], 0, h, lane);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+    };
     const int full = bytes / kStepBytes;
-    constexpr int kBatch = 4;
+    // steps in flight per wave: e4m3 with four held too many registers (128 x 8 rows
+    // of 4096 x 4096 over 128 experts 377 us, with two 341), bf16 with two too few
+    // bytes (one token 75 us, with four 69)
+    constexpr int kBatch = kE4m3 ? 2 : 4;
     int s = wave;
     for (; s + (kBatch - 1) * kStreamWaves < full; s += kBatch * kStreamWaves) {
         i32x4 w[kBatch][kQ][2], x[kBatch][kMI][2];
@@ -1127,31 +1159,37 @@ __global__ __launch_bounds__(kStreamWaves *kWave) void k_product_stream(const Pr
             for (int h = 0; h < 2; ++h) {
 #pragma unroll
                 for (int q = 0; q < kQ; ++q)
-                    w[b][q][h] = *reinterpret_cast<const i32x4 *>(qp[q] + o + h * 64);
+                    w[b][q][h] = __builtin_nontemporal_load(
+                        reinterpret_cast<const i32x4 *>(qp[q][h] + o));
 #pragma unroll
                 for (int i = 0; i < kMI; ++i)
                     x[b][i][h] = *reinterpret_cast<const i32x4 *>(pp[i] + o + h * 64);
             }
         }
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b)
+        for (int b = 0; b < kBatch; ++b) {
+            turned(w[b], b & 1);
             one(w[b], x[b], s + b * kStreamWaves);
+        }
     }
     for (; s * kStepBytes < bytes; s += kStreamWaves) {
         i32x4 w[kQ][2], x[kMI][2];
         const size_t o = (size_t)s * kStepBytes;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const bool in = s * kStepBytes + at + h * 64 < bytes;  // past the row: zeros
+            // past the row: zeros
+            const bool win = s * kStepBytes + (lane & 7) * 16 < bytes;
+            const bool in = s * kStepBytes + at + h * 64 < bytes;
 #pragma unroll
             for (int q = 0; q < kQ; ++q)
-                w[q][h] = in ? *reinterpret_cast<const i32x4 *>(qp[q] + o + h * 64)
-                             : i32x4{0, 0, 0, 0};
+                w[q][h] = win ? *reinterpret_cast<const i32x4 *>(qp[q][h] + o)
+                              : i32x4{0, 0, 0, 0};
 #pragma unroll
             for (int i = 0; i < kMI; ++i)
                 x[i][h] = in ? *reinterpret_cast<const i32x4 *>(pp[i] + o + h * 64)
                              : i32x4{0, 0, 0, 0};
         }
+        turned(w, 0);
         one(w, x, s);
     }
 #pragma unroll

@@ -88,11 +88,12 @@ def _rows_case(rng, T, K, E, hot=None, drop=0.0):
     return routed_op(idx, E), off, T * K
 
 
-# (T, K, E, in, out): few rows per expert (streamed weights) and many (tiles),
-# one token, ragged columns, contractions that end inside a step or are shorter
+# (T, K, E, in, out): few rows per expert (weights streamed past 16 or 32 rows)
+# and many (tiles), one token, ragged columns, contractions that end inside a
+# step or are shorter
 # than one, and rows around a tile's edge
 SHAPES = [(1, 1, 1, 8, 8), (1, 2, 4, 64, 16), (1, 8, 64, 264, 136), (3, 2, 2, 72, 24),
-          (16, 2, 8, 520, 200), (17, 1, 1, 128, 264), (63, 1, 1, 192, 72), (64, 2, 2, 136, 256),
+          (16, 2, 8, 520, 200), (17, 1, 1, 128, 264), (45, 2, 4, 152, 104), (63, 1, 1, 192, 72), (64, 2, 2, 136, 256),
           (65, 1, 1, 1032, 520), (200, 4, 8, 56, 312), (255, 1, 1, 320, 296), (257, 1, 1, 8, 8),
           (256, 2, 2, 264, 512), (700, 2, 3, 200, 1048)]
 
@@ -115,7 +116,7 @@ def test_forward_exact_integers(T, K, E, fin, fout):
 
 
 @pytest.mark.parametrize("act", ["none", "relu", "gelu", "silu", "swiglu", "geglu"])
-@pytest.mark.parametrize("T,K,E,fin,fout", [(2, 4, 8, 264, 80), (60, 2, 4, 200, 176),
+@pytest.mark.parametrize("T,K,E,fin,fout", [(2, 4, 8, 264, 80), (33, 2, 4, 584, 112), (60, 2, 4, 200, 176),
                                             (400, 2, 3, 328, 304)])
 def test_forward_activations(T, K, E, fin, fout, act):
     rng = np.random.default_rng(T)
