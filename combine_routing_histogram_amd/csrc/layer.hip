@@ -51,17 +51,19 @@ epdc_status launch(const char *name, F &&f)
 constexpr int kMaxFeatures = 1 << 20;
 constexpr int64_t kMaxExpertBytes = (int64_t)0x7fff0000;
 
-int gate_blocks(int64_t tokens, int limit)
+int gate_blocks(int64_t tokens, int experts, int limit)
 {
-    const int64_t per = kGateThreads / gate_lanes(tokens), b = (tokens + per - 1) / per;
+    const int64_t per = kGateThreads / gate_lanes(tokens, experts);
+    const int64_t b = (tokens + per - 1) / per;
     return (int)(b < 1 ? 1 : (b < limit ? b : limit));
 }
 
 // Blocks of a balance: in small batches half as many, whose sums take half as
 // long to add (4093 x 128: 17.9 us for the forward, with 512 blocks 18.9).
-int balance_blocks(int64_t tokens)
+int balance_blocks(int64_t tokens, int experts)
 {
-    return gate_blocks(tokens, tokens <= kGateWaveTokens ? kGateMaxBlocks / 2 : kGateMaxBlocks);
+    return gate_blocks(tokens, experts,
+                       gate_lanes(tokens, experts) == 64 ? kGateMaxBlocks / 2 : kGateMaxBlocks);
 }
 
 epdc_status check_gate(const epdc_gate_args *g)
@@ -109,7 +111,7 @@ template <typename F>
 void gate_form(int64_t tokens, int experts, F &&f)
 {
     const int step = experts <= 64 ? 0 : experts <= 128 ? 1 : experts <= 256 ? 2 : 3;
-    if (gate_lanes(tokens) == 64) {
+    if (gate_lanes(tokens, experts) == 64) {
         switch (step) {
         case 0: f(Count<64>(), Count<1>()); break;
         case 1: f(Count<64>(), Count<2>()); break;
@@ -274,8 +276,9 @@ epdc_status epdc_gate_scratch_bytes(int32_t max_tokens, int32_t num_experts, siz
                                            "are required", kMaxExperts);
     // the most blocks a call of up to max_tokens tokens takes: a wave per token
     // needs more of them than 16 lanes
-    const int small = max_tokens < kGateWaveTokens ? max_tokens : kGateWaveTokens;
-    const int a = balance_blocks(small), b = balance_blocks(max_tokens);
+    const int64_t wave = gate_wave_tokens(num_experts);
+    const int a = balance_blocks(max_tokens < wave ? max_tokens : wave, num_experts);
+    const int b = balance_blocks(max_tokens, num_experts);
     *bytes = 256 + sizeof(float) * (size_t)((a > b ? a : b) + kGateMaxFan) *
                        (size_t)gate_partial_words(num_experts);
     return ok();
@@ -308,14 +311,14 @@ epdc_status epdc_gate(const epdc_gate_args *args, void *stream, float *weights, 
     if (balance) {
         a.ticket = static_cast<uint32_t *>(scratch);
         a.partial = reinterpret_cast<float *>(static_cast<uint8_t *>(scratch) + 256);
-        const int grid = balance_blocks(a.tokens);
+        const int grid = balance_blocks(a.tokens, a.experts);
         const size_t lds = sizeof(float) * ((size_t)a.experts + 1 +
                                             kGateThreads / 64 * (size_t)a.experts +
-                                            kGateThreads / gate_lanes(a.tokens));
+                                            kGateThreads / gate_lanes(a.tokens, a.experts));
         s = launch("k_gate", [&] { launch_gate<true>(grid, lds, st, a); });
     } else {
         s = launch("k_gate",
-                   [&] { launch_gate<false>(gate_blocks(a.tokens, 1 << 20), 0, st, a); });
+                   [&] { launch_gate<false>(gate_blocks(a.tokens, a.experts, 1 << 20), 0, st, a); });
     }
     return s == EPDC_SUCCESS ? ok() : s;
 }
@@ -345,7 +348,8 @@ epdc_status epdc_gate_backward(const epdc_gate_args *args, void *stream, const i
     a.grad_losses = grad_losses;
     a.grad_logits = grad_logits;
     s = launch("k_gate_backward", [&] {
-        launch_gate_backward(gate_blocks(a.tokens, 1 << 20), static_cast<hipStream_t>(stream), a);
+        launch_gate_backward(gate_blocks(a.tokens, a.experts, 1 << 20),
+                             static_cast<hipStream_t>(stream), a);
     });
     return s == EPDC_SUCCESS ? ok() : s;
 }

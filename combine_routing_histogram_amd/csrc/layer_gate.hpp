@@ -22,14 +22,19 @@ constexpr int kGateMaxFan = 32;
 // Rows of partial sums one block adds; two levels of them hold every block.
 __host__ __device__ inline int gate_fan(int blocks) { return blocks <= 256 ? 16 : kGateMaxFan; }
 static_assert(kGateMaxBlocks <= kGateMaxFan * kGateMaxFan, "two levels of sums");
-// Up to this many tokens a whole wave takes one: with 16 lanes 4096 tokens are
-// only one wave per SIMD, and a wave's chain of top-k steps is the time.
-constexpr int kGateWaveTokens = 8192;
+// A whole wave per token up to 16 tokens per expert, then 16 lanes.  In 16 lanes
+// a token's chain of top-k steps is longer and few tokens leave most SIMDs with
+// one wave or none; with many the whole waves' steps are mostly idle lanes.
+// Forward and backward with a balance, 64 lanes against 16: 256 experts, 2048
+// tokens 24 and 30 us, 4096: 31 and 32, 8192: 45 and 33; 128 experts, 4093
+// tokens: 26 and 23.
+__host__ __device__ inline int64_t gate_wave_tokens(int experts) { return 16 * (int64_t)experts; }
 
-__host__ __device__ inline int gate_lanes(int64_t tokens)
+__host__ __device__ inline int gate_lanes(int64_t tokens, int experts)
 {
-    return tokens <= kGateWaveTokens ? 64 : 16;
+    return tokens <= gate_wave_tokens(experts) ? 64 : 16;
 }
+
 constexpr int kMaxTopk = 16;
 
 enum { kScoreSoftmax = 0, kScoreSigmoid = 1 };

@@ -171,12 +171,29 @@ def test_gate_matches_the_definition(T, E, K, cfg, dtype):
     _check(op, logits, K, cfg, bias=bias, mask=mask, seed=1)
 
 
+# more than 16 tokens per expert: four tokens share a wave
+@pytest.mark.parametrize("cfg", [CONFIGS[0], CONFIGS[2], CONFIGS[3]],
+                         ids=lambda c: f"{c.score}-{c.renormalize}")
+@pytest.mark.parametrize("T,E,K", [(17, 1, 1), (130, 8, 2), (1030, 64, 8), (1043, 65, 16),
+                                   (2049, 128, 8), (2070, 129, 6), (4113, 257, 5)])
+def test_gate_many_tokens(T, E, K, cfg):
+    print(f"gate T={T} E={E} K={K} {cfg}", flush=True)
+    rng = np.random.default_rng(T)
+    dtype = torch.bfloat16 if T % 2 else torch.float32
+    logits = torch.from_numpy(2 * rng.standard_normal((T, E))).to(DEV).to(dtype)
+    bias = torch.from_numpy(0.2 * rng.standard_normal(E).astype(np.float32)).to(DEV)
+    mask = torch.from_numpy((rng.random(T) < 0.8).astype(np.uint8)).to(DEV)
+    _check(_op(T, E, K), logits, K, cfg, bias=bias if T % 3 else None, mask=mask)
+
+
+# 24 experts: up to 384 tokens a wave each, then four to a wave
+@pytest.mark.parametrize("T", [40, 400])
 @pytest.mark.parametrize("cfg", CONFIGS, ids=lambda c: f"{c.score}-{c.renormalize}")
-def test_masked_and_missing(cfg):
+def test_masked_and_missing(cfg, T):
     """Masked tokens whatever they hold, rows without experts, fewer experts than
     K, and logits that are not numbers."""
     rng = np.random.default_rng(3)
-    T, E, K = 40, 24, 4
+    E, K = 24, 4
     l = 2 * rng.standard_normal((T, E)).astype(np.float32)
     inf = np.inf
     l[0] = -inf                 # no expert
@@ -200,11 +217,12 @@ def test_masked_and_missing(cfg):
     _check(op, logits, K, cfg, bias=bias, mask=mk)
 
 
+@pytest.mark.parametrize("T", [256, 2100])
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
-def test_ties_and_near_ties_with_a_bias(score):
+def test_ties_and_near_ties_with_a_bias(score, T):
     """Keys that agree in 32 bits are ordered as in 64; equal ones by index."""
     rng = np.random.default_rng(5)
-    T, E, K = 256, 128, 8
+    E, K = 128, 8
     l = np.round(4 * rng.standard_normal((T, E)) / 2) / 2          # many equal logits
     l[::2] += rng.integers(0, 3, (T // 2, E)) * 2.0 ** -22         # or nearly equal
     logits = torch.from_numpy(l.astype(np.float32)).to(DEV)
