@@ -155,6 +155,8 @@ epdc_status check_product(const epdc_product_args *p)
         return fail(EPDC_ERR_INVALID_ARGS, "rows must be in [0, 2^30]");
     if (p->num_experts < 1 || p->num_experts > kMaxExperts)
         return fail(EPDC_ERR_INVALID_ARGS, "num_experts must be in [1, %d]", kMaxExperts);
+    if (p->expected_rows < 0)
+        return fail(EPDC_ERR_INVALID_ARGS, "expected_rows must be >= 0");
     if (p->activation < EPDC_ACT_NONE || p->activation > EPDC_ACT_GEGLU)
         return fail(EPDC_ERR_INVALID_ARGS, "unknown activation %d", p->activation);
     if (p->dtype != EPDC_DT_BF16 && p->dtype != EPDC_DT_E4M3)
@@ -177,6 +179,12 @@ epdc_status check_product(const epdc_product_args *p)
         return fail(EPDC_ERR_INVALID_ARGS, "input, weight and bias must be 16-byte aligned, the "
                                            "other arrays 4-byte aligned");
     return EPDC_SUCCESS;
+}
+
+int64_t mean_rows(const epdc_product_args &p)
+{
+    const int rows = p.expected_rows > 0 && p.expected_rows < p.rows ? p.expected_rows : p.rows;
+    return rows / p.num_experts;
 }
 
 // Row tiles that `experts` experts with at most `rows` rows between them can
@@ -243,9 +251,9 @@ epdc_status launch_stream(hipStream_t st, ProductArgs &a)
 }
 
 template <bool kE4m3>
-epdc_status launch_forward(hipStream_t st, ProductArgs &a)
+epdc_status launch_forward(hipStream_t st, ProductArgs &a, int64_t mean)
 {
-    // By mean rows per expert, what is known here of the experts' counts.  The
+    // By mean rows per expert, all that is known here of the experts' counts.  The
     // streamed form reads the weights fastest but once per 16 (32) rows of an
     // expert, the tiles once per 64 (256) at 85% of that rate.  Measured over 64
     // experts of 4096 x 4096, streamed (16), streamed (32), 64-row tiles: bf16 mean
@@ -253,7 +261,6 @@ epdc_status launch_forward(hipStream_t st, ProductArgs &a)
     // e4m3: 12: 195, 239, 238; 16: 261, 253, 236 (with 32 rows its registers
     // leave too few waves).  64- against 256-row tiles, bf16: 64 rows 421, 433; 96:
     // 497, 466.
-    const int64_t mean = (int64_t)a.rows / a.experts;
     if (mean <= (kE4m3 ? 12 : 10))
         return launch_stream<kE4m3, 1>(st, a);
     if constexpr (!kE4m3) {
@@ -388,7 +395,8 @@ epdc_status epdc_expert_product(const epdc_product_args *args, void *stream, con
     a.out = static_cast<uint8_t *>(out);
     a.preact = static_cast<uint16_t *>(preact);
     hipStream_t st = static_cast<hipStream_t>(stream);
-    s = e4m3 ? launch_forward<true>(st, a) : launch_forward<false>(st, a);
+    const int64_t mean = mean_rows(*args);
+    s = e4m3 ? launch_forward<true>(st, a, mean) : launch_forward<false>(st, a, mean);
     return s == EPDC_SUCCESS ? ok() : s;
 }
 
@@ -449,7 +457,7 @@ epdc_status epdc_expert_backward(const epdc_product_args *args, void *stream,
     GradArgs g = {};
     g.weight = g.input = a;
     // few rows per expert: 64-row tiles for the rows' gradient, as in the forward
-    const bool few = args->rows / args->num_experts <= 64;
+    const bool few = mean_rows(*args) <= 64;
     int64_t blocks = 0;
     if (grad_weight) {
         g.weight.out_rows = of;

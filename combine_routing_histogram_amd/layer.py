@@ -43,7 +43,7 @@ class epdc_gate_args(ctypes.Structure):
 
 class epdc_product_args(ctypes.Structure):
     _fields_ = [(n, I32) for n in ("rows", "num_experts", "in_features", "out_features", "dtype",
-                                   "activation")] + \
+                                   "activation", "expected_rows")] + \
                [(n, P) for n in ("input", "scales", "weight", "weight_scales", "bias",
                                  "expert_off")]
 
@@ -101,11 +101,11 @@ def make_gate_args(num_tokens: int, num_experts: int, topk: int, score: int = EP
 
 
 def make_product_args(rows: int, num_experts: int, in_features: int, out_features: int,
-                      dtype: int = EPDC_DT_BF16, activation: int = EPDC_ACT_NONE, input: int = 0,
-                      scales: int = 0, weight: int = 0, weight_scales: int = 0, bias: int = 0,
+                      dtype: int = EPDC_DT_BF16, activation: int = EPDC_ACT_NONE,
+                      expected_rows: int = 0, input: int = 0, scales: int = 0, weight: int = 0, weight_scales: int = 0, bias: int = 0,
                       expert_off: int = 0) -> epdc_product_args:
     return epdc_product_args(rows, num_experts, in_features, out_features, dtype, activation,
-                             input or None, scales or None, weight or None, weight_scales or None,
+                             expected_rows, input or None, scales or None, weight or None, weight_scales or None,
                              bias or None, expert_off or None)
 
 

@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import dataclasses
 import enum
+import functools
 from typing import Optional, Tuple
 
 import torch
@@ -99,6 +100,18 @@ if not hasattr(torch._C, "_cuda_getCurrentRawStream"):  # older torch
         return torch.cuda.current_stream(device_index).cuda_stream
 
 
+def _on_op_device(method):
+    """Run a method with the op's device current, whatever the caller's is: its
+    kernels and its new tensors belong there."""
+    @functools.wraps(method)
+    def call(self, *args, **kwargs):
+        if self._dev_index < 0 or torch.cuda.current_device() == self._dev_index:
+            return method(self, *args, **kwargs)
+        with torch.cuda.device(self._dev_index):
+            return method(self, *args, **kwargs)
+    return call
+
+
 class EpDispatchCombineOp:
     def __init__(self, config: EpDispatchCombineConfig, device: Optional[torch.device] = None):
         self.config = config
@@ -124,6 +137,9 @@ class EpDispatchCombineOp:
             self._combined_weights = torch.empty((config.max_tokens, config.topk),
                                                  dtype=torch.float32, device=dev)
             self._combine_in = None
+            # zeroed here, before epdc_create waits for the device: a first gate()
+            # on another stream or under graph capture finds the scratch ready
+            self._gate = self._gate_buffers()
             self._op = B.epdc_create(c, self.workspace.data_ptr(), ws_bytes)
         self._tokens = 0
         self._scales_dtype = None
@@ -141,7 +157,6 @@ class EpDispatchCombineOp:
         self._last_dedup = False
         self._staging = None
         self._units = None          # unit-row buffers, allocated on first use
-        self._gate = None           # the gate's buffers, allocated on first use
         self._gate_cut = (-1, None)
         self._unit_carried = (False, False)
 
@@ -536,21 +551,15 @@ class EpDispatchCombineOp:
 
     # ---- the gate ------------------------------------------------------------------------
     def _gate_buffers(self) -> dict:
-        if self._gate is None:
-            cfg, dev = self.config, self.device
-            with torch.cuda.device(dev):
-                self._gate = {
-                    "weights": torch.empty((cfg.max_tokens, cfg.topk), dtype=torch.float32,
-                                           device=dev),
-                    "indices": torch.empty((cfg.max_tokens, cfg.topk), dtype=torch.int32,
-                                           device=dev),
-                    "counts": torch.empty(cfg.num_experts + 1, dtype=torch.int32, device=dev),
-                    "losses": torch.empty(2, dtype=torch.float32, device=dev),
-                    "scratch": torch.zeros(L.epdc_gate_scratch_bytes(cfg.max_tokens,
-                                                                     cfg.num_experts),
-                                           dtype=torch.uint8, device=dev),
-                }
-        return self._gate
+        cfg, dev = self.config, self.device
+        scratch = L.epdc_gate_scratch_bytes(cfg.max_tokens, cfg.num_experts)
+        return {
+            "weights": torch.empty((cfg.max_tokens, cfg.topk), dtype=torch.float32, device=dev),
+            "indices": torch.empty((cfg.max_tokens, cfg.topk), dtype=torch.int32, device=dev),
+            "counts": torch.empty(cfg.num_experts + 1, dtype=torch.int32, device=dev),
+            "losses": torch.empty(2, dtype=torch.float32, device=dev),
+            "scratch": torch.zeros(scratch, dtype=torch.uint8, device=dev),
+        }
 
     def _gate_args(self, logits, gate, bias, mask) -> L.epdc_gate_args:
         cfg = self.config
@@ -575,6 +584,7 @@ class EpDispatchCombineOp:
                                 else L.EPDC_DT_BF16,
                                 gate.scale, logits.data_ptr(), _ptr(bias), _ptr(mask))
 
+    @_on_op_device
     def gate(self, logits: torch.Tensor, gate: GateConfig = GateConfig(), *,
              bias: Optional[torch.Tensor] = None, mask: Optional[torch.Tensor] = None,
              balance: bool = False):
@@ -589,7 +599,7 @@ class EpDispatchCombineOp:
         views of buffers of the op that the next gate() overwrites."""
         args = self._gate_args(logits, gate, bias, mask)
         T = args.num_tokens
-        g = self._gate_buffers()
+        g = self._gate
         if self._gate_cut[0] != T:
             self._gate_cut = (T, (g["weights"][:T], g["indices"][:T]))
         views = self._gate_cut[1]
@@ -600,6 +610,7 @@ class EpDispatchCombineOp:
                     _ptr(g["counts"]), _ptr(g["losses"]), _ptr(g["scratch"]))
         return views + (g["counts"], g["losses"])
 
+    @_on_op_device
     def gate_backward(self, logits: torch.Tensor, indices: torch.Tensor,
                       gate: GateConfig = GateConfig(), *,
                       grad_weights: Optional[torch.Tensor] = None,
@@ -669,7 +680,7 @@ class EpDispatchCombineOp:
             self._need(bias, "bias", torch.float32, (n, out_f))
         off, _ = B.epdc_get_offsets(self._op)
         return L.make_product_args(rows, n, in_f, out_f, dtype, ACTIVATIONS[activation],
-                                   input.data_ptr(), _ptr(scales), weight.data_ptr(),
+                                   rows * n // cfg.num_experts, input.data_ptr(), _ptr(scales), weight.data_ptr(),
                                    _ptr(weight_scales), _ptr(bias), off + 4 * first_expert)
 
     def _need_rows(self, t, name, rows, cols) -> None:
@@ -677,6 +688,7 @@ class EpDispatchCombineOp:
         if t.dim() != 2 or t.shape[0] < rows or t.shape[1] != cols:
             raise ValueError(f"{name} must be [>= {rows}, {cols}], got {tuple(t.shape)}")
 
+    @_on_op_device
     def expert_product(self, input: torch.Tensor, weight: torch.Tensor, *,
                        scales: Optional[torch.Tensor] = None,
                        weight_scales: Optional[torch.Tensor] = None,
@@ -710,9 +722,12 @@ class EpDispatchCombineOp:
             out = torch.empty((rows, cols), dtype=torch.bfloat16, device=self.device)
         else:
             self._need_rows(out, "out", rows, cols)
+            if out.data_ptr() in (input.data_ptr(), _ptr(preact) or -1):
+                raise ValueError("out must be a tensor of its own (or residual)")
         L.epdc_expert_product(args, self._stream(), _ptr(residual), out.data_ptr(), _ptr(preact))
         return out
 
+    @_on_op_device
     def expert_product_backward(self, grad_output: torch.Tensor, input: torch.Tensor,
                                 weight: torch.Tensor, *, activation: str = "none",
                                 preact: Optional[torch.Tensor] = None, bias: bool = False,
@@ -755,6 +770,7 @@ class EpDispatchCombineOp:
         return grad_input, grad_weight, grad_bias
 
     # ---- gradients of combine and dispatch ---------------------------------------------------
+    @_on_op_device
     def combine_backward(self, grad_output: torch.Tensor, input: torch.Tensor,
                          weights: Optional[torch.Tensor] = None):
         """Gradients of combine(input, weights) under the routing of the last
@@ -774,6 +790,7 @@ class EpDispatchCombineOp:
                                 grad_input.data_ptr(), grad_weights.data_ptr())
         return grad_input, grad_weights
 
+    @_on_op_device
     def dispatch_backward(self, grad_output: torch.Tensor) -> torch.Tensor:
         """Gradient of dispatch's bf16 input: bf16 [T, H], the fp32 sum of each
         token's rows of grad_output (bf16 [>= T*K, H], received layout)."""

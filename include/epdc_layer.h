@@ -152,6 +152,8 @@ typedef struct epdc_product_args {
     int32_t out_features;    /* [8, 2^20]: rows of weight (both halves of a gated one) */
     int32_t dtype;           /* EPDC_DT_BF16 or EPDC_DT_E4M3 */
     int32_t activation;      /* epdc_activation */
+    int32_t expected_rows;   /* rows these experts are likely to hold, 0 = all `rows`:
+                                decides which form runs fastest, nothing else */
     const void *input;       /* [rows, in] */
     const float *scales;     /* e4m3: [rows, in/128], else NULL */
     const void *weight;      /* [E, out, in] */

@@ -157,3 +157,47 @@ def test_padded_batch():
                           grad_losses=layer.gl)
     assert not dl[20:].any() and bool(dl[:20].any())
     assert op.device_error() == 1
+
+
+def test_first_gate_call_is_captured():
+    """An op whose very first gate() is recorded into a graph: its scratch was made
+    ready with the op, so eager calls before the first replay work too."""
+    T, E, K = 64, 16, 2
+    op = EpDispatchCombineOp(EpDispatchCombineConfig(T, 8, K, E, 1), DEV)
+    logits = normal(np.random.default_rng(0), (T, E), dtype=torch.float32)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        outs = op.gate(logits, CFG, balance=True)
+    eager = [t.clone() for t in op.gate(logits, CFG, balance=True)]
+    assert int(eager[2][E]) == T and float(eager[3][0]) > 0
+    for _ in range(3):
+        for t in outs:
+            t.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(outs, eager):
+            assert torch.equal(a, b)
+
+
+def test_one_ranks_experts():
+    """The experts of one rank, as a rank of a group holds them: the rows of its
+    segment only, whatever form their number picks."""
+    rng = np.random.default_rng(9)
+    T, H, N, E, K, R = 24, 128, 64, 32, 4, 4
+    op = EpDispatchCombineOp(EpDispatchCombineConfig(T, H, K, E, R), DEV)
+    logits = normal(rng, (T, E), dtype=torch.float32)
+    weights, indices = op.gate(logits, CFG)
+    rows, _, _, _, _ = op.dispatch(normal(rng, (T, H)), weights, None, indices)
+    w = normal(rng, (E, N, H), H ** -0.5)
+    whole = op.expert_product(rows, w, activation="gelu")
+    _, rank_off = op.get_offsets()
+    off = rank_off.tolist()
+    for r in range(R):
+        mine = op.expert_product(rows, w[r * 8:(r + 1) * 8].contiguous(), activation="gelu",
+                                 first_expert=r * 8)
+        s = slice(off[r], off[r + 1])
+        # the forms may add the contraction in other orders: both are within
+        # 128 * 2^-23 of the terms' absolute sum (below 10 here), times gelu's 1.13,
+        # of the exact value, and rounded by half a step, 2^-8
+        assert torch.allclose(mine[s].float(), whole[s].float(), rtol=2 * 2.0 ** -8,
+                              atol=2 * 1.13 * 128 * 2.0 ** -23 * 10)

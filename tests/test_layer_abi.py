@@ -123,6 +123,7 @@ BAD_PRODUCTS = [
     (dict(out_features=60), "out_features"),
     (dict(out_features=72, activation=L.EPDC_ACT_SWIGLU), "out_features"),
     (dict(in_features=1 << 20, out_features=1 << 10), "2 GiB"),
+    (dict(expected_rows=-1), "expected_rows"),
     (dict(activation=6), "activation"),
     (dict(activation=-1), "activation"),
     (dict(dtype=L.EPDC_DT_FP32), "bf16 or e4m3"),
@@ -228,6 +229,7 @@ def test_op_refuses_bad_product_tensors(monkeypatch):
            (x, w.float(), {}), (x, w[0], {}), (x, w, dict(first_expert=1)),
            (x, w, dict(first_expert=-1)), (x, w, dict(activation="tanh")),
            (x, w, dict(residual=g[:, :32].contiguous())), (x, w, dict(out=g[:39])),
+           (x, torch.zeros(8, 256, 256, dtype=bf), dict(out=x)),
            (x, w, dict(preact=g.float())), (x, w, dict(bias=torch.zeros(8, 63))), (x, w, dict(bias=torch.zeros(8, 64, dtype=bf))),
            (x, w, dict(scales=s8, weight_scales=ws8)), (x8, w8, {}),
            (x8, w, {}), (x8, w8, dict(scales=s8[:39], weight_scales=ws8)),
