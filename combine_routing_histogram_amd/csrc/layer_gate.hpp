@@ -393,7 +393,9 @@ __device__ inline int choose64(const GateArgs &a, int64_t t, int j, float m, int
 // Reads the logits once; a token's choice is kept by its group's lanes (lane k
 // has choice k).  With a balance, each lane sums its experts' probabilities
 // over its tokens; waves, then blocks, are added in a fixed order, the blocks
-// by the last one to finish.
+// by the last one to finish.  (32768 x 256 fp32, sigmoid, top-8 with balance:
+// 50 us, 0.7 TB/s; 4093 x 128 bf16: 16 us; one token of 256 experts: 6 us, a
+// launch.  Large batches are bound by the choice's steps per token, not bytes.)
 template <int kLanes, int kV, bool kBalance>
 __global__ __launch_bounds__(kGateThreads, kV < 32 ? 4 : 2) void k_gate(const GateArgs a)
 {
@@ -638,6 +640,7 @@ __global__ __launch_bounds__(kGateThreads, kV < 32 ? 4 : 2) void k_gate(const Ga
 
 // One pass over the logits: with p the scores' softmax (sigmoid: s / sum s),
 //   d/dl_j of scale * r(chosen)  and of  E/n sum_e f_e p_e  and of  lse^2 / n.
+// (32768 x 256 fp32: 32 us, 2.1 TB/s; 4093 x 128 bf16: 7 us.)
 template <int kLanes, int kV>
 __global__ __launch_bounds__(kGateThreads, kV < 32 ? 4 : 2) void k_gate_backward(const GateArgs a)
 {
@@ -785,7 +788,8 @@ constexpr int kCombineGradThreads = 512;
 // A block per token: a thread reads a vector of the token's gradient once and
 // serves the K rows with it -- the row's vector for the dot product in, the
 // scaled gradient out.  Bytes are the bound (one row read and one written per
-// pair).
+// pair): 4096 x 7168 bf16, top-8, 998 MB in 177 to 196 us, 5.1 to 5.6 TB/s of the
+// 5.7 that copies reach; with 1024 threads 225 us where 512 took 195.
 template <int kTopk>
 __global__ __launch_bounds__(kCombineGradThreads) void k_combine_grad(const CombineGradArgs a)
 {
