@@ -680,8 +680,9 @@ class EpDispatchCombineOp:
             self._need(bias, "bias", torch.float32, (n, out_f))
         off, _ = B.epdc_get_offsets(self._op)
         return L.make_product_args(rows, n, in_f, out_f, dtype, ACTIVATIONS[activation],
-                                   rows * n // cfg.num_experts, input.data_ptr(), _ptr(scales), weight.data_ptr(),
-                                   _ptr(weight_scales), _ptr(bias), off + 4 * first_expert)
+                                   rows * n // cfg.num_experts, input.data_ptr(), _ptr(scales),
+                                   weight.data_ptr(), _ptr(weight_scales), _ptr(bias),
+                                   off + 4 * first_expert)
 
     def _need_rows(self, t, name, rows, cols) -> None:
         self._need(t, name, torch.bfloat16)
