@@ -288,11 +288,17 @@ __device__ inline float log_score(int score, float l)
     return fminf(l, 0.0f) - log1pf(expf(-fabsf(l)));
 }
 
-// exp(-l) is kept finite: past 80 the score is 0 to within e^-80
+// By the exponential of -|l|, which cannot overflow; -inf gives 0.
 __device__ inline float sigmoid(float l)
 {
-    return recip_near(1.0f + exp_near(fminf(-l, 80.0f)));
+    const float x = exp_near(-fabsf(l)), r = recip_near(1.0f + x);
+    return l >= 0.0f ? r : x * r;
 }
+
+// A sigmoid's shares s / sum s where the row's largest logit m is this low: all
+// s are e^l to within e^-20 of themselves (far below an ulp), so the shares are
+// the softmax's, whose terms e^(l - m) do not vanish together as the s do.
+__device__ inline bool far_below(float m) { return m < -20.0f; }
 
 // Keys with a bias, s + b, are rounded sums of rounded scores.  In fp32 s is
 // off by a few ulp of at most 1 and the sum by half an ulp of the key, so two
@@ -439,11 +445,13 @@ __global__ __launch_bounds__(kGateThreads, kV < 32 ? 4 : 2) void k_gate(const Ga
             for (int v = 0; v < kV; ++v)
                 key[v] = l[v];
             if (scores) {
+                // s: what the shares are of; a key's score is one factor away
+                const bool exps = softmax || (kBalance && far_below(m));
                 float s[kV], part = 0.0f, esum = 0.0f;
 #pragma unroll
                 for (int v = 0; v < kV; ++v) {
                     const float x = softmax || kBalance ? exp_near(l[v] - m) : 0.0f;
-                    s[v] = softmax ? x : sigmoid(l[v]);
+                    s[v] = exps ? x : sigmoid(l[v]);
                     part += s[v];
                     esum += x;
                 }
@@ -451,13 +459,13 @@ __global__ __launch_bounds__(kGateThreads, kV < 32 ? 4 : 2) void k_gate(const Ga
                     inv = 1.0f / group_sum<kLanes>(part);
                 if (kBalance)
                     lse = m + logf(softmax ? 1.0f / inv : group_sum<kLanes>(esum));
+                const float of_key = softmax ? inv : (exps ? exp_near(m) : 1.0f);
 #pragma unroll
                 for (int v = 0; v < kV; ++v) {
                     if (kBalance)
                         prob[v] += s[v] * inv;
                     if (a.bias && l[v] > lowest<float>())
-                        key[v] = (softmax ? s[v] * inv : s[v]) +
-                                 bias[slot_expert<kLanes, kV>(v, j)];
+                        key[v] = s[v] * of_key + bias[slot_expert<kLanes, kV>(v, j)];
                 }
             }
             // with a bias on to the first clear gap behind the choice, 16 at most
@@ -686,13 +694,14 @@ __global__ __launch_bounds__(kGateThreads, kV < 32 ? 4 : 2) void k_gate_backward
         for (int v = 0; v < kV; ++v)
             d[v] = kind == kTokenBad ? __builtin_nanf("") : 0.0f;
         if (kind == kTokenIn) {
-            // the rows' softmax x / xs and sigmoids s / ss
+            // the rows' softmax x / xs and shares s / ss
+            const bool exps = softmax || far_below(m);
             float x[kV], s[kV], xs = 0.0f, ss = 0.0f, fp = 0.0f;
 #pragma unroll
             for (int v = 0; v < kV; ++v) {
                 x[v] = exp_near(l[v] - m);
                 xs += x[v];
-                s[v] = softmax ? x[v] : sigmoid(l[v]);
+                s[v] = exps ? x[v] : sigmoid(l[v]);
                 ss += s[v];
                 fp += share[v] * s[v];
             }
@@ -723,7 +732,7 @@ __global__ __launch_bounds__(kGateThreads, kV < 32 ? 4 : 2) void k_gate_backward
             for (int v = 0; v < kV; ++v) {
                 const float q = x[v] * rx;
                 float b = gb * (s[v] * rs) * (share[v] - fp);
-                if (!softmax)
+                if (!exps)   // of far_below's, 1 to within e^-20
                     b *= 1.0f - s[v];
                 d[v] = b + (gz * lse - all) * q;
             }
