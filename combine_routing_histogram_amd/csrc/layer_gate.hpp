@@ -288,12 +288,16 @@ __device__ inline float log_score(int score, float l)
     return fminf(l, 0.0f) - log1pf(expf(-fabsf(l)));
 }
 
-// By the exponential of -|l|, which cannot overflow; -inf gives 0.
-__device__ inline float sigmoid(float l)
+// The smaller of a sigmoid s and 1 - s, by the exponential of -|l|, which cannot
+// overflow; 0 for -inf.  The slope s (1 - s) comes from it: by way of s
+// rounded, 1 - s would be lost near 1.
+__device__ inline float sigmoid_low(float l)
 {
-    const float x = exp_near(-fabsf(l)), r = recip_near(1.0f + x);
-    return l >= 0.0f ? r : x * r;
+    const float x = exp_near(-fabsf(l));
+    return x * recip_near(1.0f + x);
 }
+__device__ inline float sigmoid_of_low(float l, float low) { return l >= 0.0f ? 1.0f - low : low; }
+__device__ inline float sigmoid(float l) { return sigmoid_of_low(l, sigmoid_low(l)); }
 
 // A sigmoid's shares s / sum s where the row's largest logit m is this low: all
 // s are e^l to within e^-20 of themselves (far below an ulp), so the shares are
@@ -694,16 +698,18 @@ __global__ __launch_bounds__(kGateThreads, kV < 32 ? 4 : 2) void k_gate_backward
         for (int v = 0; v < kV; ++v)
             d[v] = kind == kTokenBad ? __builtin_nanf("") : 0.0f;
         if (kind == kTokenIn) {
-            // the rows' softmax x / xs and shares s / ss
+            // the rows' softmax x / xs and shares s / ss; low: s, of a sigmoid's
+            // that and 1 - s the smaller
             const bool exps = softmax || far_below(m);
-            float x[kV], s[kV], xs = 0.0f, ss = 0.0f, fp = 0.0f;
+            float x[kV], low[kV], xs = 0.0f, ss = 0.0f, fp = 0.0f;
 #pragma unroll
             for (int v = 0; v < kV; ++v) {
                 x[v] = exp_near(l[v] - m);
                 xs += x[v];
-                s[v] = exps ? x[v] : sigmoid(l[v]);
-                ss += s[v];
-                fp += share[v] * s[v];
+                low[v] = exps ? x[v] : sigmoid_low(l[v]);
+                const float s = exps ? x[v] : sigmoid_of_low(l[v], low[v]);
+                ss += s;
+                fp += share[v] * s;
             }
             xs = group_sum<kLanes>(xs);
             ss = softmax ? xs : group_sum<kLanes>(ss);
@@ -718,22 +724,22 @@ __global__ __launch_bounds__(kGateThreads, kV < 32 ? 4 : 2) void k_gate_backward
                 r = rs > 0.0f ? r / rs : 0.0f;
                 dc = r * (g - group_sum<kLanes>(g * r));
                 if (!softmax)
-                    dc *= e >= 0 ? 1.0f - sigmoid(le) : 0.0f;
+                    dc *= e >= 0 ? sigmoid(-le) : 0.0f;
             } else if (softmax) {
                 r = e >= 0 ? expf(le - m) / xs : 0.0f;
                 dc = g * r;
                 all = group_sum<kLanes>(dc);
             } else {
-                r = e >= 0 ? sigmoid(le) : 0.0f;
-                dc = g * r * (1.0f - r);
+                const float lo = sigmoid_low(le);   // 0 without a choice
+                dc = g * lo * (1.0f - lo);
             }
             const float lse = m + logf(xs), rx = 1.0f / xs, rs = 1.0f / ss;
 #pragma unroll
             for (int v = 0; v < kV; ++v) {
                 const float q = x[v] * rx;
-                float b = gb * (s[v] * rs) * (share[v] - fp);
+                float b = gb * (low[v] * rs) * (share[v] - fp);
                 if (!exps)   // of far_below's, 1 to within e^-20
-                    b *= 1.0f - s[v];
+                    b *= 1.0f - low[v];
                 d[v] = b + (gz * lse - all) * q;
             }
             if (a.grad_weights)

@@ -43,3 +43,39 @@ def test_sigmoid_shares_far_below_zero(T, E, K, base):
     got = op.gate_backward(logits, _dev(idx), cfg, counts=_dev(counts), grad_losses=_dev(gl))
     ref, mag = _gradient(l.astype(np.float64), K, cfg, idx, None, counts, gl)
     assert (np.abs(got.double().cpu().numpy() - ref) <= 16 * REL * mag + 1e-37).all()
+
+
+@pytest.mark.parametrize("renormalize", [True, False])
+@pytest.mark.parametrize("base", [6.0, 10.0, 14.0, 18.0, 30.0])
+@pytest.mark.parametrize("T,E,K", [(40, 24, 4), (400, 24, 4), (20, 256, 8)])
+def test_sigmoid_slope_far_above_zero(T, E, K, base, renormalize):
+    """Gradients carry the factor 1 - s = sigma(-l), which 1 minus a rounded s
+    loses.  Every entry is a product with that factor (the rest of it bounded as
+    in _gradient), so the bound is relative to the product."""
+    rng = np.random.default_rng(T + E)
+    l = (base + rng.standard_normal((T, E))).astype(np.float32)
+    cfg = GateConfig("sigmoid", renormalize, 1.5)
+    op, logits = _op(T, E, K), _dev(l)
+    _, idx, counts, _ = [t.cpu().numpy() for t in op.gate(logits, cfg, balance=True)]
+    gw = rng.standard_normal((T, K)).astype(np.float32)
+    gl = np.array([0.5, 0.0], np.float32)
+    got = op.gate_backward(logits, _dev(idx), cfg, grad_weights=_dev(gw), counts=_dev(counts),
+                           grad_losses=_dev(gl)).double().cpu().numpy()
+    x = l.astype(np.float64)
+    s, slope = 1 / (1 + np.exp(-x)), 1 / (1 + np.exp(x))   # s and 1 - s
+    f = counts[:E] / (T * K)
+    p = s / s.sum(1, keepdims=True)
+    fp = (f * p).sum(1, keepdims=True)
+    ref = gl[0] * E / T * p * (f - fp) * slope
+    mag = gl[0] * E / T * p * (f + fp) * slope
+    sc, g = np.take_along_axis(s, idx, 1), 1.5 * gw.astype(np.float64)
+    if renormalize:
+        r = sc / sc.sum(1, keepdims=True)
+        gr = (g * r).sum(1, keepdims=True)
+        d, dm = r * (g - gr), r * (np.abs(g) + (np.abs(g) * r).sum(1, keepdims=True))
+    else:
+        d, dm = g * sc, np.abs(g) * sc
+    for t in range(T):
+        ref[t, idx[t]] += d[t] * slope[t, idx[t]]
+        mag[t, idx[t]] += dm[t] * slope[t, idx[t]]
+    assert (np.abs(got - ref) <= 16 * REL * mag + 1e-37).all()
