@@ -113,6 +113,10 @@ def _on_op_device(method):
 
 
 class EpDispatchCombineOp:
+    # phases sent to the side stream and not known to be over; unlike
+    # _sent_dispatch and _sent_combine they outlive a reset(), as the work does
+    _on_side = frozenset()
+
     def __init__(self, config: EpDispatchCombineConfig, device: Optional[torch.device] = None):
         self.config = config
         self.device = torch.device(device) if device is not None else torch.device(
@@ -293,6 +297,7 @@ class EpDispatchCombineOp:
         self._tokens = T
         self._last_dedup = False
         self._sent_dispatch = (weights is not None, scales is not None)
+        self._on_side |= {"dispatch"}
 
     def dispatch_recv(self):
         """Second phase: the caller's stream waits for the sent dispatch;
@@ -302,6 +307,7 @@ class EpDispatchCombineOp:
         B.epdc_dispatch_recv(self._op, self._stream())
         has_w, has_s = self._sent_dispatch
         self._sent_dispatch = None
+        self._on_side -= {"dispatch"}
         return (self.received_payload(), self._out_weights if has_w else None,
                 self.received_scales(has_s), self._out_indices, self._recv_count)
 
@@ -391,6 +397,7 @@ class EpDispatchCombineOp:
         B.epdc_combine_send(self._op, side.cuda_stream, _ptr(input), _ptr(weights), _ptr(indices),
                             _ptr(self._combined), _ptr(self._combined_weights))
         self._sent_combine = True
+        self._on_side |= {"combine"}
 
     def combine_recv(self) -> Tuple[torch.Tensor, torch.Tensor]:
         """Second phase: the caller's stream waits for the sent combine;
@@ -399,6 +406,7 @@ class EpDispatchCombineOp:
             raise B.EpdcError(B.EPDC_ERR_BAD_STATE, "combine_recv without a combine_send")
         B.epdc_combine_recv(self._op, self._stream())
         self._sent_combine = None
+        self._on_side -= {"combine"}
         T = self._tokens
         return self._combined[:T], self._combined_weights[:T]
 
@@ -561,6 +569,22 @@ class EpDispatchCombineOp:
             "scratch": torch.zeros(scratch, dtype=torch.uint8, device=dev),
         }
 
+    def _wait_for_side(self) -> None:
+        """The caller's stream waits for sent phases, which may still read the
+        gate's weights and indices."""
+        if not self._on_side:
+            return
+        captured = torch.cuda.is_current_stream_capturing()
+        if captured:
+            with torch.cuda.stream(self._side_stream):
+                inside = torch.cuda.is_current_stream_capturing()
+            if not inside:   # its end cannot be waited for from within a graph
+                raise B.EpdcError(B.EPDC_ERR_BAD_STATE, "gate is being captured while a phase "
+                                  "sent before the capture may still read its buffers")
+        torch.cuda.current_stream(self.device).wait_stream(self._side_stream)
+        if not captured:
+            self._on_side = frozenset()
+
     def _gate_args(self, logits, gate, bias, mask) -> L.epdc_gate_args:
         cfg = self.config
         if logits.dim() != 2 or logits.shape[1] != cfg.num_experts:
@@ -596,8 +620,10 @@ class EpDispatchCombineOp:
         them, and with balance also (counts int32 [E + 1], losses fp32 [2]):
         choices per expert followed by the number of tokens that took part, and
         the balance and z losses (epdc_layer.h gives the formulas).  All are
-        views of buffers of the op that the next gate() overwrites."""
+        views of buffers of the op that the next gate() overwrites; a dispatch or
+        combine that was sent and may still read them it waits for first."""
         args = self._gate_args(logits, gate, bias, mask)
+        self._wait_for_side()
         T = args.num_tokens
         g = self._gate
         if self._gate_cut[0] != T:
