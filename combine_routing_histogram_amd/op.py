@@ -116,6 +116,8 @@ class EpDispatchCombineOp:
     # phases sent to the side stream and not known to be over; unlike
     # _sent_dispatch and _sent_combine they outlive a reset(), as the work does
     _on_side = frozenset()
+    _sent_dispatch = _sent_combine = None
+    _routing_sent = False       # the last dispatch was sent and not received
 
     def __init__(self, config: EpDispatchCombineConfig, device: Optional[torch.device] = None):
         self.config = config
@@ -155,8 +157,6 @@ class EpDispatchCombineOp:
         self._payload_v = self._payload_view(self._out)
         self._combined_cut = (-1, None)   # (T, (output view, weights view))
         self._side_stream = None
-        self._sent_dispatch = None
-        self._sent_combine = None
         self.u_cap = config.max_tokens * min(config.topk, config.num_ranks)
         self._last_dedup = False
         self._staging = None
@@ -249,7 +249,7 @@ class EpDispatchCombineOp:
         if st:
             B._check(st)
         self._tokens = T
-        self._last_dedup = False
+        self._last_dedup = self._routing_sent = False
         return self._dispatch_views(weights, scales)
 
     def dispatch_replay(self, input: torch.Tensor, weights: Optional[torch.Tensor] = None,
@@ -297,6 +297,7 @@ class EpDispatchCombineOp:
         self._tokens = T
         self._last_dedup = False
         self._sent_dispatch = (weights is not None, scales is not None)
+        self._routing_sent = True
         self._on_side |= {"dispatch"}
 
     def dispatch_recv(self):
@@ -307,6 +308,7 @@ class EpDispatchCombineOp:
         B.epdc_dispatch_recv(self._op, self._stream())
         has_w, has_s = self._sent_dispatch
         self._sent_dispatch = None
+        self._routing_sent = False
         self._on_side -= {"dispatch"}
         return (self.received_payload(), self._out_weights if has_w else None,
                 self.received_scales(has_s), self._out_indices, self._recv_count)
@@ -472,6 +474,7 @@ class EpDispatchCombineOp:
                               _ptr(ub["indices"]), _ptr(ub["recv"]))
         self._tokens = T
         self._last_dedup = True
+        self._routing_sent = False
         self._unit_carried = (weights is not None, scales is not None)
         return self._unit_views(*self._unit_carried)
 
@@ -664,7 +667,11 @@ class EpDispatchCombineOp:
 
     # ---- the experts' products -------------------------------------------------------------
     def _routed(self) -> int:
-        """Rows the last dispatch may have written; raises if there is none."""
+        """Rows the last dispatch may have written; raises if there is none, or it
+        was sent and not received: its routing is still being written."""
+        if self._routing_sent:
+            raise B.EpdcError(B.EPDC_ERR_BAD_STATE, "the dispatch that was sent has not been "
+                              "received (dispatch_recv)")
         if self._tokens == 0:
             B.epdc_get_offsets(self._op)   # BAD_STATE without a recorded dispatch
         return self._tokens * self.config.topk
@@ -831,7 +838,7 @@ class EpDispatchCombineOp:
     def reset(self) -> None:
         B.epdc_reset(self._op)
         self._tokens = 0
-        self._last_dedup = False
+        self._last_dedup = self._routing_sent = False
         self._sent_dispatch = self._sent_combine = None
 
     def get_dispatch_src_token_pos(self) -> torch.Tensor:

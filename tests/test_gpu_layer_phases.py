@@ -64,3 +64,43 @@ def test_gate_between_send_and_recv_captured():
         torch.cuda.synchronize()
         for p, q in zip(outs, want):
             assert torch.equal(p, q)
+
+
+def _case(seed, T=300, H=256, E=16, K=4, R=4):
+    rng = np.random.default_rng(seed)
+    op = EpDispatchCombineOp(EpDispatchCombineConfig(T, H, K, E, R), DEV)
+    logits = normal(rng, (T, E), dtype=torch.float32)
+    w, idx = [t.clone() for t in op.gate(logits)]
+    return rng, op, w, idx, normal(rng, (T, H)), normal(rng, (E, 64, H), H ** -0.5)
+
+
+def _layer(op, rows, row_w, w1, dy):
+    """A product, its gradients and combine's and dispatch's, over given rows."""
+    z = torch.empty(rows.shape[0], w1.shape[1], dtype=torch.bfloat16, device=DEV)
+    h = op.expert_product(rows, w1, activation="silu", preact=z)
+    gx, gw, gb = op.expert_product_backward(h, rows, w1, activation="silu", preact=z, bias=True)
+    do, dw = op.combine_backward(dy, rows, row_w)
+    n = op.n_cap
+    return [t[:n].clone() for t in (h, gx, gw, gb, do, dw, op.dispatch_backward(gx))]
+
+
+@pytest.mark.parametrize("how", ["split", "replay", "dedup"])
+def test_products_behind_every_kind_of_dispatch(how):
+    """Split phases, a replay of the routing and the expanded unit rows leave the
+    rows and the routing of a plain dispatch, so everything behind is equal."""
+    rng, op, w, idx, x, w1 = _case(5)
+    dy = normal(rng, tuple(x.shape))
+    rows, row_w, _, _, _ = op.dispatch(x, w, None, idx)
+    want = _layer(op, rows, row_w, w1, dy)
+    if how == "split":
+        op.dispatch(torch.zeros_like(x), w, None, torch.zeros_like(idx))
+        op.dispatch_send(x, w, None, idx)
+        got = op.dispatch_recv()
+    elif how == "replay":
+        op.dispatch(torch.zeros_like(x), w, None, idx)
+        got = op.dispatch_replay(x, w)
+    else:
+        op.dispatch_dedup(x, w, None, idx)
+        got = op.units_to_experts()
+    for a, b in zip(_layer(op, got[0], got[1], w1, dy), want):
+        assert torch.equal(a, b)

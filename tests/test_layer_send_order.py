@@ -121,3 +121,30 @@ def test_gate_in_a_capture_refuses_a_send_from_outside_it(traced, monkeypatch):
     monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
     op.gate(LOGITS)
     assert log == ["caller waits for side", "gate"]
+
+
+def test_products_and_gradients_refuse_a_dispatch_not_received(traced, monkeypatch):
+    """They read the routing that the sent dispatch is still writing."""
+    op, log = traced
+    _send(op)
+    monkeypatch.setattr(B, "epdc_get_offsets", lambda op: (4096, 4096))
+    monkeypatch.setattr(B, "epdc_get_routing", lambda op: (4096, 4096, 4096))
+    for mod, name in ((L, "epdc_expert_product"), (L, "epdc_expert_backward"),
+                      (L, "epdc_combine_backward"), (B, "epdc_combine")):
+        monkeypatch.setattr(mod, name, lambda *a, _n=name[5:]: log.append(_n))
+    bf = torch.bfloat16
+    x, w, g = torch.zeros(64, 256, dtype=bf), torch.zeros(8, 64, 256, dtype=bf), \
+        torch.zeros(64, 64, dtype=bf)
+    calls = [lambda: op.expert_product(x, w), lambda: op.expert_product_backward(g, x, w),
+             lambda: op.combine_backward(torch.zeros(16, 256, dtype=bf), x),
+             lambda: op.dispatch_backward(x)]
+    del log[:]
+    for call in calls:
+        with pytest.raises(B.EpdcError) as ei:
+            call()
+        assert ei.value.status == B.EPDC_ERR_BAD_STATE and log == []
+    op.dispatch_recv()
+    del log[:]
+    for call in calls:
+        call()
+    assert log == ["expert_product", "expert_backward", "combine_backward", "combine"]
