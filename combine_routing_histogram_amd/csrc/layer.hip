@@ -50,6 +50,7 @@ epdc_status launch(const char *name, F &&f)
 
 constexpr int kMaxFeatures = 1 << 20;
 constexpr int64_t kMaxExpertBytes = (int64_t)0x7fff0000;
+constexpr int64_t kMaxThreads = (int64_t)0xffffffff;  // of a launch, in all its blocks
 
 int gate_blocks(int64_t tokens, int experts, int limit)
 {
@@ -270,6 +271,18 @@ epdc_status launch_forward(hipStream_t st, ProductArgs &a, int64_t mean)
     if (mean <= 64)
         return launch_tile<kE4m3, 1>(st, a);
     return launch_tile<kE4m3, 4>(st, a);
+}
+
+void launch_combine_grad(int grid, hipStream_t st, const CombineGradArgs &a)
+{
+    switch (a.topk) {
+    case 1: k_combine_grad<1><<<grid, kCombineGradThreads, 0, st>>>(a); break;
+    case 2: k_combine_grad<2><<<grid, kCombineGradThreads, 0, st>>>(a); break;
+    case 4: k_combine_grad<4><<<grid, kCombineGradThreads, 0, st>>>(a); break;
+    case 6: k_combine_grad<6><<<grid, kCombineGradThreads, 0, st>>>(a); break;
+    case 8: k_combine_grad<8><<<grid, kCombineGradThreads, 0, st>>>(a); break;
+    default: k_combine_grad<0><<<grid, kCombineGradThreads, 0, st>>>(a); break;
+    }
 }
 
 }  // namespace
@@ -538,17 +551,16 @@ epdc_status epdc_combine_backward(void *stream, int32_t num_tokens, int32_t topk
     a.grad_input = static_cast<uint8_t *>(grad_input);
     a.grad_weights = grad_weights;
     hipStream_t st = static_cast<hipStream_t>(stream);
-    const epdc_status s = launch("k_combine_grad", [&] {
-        switch (topk) {
-        case 1: k_combine_grad<1><<<num_tokens, kCombineGradThreads, 0, st>>>(a); break;
-        case 2: k_combine_grad<2><<<num_tokens, kCombineGradThreads, 0, st>>>(a); break;
-        case 4: k_combine_grad<4><<<num_tokens, kCombineGradThreads, 0, st>>>(a); break;
-        case 6: k_combine_grad<6><<<num_tokens, kCombineGradThreads, 0, st>>>(a); break;
-        case 8: k_combine_grad<8><<<num_tokens, kCombineGradThreads, 0, st>>>(a); break;
-        default: k_combine_grad<0><<<num_tokens, kCombineGradThreads, 0, st>>>(a); break;
-        }
-    });
-    return s == EPDC_SUCCESS ? ok() : s;
+    // one launch, unless there are more tokens than it holds blocks
+    constexpr int kBlocks = (int)(kMaxThreads / kCombineGradThreads);
+    for (int64_t first = 0; first < num_tokens; first += kBlocks) {
+        a.first = (int)first;
+        const int grid = (int)(num_tokens - first < kBlocks ? num_tokens - first : kBlocks);
+        const epdc_status s = launch("k_combine_grad", [&] { launch_combine_grad(grid, st, a); });
+        if (s != EPDC_SUCCESS)
+            return s;
+    }
+    return ok();
 }
 
 const char *epdc_layer_last_error(void) { return g_last_error.c_str(); }

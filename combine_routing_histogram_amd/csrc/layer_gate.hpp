@@ -791,6 +791,7 @@ __global__ __launch_bounds__(kGateThreads, kV < 32 ? 4 : 2) void k_gate_backward
 
 struct CombineGradArgs {
     int32_t tokens, topk, row_vecs;  // 16-byte vectors of a row
+    int32_t first;                   // token of the launch's first block
     const int32_t *slot_of;
     const uint8_t *grad_output, *input;
     const float *weights;
@@ -811,7 +812,7 @@ __global__ __launch_bounds__(kCombineGradThreads) void k_combine_grad(const Comb
     constexpr int kMax = kTopk ? kTopk : kMaxTopk, kWaves = kCombineGradThreads / 64;
     __shared__ float part[kWaves][kMax];
     const int K = kTopk ? kTopk : a.topk;
-    const int64_t t = blockIdx.x;
+    const int64_t t = (int64_t)a.first + blockIdx.x;
     const int lane = threadIdx.x & 63, wave = threadIdx.x / 64;
     int slot[kMax];
     float w[kMax], dot[kMax];
