@@ -197,10 +197,10 @@ int64_t row_tile_bound(int64_t rows, int experts, int bm)
 }
 
 // Blocks for `tiles` tiles: whole rounds of one run per XCD (tile_number).
-epdc_status grid_of(int64_t tiles, int *grid)
+epdc_status grid_of(int64_t tiles, int threads, int *grid)
 {
     const int64_t round = kXcds * kRun, g = (tiles + round - 1) / round * round;
-    if (g > 0x7fffffff)
+    if (g > kMaxThreads / threads)
         return fail(EPDC_ERR_INVALID_ARGS, "more tiles than a launch can hold");
     *grid = (int)g;
     return EPDC_SUCCESS;
@@ -220,7 +220,7 @@ epdc_status plan_tiles(ProductArgs &a, int *grid)
     } else {
         tiles = row_tile_bound(a.rows, a.experts, kGroups * 64) * a.col_tiles;
     }
-    return grid_of(tiles, grid);
+    return grid_of(tiles, kTileWaves * kWave, grid);
 }
 
 template <bool kE4m3, int kGroups>
@@ -240,7 +240,8 @@ epdc_status launch_stream(hipStream_t st, ProductArgs &a)
 {
     a.col_tiles = (a.out_cols + 15) / 16;
     int grid;
-    const epdc_status s = grid_of(row_tile_bound(a.rows, a.experts, kMI * 16) * a.col_tiles, &grid);
+    const epdc_status s = grid_of(row_tile_bound(a.rows, a.experts, kMI * 16) * a.col_tiles,
+                                  kStreamWaves * kWave, &grid);
     if (s != EPDC_SUCCESS)
         return s;
     return launch("k_product_stream", [&] {
@@ -504,7 +505,7 @@ epdc_status epdc_expert_backward(const epdc_product_args *args, void *stream,
         g.bias_cols = (of + kWave * 8 - 1) / (kWave * 8);
         blocks += (int64_t)args->num_experts * g.bias_cols;
     }
-    if (blocks > 0x7fffffff)
+    if (blocks > kMaxThreads / (kTileWaves * kWave))
         return fail(EPDC_ERR_INVALID_ARGS, "more tiles than a launch can hold");
     if (blocks > 0) {
         s = launch("k_product_grads", [&] {

@@ -135,6 +135,9 @@ epdc_status epdc_gate_backward(const epdc_gate_args *args, void *stream, const i
  *   z = input[s, :] . weight[e]^T + bias[e]
  *   out[s, :] = round(act(z) + residual[s, :])
  * Rows outside [expert_off[0], expert_off[num_experts]) are left as they were.
+ * Each call is one launch of fewer than 2^32 threads (512 for a tile of 256
+ * columns by 64 or 256 rows, 256 for one of 16 columns by 16 or 32 rows); a
+ * call of more tiles is refused.
  *   bf16: in_features and out_features multiples of 8 (gated: out_features a
  *         multiple of 16).
  *   e4m3: in_features a multiple of 128; scales [rows, in/128] fp32 (the
