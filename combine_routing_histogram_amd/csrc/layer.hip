@@ -440,30 +440,12 @@ epdc_status epdc_expert_backward(const epdc_product_args *args, void *stream,
                     "payload arrays must be 16-byte aligned, grad_bias 4-byte aligned");
     hipStream_t st = static_cast<hipStream_t>(stream);
     const int in = args->in_features, of = args->out_features;
-    const void *z = grad_out;
-    if (act && args->rows > 0 && (grad_input || grad_weight)) {
-        ActGradArgs g = {};
-        g.rows = args->rows;
-        g.experts = args->num_experts;
-        g.act = args->activation;
-        g.cols = act_gated(g.act) ? of / 2 : of;
-        g.expert_off = args->expert_off;
-        g.grad_out = static_cast<const uint16_t *>(grad_out);
-        g.preact = static_cast<const uint16_t *>(preact);
-        g.dz = static_cast<uint16_t *>(dz);
-        const int blocks = (args->rows + kActRows - 1) / kActRows;
-        s = launch("k_act_grad", [&] {
-            k_act_grad<<<blocks < 16384 ? blocks : 16384, dim3(kWave, kActRows), 0, st>>>(g);
-        });
-        if (s != EPDC_SUCCESS)
-            return s;
-        z = dz;
-    }
+    const bool with_dz = act && args->rows > 0 && (grad_input || grad_weight);
     ProductArgs a = {};
     a.rows = args->rows;
     a.experts = args->num_experts;
     a.weight_rows = of;
-    a.p = static_cast<const uint8_t *>(z);
+    a.p = static_cast<const uint8_t *>(with_dz ? dz : grad_out);
     a.p_bytes = of * 2;
     a.q_bytes = in * 2;
     a.out_cols = in;
@@ -507,6 +489,23 @@ epdc_status epdc_expert_backward(const epdc_product_args *args, void *stream,
     }
     if (blocks > kMaxThreads / (kTileWaves * kWave))
         return fail(EPDC_ERR_INVALID_ARGS, "more tiles than a launch can hold");
+    if (with_dz) {
+        ActGradArgs d = {};
+        d.rows = args->rows;
+        d.experts = args->num_experts;
+        d.act = args->activation;
+        d.cols = act_gated(d.act) ? of / 2 : of;
+        d.expert_off = args->expert_off;
+        d.grad_out = static_cast<const uint16_t *>(grad_out);
+        d.preact = static_cast<const uint16_t *>(preact);
+        d.dz = static_cast<uint16_t *>(dz);
+        const int rounds = (args->rows + kActRows - 1) / kActRows;
+        s = launch("k_act_grad", [&] {
+            k_act_grad<<<rounds < 16384 ? rounds : 16384, dim3(kWave, kActRows), 0, st>>>(d);
+        });
+        if (s != EPDC_SUCCESS)
+            return s;
+    }
     if (blocks > 0) {
         s = launch("k_product_grads", [&] {
             if (few)

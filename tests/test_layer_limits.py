@@ -44,3 +44,13 @@ def test_backward(rows, experts, fin, fout, gx, gw):
     with pytest.raises(B.EpdcError) as ei:
         L.epdc_expert_backward(args, 0, 4 * A, 0, 0, gx, gw, L.EPDC_DT_BF16, 0)
     assert ei.value.status == B.EPDC_ERR_INVALID_ARGS and "launch" in str(ei.value)
+
+
+def test_backward_refuses_before_the_activation_is_launched():
+    """A status other than SUCCESS leaves nothing enqueued: without a GPU the
+    launch of the activation's gradient would show as another status."""
+    args = L.make_product_args(1, 512, 1 << 20, 776, activation=L.EPDC_ACT_SILU, input=A,
+                               weight=2 * A, expert_off=3 * A)
+    with pytest.raises(B.EpdcError) as ei:
+        L.epdc_expert_backward(args, 0, 4 * A, 8 * A, 9 * A, 0, 6 * A, L.EPDC_DT_BF16, 0)
+    assert ei.value.status == B.EPDC_ERR_INVALID_ARGS and "tiles" in str(ei.value)
