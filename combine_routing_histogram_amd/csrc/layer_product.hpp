@@ -73,7 +73,33 @@ __device__ inline float act_silu(float x)
 {
     return x * __builtin_amdgcn_rcpf(1.0f + __expf(-x));
 }
-__device__ inline float act_gelu(float x) { return 0.5f * x * (1.0f + erff(x * 0.70710678f)); }
+// The normal distribution function, and e^(-x^2 / 2), which it goes through.  By way
+// of 1 + erf its tail would cancel: at -5 several percent of it are lost, below
+// -5.5 all.  Its tail times e^(x^2 / 2) is smooth and falls like 1 / x: s P(s) with
+// s = 1 / (1 + 0.305 |x|), P of degree 7 by least squares reweighted toward the
+// largest relative error over [0, 14], which is 2^-23; with the exponential's
+// argument rounded 2^-18 at 8.  (gelu over 32768 x 512 x 4096 and its gradients:
+// 350 and 818 us with 1 + erff, 386 and 858 with erfcf, 284 and 756 so.)
+__device__ inline float normal_cdf(float x, float &e)
+{
+    const float s = __builtin_amdgcn_rcpf(__builtin_fmaf(0.305f, fabsf(x), 1.0f));
+    e = __builtin_amdgcn_exp2f(x * x * -0.72134752f);
+    float p = 0.0366991945f;
+    p = __builtin_fmaf(p, s, -0.15298833f);
+    p = __builtin_fmaf(p, s, 0.185716927f);
+    p = __builtin_fmaf(p, s, -0.0379768424f);
+    p = __builtin_fmaf(p, s, 0.121021688f);
+    p = __builtin_fmaf(p, s, 0.103420861f);
+    p = __builtin_fmaf(p, s, 0.122466817f);
+    p = __builtin_fmaf(p, s, 0.121639736f);
+    const float tail = p * s * e;
+    return x < 0.0f ? tail : 1.0f - tail;
+}
+__device__ inline float act_gelu(float x)
+{
+    float e;
+    return x * normal_cdf(x, e);
+}
 
 __device__ inline float act_one(int act, float x)
 {
@@ -92,9 +118,11 @@ __device__ inline float act_one_grad(int act, float x)
     switch (act) {
     case kActRelu: return x > 0.0f ? 1.0f : (x != x ? x : 0.0f);
     case kActGelu:
-    case kActGeglu:
-        return 0.5f * (1.0f + erff(x * 0.70710678f)) +
-               x * 0.39894228f * __expf(-0.5f * x * x);
+    case kActGeglu: {
+        float e;
+        const float cdf = normal_cdf(x, e);
+        return __builtin_fmaf(x * 0.39894228f, e, cdf);
+    }
     case kActSilu:
     case kActSwiglu: {
         const float s = __builtin_amdgcn_rcpf(1.0f + __expf(-x));
