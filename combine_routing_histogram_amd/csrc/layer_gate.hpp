@@ -304,10 +304,17 @@ __device__ inline float sigmoid(float l) { return sigmoid_of_low(l, sigmoid_low(
 // the softmax's, whose terms e^(l - m) do not vanish together as the s do.
 __device__ inline bool far_below(float m) { return m < -20.0f; }
 
-// Keys with a bias, s + b, are rounded sums of rounded scores.  In fp32 s is
-// off by a few ulp of at most 1 and the sum by half an ulp of the key, so two
-// neighbours of the order further apart than this are certainly in order.
-__device__ inline float key_slack(float k) { return 1.5e-6f + 2.5e-7f * fabsf(k); }
+// Keys with a bias, s + b, are rounded sums of rounded scores; two neighbours of
+// the order further apart than this are certainly in order.  In units of 2^-24:
+// a softmax's sum has at most kV + 5 additions (kV - 1 in the lane, 4 or 6 across)
+// of terms off by 4, its inverse and the product by one each, its terms' own 4
+// count once, since the two scores add up to at most 1: kV + 15.  A sigmoid
+// is off by 5, two of them by 10.  The sum s + b is off by half an ulp of each key.
+template <int kV>
+__device__ inline float key_slack(float k)
+{
+    return (kV + 16) * 5.9604645e-8f + 2.5e-7f * fabsf(k);
+}
 
 __device__ inline void store_agent(float *p, float v)
 {
@@ -481,7 +488,7 @@ __global__ __launch_bounds__(kGateThreads, kV < 32 ? 4 : 2) void k_gate(const Ga
                 take_top<kLanes, kV>(key, j, best, e);
                 if (e < 0)
                     break;
-                const bool near = before - best <= key_slack(best);
+                const bool near = before - best <= key_slack<kV>(best);
                 if (k >= K && !near)
                     break;
                 close |= near;

@@ -79,3 +79,29 @@ def test_sigmoid_slope_far_above_zero(T, E, K, base, renormalize):
         ref[t, idx[t]] += d[t] * slope[t, idx[t]]
         mag[t, idx[t]] += dm[t] * slope[t, idx[t]]
     assert (np.abs(got - ref) <= 16 * REL * mag + 1e-37).all()
+
+
+@pytest.mark.parametrize("T", [100, 8200])   # a wave per token, four tokens to a wave
+def test_order_where_the_softmax_sum_is_at_its_worst(T):
+    """Exact order of keys although the fp32 sum of the row is off as far as it can
+    be: beside e^0 = 1 every other term is just below half an ulp of 1 and is lost
+    from the lane's sum, so the one large score comes out too large, and its
+    rival's key lies between its true and its rounded one."""
+    E = 512
+    l = np.full(E, -16.6356, np.float32)   # e^l = 0.99996 * 2^-24
+    l[0] = 0.0
+    x = np.exp(l.astype(np.float64))
+    s = x / x.sum()
+    rival = 300
+    bias = np.full(E, -8.0, np.float32)
+    bias[0] = -1.0 + 2.0 ** -15
+    for above in (1e-7, 3e-7, 6e-7, 1e-6, -1e-7):   # of the rival's key over the exact one
+        bias[rival] = s[0] + float(bias[0]) + above - s[rival]
+        key = s + bias.astype(np.float64)
+        best = int(np.argmax(key))
+        assert best == (rival if above > 0 else 0)
+        op = _op(T, E, 1)
+        logits = _dev(np.tile(l, (T, 1)))
+        for balance in (False, True):
+            idx = op.gate(logits, GateConfig(), bias=_dev(bias), balance=balance)[1]
+            assert bool((idx == best).all()), (above, balance)
