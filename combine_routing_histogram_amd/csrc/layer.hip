@@ -9,6 +9,7 @@
 
 #include <cstdarg>
 #include <cstdio>
+#include <initializer_list>
 #include <string>
 
 using namespace epdc_layer;
@@ -35,6 +36,28 @@ epdc_status ok()
 }
 
 bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+
+// An array of a call, NULL if it has none or does not touch it.
+struct Array {
+    const char *name;
+    const void *at;
+    int64_t bytes;
+};
+
+bool overlap(const Array &a, const Array &b)
+{
+    const uintptr_t p = (uintptr_t)a.at, q = (uintptr_t)b.at;
+    return p && q && p < q + (uint64_t)b.bytes && q < p + (uint64_t)a.bytes;
+}
+
+// An output that shares no byte with the others; SUCCESS sets no message.
+epdc_status check_apart(const Array &out, std::initializer_list<Array> others)
+{
+    for (const Array &o : others)
+        if (overlap(out, o))
+            return fail(EPDC_ERR_INVALID_ARGS, "%s may not overlap %s", out.name, o.name);
+    return EPDC_SUCCESS;
+}
 
 template <typename F>
 epdc_status launch(const char *name, F &&f)
@@ -180,6 +203,23 @@ epdc_status check_product(const epdc_product_args *p)
         return fail(EPDC_ERR_INVALID_ARGS, "input, weight and bias must be 16-byte aligned, the "
                                            "other arrays 4-byte aligned");
     return EPDC_SUCCESS;
+}
+
+// The arrays that a product's arguments name.
+struct Operands {
+    Array input, scales, weight, weight_scales, bias, offsets;
+};
+
+Operands operands(const epdc_product_args &p)
+{
+    const int64_t rows = p.rows, experts = p.num_experts, in = p.in_features, of = p.out_features;
+    const int64_t elem = p.dtype == EPDC_DT_E4M3 ? 1 : 2, blocks = in / 128;
+    return {{"input", p.input, rows * in * elem},
+            {"scales", p.scales, rows * blocks * 4},
+            {"weight", p.weight, experts * of * in * elem},
+            {"weight_scales", p.weight_scales, experts * ((of + 127) / 128) * blocks * 4},
+            {"bias", p.bias, experts * of * 4},
+            {"expert_off", p.expert_off, (experts + 1) * 4}};
 }
 
 int64_t mean_rows(const epdc_product_args &p)
@@ -391,6 +431,19 @@ epdc_status epdc_expert_product(const epdc_product_args *args, void *stream, con
         return fail(EPDC_ERR_INVALID_ARGS, "residual, out and preact must be 16-byte aligned");
     if (args->rows == 0)
         return ok();
+    const int cols =
+        act_gated(args->activation) ? args->out_features / 2 : args->out_features;
+    const Operands in = operands(*args);
+    const Array to = {"out", out, (int64_t)args->rows * cols * 2},
+                z = {"preact", preact, (int64_t)args->rows * args->out_features * 2},
+                res = {"residual", residual, to.bytes};
+    s = check_apart(to, {in.input, in.scales, in.weight, in.weight_scales, in.bias, in.offsets, z,
+                         residual == out ? Array{} : res});  // an element's own residual is read first
+    if (s == EPDC_SUCCESS)
+        s = check_apart(z, {in.input, in.scales, in.weight, in.weight_scales, in.bias, in.offsets,
+                            res});
+    if (s != EPDC_SUCCESS)
+        return s;
     ProductArgs a = {};
     a.rows = args->rows;
     a.experts = args->num_experts;
@@ -398,7 +451,7 @@ epdc_status epdc_expert_product(const epdc_product_args *args, void *stream, con
     a.p_bytes = a.q_bytes = args->in_features * (e4m3 ? 1 : 2);
     a.weight_rows = args->out_features;
     a.act = args->activation;
-    a.out_cols = act_gated(a.act) ? args->out_features / 2 : args->out_features;
+    a.out_cols = cols;
     a.p = static_cast<const uint8_t *>(args->input);
     a.q = static_cast<const uint8_t *>(args->weight);
     a.scales = args->scales;
@@ -441,6 +494,36 @@ epdc_status epdc_expert_backward(const epdc_product_args *args, void *stream,
     hipStream_t st = static_cast<hipStream_t>(stream);
     const int in = args->in_features, of = args->out_features;
     const bool with_dz = act && args->rows > 0 && (grad_input || grad_weight);
+    {
+        const Operands r = operands(*args);
+        const bool gated = act_gated(args->activation), rows = args->rows > 0;
+        const int64_t z_bytes = (int64_t)args->rows * of * 2;
+        // what the products and the biases read behind the activation's gradient
+        const Array dy = {"grad_out", rows ? grad_out : nullptr, gated ? z_bytes / 2 : z_bytes},
+                    z = {"preact", act && rows ? preact : nullptr, z_bytes},
+                    d = {"dz", with_dz ? dz : nullptr, z_bytes},
+                    x = grad_weight && rows ? r.input : Array{},
+                    w = grad_input && rows ? r.weight : Array{},
+                    dy_read = with_dz && !grad_bias ? Array{} : dy,
+                    z_read = grad_bias ? z : Array{};
+        const Array gx = {"grad_input", rows ? grad_input : nullptr, r.input.bytes},
+                    gw = {"grad_weight", grad_weight,
+                          r.weight.bytes * (grad_weight_dtype == EPDC_DT_FP32 ? 2 : 1)},
+                    gb = {"grad_bias", grad_bias, r.bias.bytes};
+        // dz may take the place of one of its factors, element by element, unless
+        // the biases' gradient reads that again
+        const bool on_z = dz == preact && !grad_bias,
+                   on_dy = dz == grad_out && !gated && !grad_bias;
+        s = check_apart(d, {x, w, on_z ? Array{} : z, on_dy ? Array{} : dy, r.offsets});
+        if (s == EPDC_SUCCESS)
+            s = check_apart(gx, {x, w, d, dy_read, z_read, gw, gb, r.offsets});
+        if (s == EPDC_SUCCESS)
+            s = check_apart(gw, {x, w, d, dy_read, z_read, gb, r.offsets});
+        if (s == EPDC_SUCCESS)
+            s = check_apart(gb, {x, w, d, dy_read, z_read, r.offsets});
+        if (s != EPDC_SUCCESS)
+            return s;
+    }
     ProductArgs a = {};
     a.rows = args->rows;
     a.experts = args->num_experts;
@@ -540,6 +623,19 @@ epdc_status epdc_combine_backward(void *stream, int32_t num_tokens, int32_t topk
                     "rows must be 16-byte aligned, the other arrays 4-byte aligned");
     if (num_tokens == 0 || (!grad_input && !grad_weights))
         return ok();
+    const int64_t pairs = (int64_t)num_tokens * topk;
+    const Array slots = {"slot_of", slot_of, pairs * 4},
+                dy = {"grad_output", grad_output, (int64_t)num_tokens * hidden * 2},
+                x = {"input", grad_weights ? input : nullptr, pairs * hidden * 2},
+                w = {"weights", weights, pairs * topk * 4},
+                gx = {"grad_input", grad_input, x.bytes},
+                gw = {"grad_weights", grad_weights, pairs * 4};
+    // a row's gradient may take its place: the thread that writes an element has read it
+    epdc_status apart = check_apart(gx, {slots, dy, grad_input == input ? Array{} : x, w, gw});
+    if (apart == EPDC_SUCCESS)
+        apart = check_apart(gw, {slots, dy, x, w});
+    if (apart != EPDC_SUCCESS)
+        return apart;
     CombineGradArgs a = {};
     a.tokens = num_tokens;
     a.topk = topk;

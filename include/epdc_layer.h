@@ -167,7 +167,8 @@ typedef struct epdc_product_args {
 
 /* residual [rows, cols] bf16 or NULL; out [rows, cols] bf16, cols = out_features
  * (gated: half of it); preact [rows, out_features] bf16 or NULL: z, rounded, for
- * expert_backward.  out may not overlap an input, except residual itself. */
+ * expert_backward.  out and preact may overlap neither each other nor an input,
+ * except that out may be residual itself. */
 epdc_status epdc_expert_product(const epdc_product_args *args, void *stream, const void *residual,
                                 void *out, void *preact);
 
@@ -184,6 +185,8 @@ epdc_status epdc_expert_product(const epdc_product_args *args, void *stream, con
  *   dz           [rows, out_features] bf16 workspace; NULL for EPDC_ACT_NONE, or
  *                when only grad_bias is asked for
  *   grad_weight  [E, out, in] in grad_weight_dtype (EPDC_DT_BF16 or EPDC_DT_FP32)
+ * Outputs and dz may overlap neither each other nor anything the call reads;
+ * without grad_bias dz may be preact itself or (not gated) grad_out itself.
  */
 epdc_status epdc_expert_backward(const epdc_product_args *args, void *stream,
                                  const void *grad_out, const void *preact, void *dz,
@@ -197,7 +200,8 @@ epdc_status epdc_expert_backward(const epdc_product_args *args, void *stream,
  *   grad_weights[t, k] = sum_h grad_output[t, h] * input[s, h]
  * A pair without a slot gets grad_weights 0; rows without a pair are left as
  * they were.  slot_of is epdc_get_routing's.  grad_weights may be NULL (input
- * is then not read and may be NULL); grad_input may be NULL.
+ * is then not read and may be NULL); grad_input may be NULL.  The outputs may
+ * overlap neither each other nor an input, except that grad_input may be input.
  */
 epdc_status epdc_combine_backward(void *stream, int32_t num_tokens, int32_t topk, int32_t hidden,
                                   const int32_t *slot_of, const void *grad_output,
