@@ -767,14 +767,20 @@ class EpDispatchCombineOp:
                                 preact: Optional[torch.Tensor] = None, bias: bool = False,
                                 first_expert: int = 0, need_input: bool = True,
                                 need_weight: bool = True,
-                                weight_dtype: torch.dtype = torch.bfloat16):
+                                weight_dtype: torch.dtype = torch.bfloat16,
+                                grad_input: Optional[torch.Tensor] = None):
         """Gradients of a bf16 expert_product.
 
         grad_output: bf16 rows like its result; preact: what the forward filled
         (with an activation).  Returns (grad_input bf16 [T*K, in], grad_weight
         [n, out, in] in weight_dtype (bfloat16 or float32), grad_bias fp32 [n,
         out]); None for what is not asked for.  Experts without rows get zero
-        weight and bias gradients.  The residual's gradient is grad_output."""
+        weight and bias gradients.  The residual's gradient is grad_output.
+
+        grad_input: a bf16 buffer [>= T*K, in] of which only the rows of these
+        experts are written, so that ranks can share one.  Without it a call over
+        some of the experts returns zeros in all other rows; a call over all of
+        them leaves the rows behind the last expert's, which hold no pair, unset."""
         rows = self._routed()
         if weight.dtype != torch.bfloat16:
             raise ValueError("the gradients take bf16 operands")
@@ -782,6 +788,10 @@ class EpDispatchCombineOp:
             raise ValueError("weight_dtype must be bfloat16 or float32")
         args = self._product_args(rows, input, weight, None, None, None, activation, first_expert)
         n, out_f, in_f = weight.shape
+        if grad_input is not None:
+            if not need_input:
+                raise ValueError("grad_input is given but not asked for")
+            self._need_rows(grad_input, "grad_input", rows, in_f)
         self._need_rows(grad_output, "grad_output", rows,
                         out_f // 2 if activation in GATED else out_f)
         dz = None
@@ -794,7 +804,10 @@ class EpDispatchCombineOp:
             if need_input or need_weight:
                 dz = torch.empty((rows, out_f), dtype=torch.bfloat16, device=self.device)
         new = lambda shape, dtype: torch.empty(shape, dtype=dtype, device=self.device)
-        grad_input = new((rows, in_f), torch.bfloat16) if need_input else None
+        if need_input and grad_input is None:
+            grad_input = new((rows, in_f), torch.bfloat16)
+            if n < self.config.num_experts:
+                grad_input.zero_()
         grad_weight = new((n, out_f, in_f), weight_dtype) if need_weight else None
         grad_bias = new((n, out_f), torch.float32) if bias else None
         L.epdc_expert_backward(args, self._stream(), grad_output.data_ptr(), _ptr(preact),
