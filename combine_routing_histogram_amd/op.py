@@ -712,8 +712,9 @@ class EpDispatchCombineOp:
         if bias is not None:
             self._need(bias, "bias", torch.float32, (n, out_f))
         off, _ = B.epdc_get_offsets(self._op)
+        expected = max(1, rows * n // cfg.num_experts)   # 0 would stand for all rows
         return L.make_product_args(rows, n, in_f, out_f, dtype, ACTIVATIONS[activation],
-                                   rows * n // cfg.num_experts, input.data_ptr(), _ptr(scales),
+                                   expected, input.data_ptr(), _ptr(scales),
                                    weight.data_ptr(), _ptr(weight_scales), _ptr(bias),
                                    off + 4 * first_expert)
 

@@ -34,3 +34,18 @@ def test_backward_takes_a_buffer_for_the_rows_gradient(op):
     with pytest.raises(ValueError):
         op.expert_product_backward(g, x, w, grad_input=ok, need_input=False)
     assert len(op.calls) == 1
+
+
+@pytest.mark.parametrize("first,n,expected", [(0, 8, 40), (0, 4, 20), (7, 1, 5)])
+def test_expected_rows(op, first, n, expected):
+    x, w = torch.zeros(40, 256, dtype=BF), torch.zeros(n, 64, 256, dtype=BF)
+    op.expert_product(x, w, first_expert=first, out=torch.empty(40, 64, dtype=BF))
+    assert op.calls[0][0].expected_rows == expected
+
+
+def test_expected_rows_of_fewer_than_one(op):
+    """0 would mean all of the rows, and the form for many."""
+    op._tokens = 1
+    x, w = torch.zeros(4, 256, dtype=BF), torch.zeros(1, 64, 256, dtype=BF)
+    op.expert_product(x, w, first_expert=3, out=torch.empty(4, 64, dtype=BF))
+    assert op.calls[0][0].expected_rows == 1
