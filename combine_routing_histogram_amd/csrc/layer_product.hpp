@@ -276,7 +276,9 @@ __device__ inline __amdgpu_buffer_rsrc_t buffer_at(const uint8_t *base, uint32_t
 // because the compiler, which cannot tell the two buffers of a tile apart,
 // else waits for every such load before a transposing LDS read; when they have
 // landed is wait_and_meet's business.  Nothing returns to registers.  M0 holds
-// the LDS address; the compiler itself has no use for M0 in these kernels.
+// the LDS address.  It is reserved to the compiler, which takes it neither as
+// a clobber nor reliably as an operand of asm; so it is set in the same block as
+// its use, and the compiler's own code may not use it (tests/test_layer_asm.py).
 __device__ __forceinline__ void load_direct(__amdgpu_buffer_rsrc_t at, uint32_t off, uint8_t *lds)
 {
     const int to = uniform((int)(uint32_t)(uintptr_t)(lds_byte *)lds);
