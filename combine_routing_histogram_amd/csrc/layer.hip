@@ -82,14 +82,6 @@ int gate_blocks(int64_t tokens, int experts, int limit)
     return (int)(b < 1 ? 1 : (b < limit ? b : limit));
 }
 
-// Blocks of a balance: in small batches half as many, whose sums take half as
-// long to add (4093 x 128: 17.9 us for the forward, with 512 blocks 18.9).
-int balance_blocks(int64_t tokens, int experts)
-{
-    return gate_blocks(tokens, experts,
-                       gate_lanes(tokens, experts) == 64 ? kGateMaxBlocks / 2 : kGateMaxBlocks);
-}
-
 epdc_status check_gate(const epdc_gate_args *g)
 {
     if (!g)
@@ -301,8 +293,9 @@ epdc_status launch_forward(hipStream_t st, ProductArgs &a, int64_t mean)
     // experts of 4096 x 4096, streamed (16), streamed (32), 64-row tiles: bf16 mean
     // 8: 327, 346, 393 us; 12: 355, 337, 394; 24: -, 366, 405; 32: -, 578, 409.
     // e4m3: 12: 195, 239, 238; 16: 261, 253, 236 (with 32 rows its registers
-    // leave too few waves).  64- against 256-row tiles, bf16: 64 rows 421, 433; 96:
-    // 497, 466.
+    // leave too few waves).  64- against 256-row tiles, bf16: 40 rows 399, 410; 64:
+    // 429, 441; 80: 462, 449; 128: 520, 475.  e4m3: 40: 242, 243; 64: 250, 249; 80:
+    // 280, 254; 128: 328, 270.
     if (mean <= (kE4m3 ? 12 : 10))
         return launch_stream<kE4m3, 1>(st, a);
     if constexpr (!kE4m3) {
@@ -338,8 +331,8 @@ epdc_status epdc_gate_scratch_bytes(int32_t max_tokens, int32_t num_experts, siz
     // the most blocks a call of up to max_tokens tokens takes: a wave per token
     // needs more of them than 16 lanes
     const int64_t wave = gate_wave_tokens(num_experts);
-    const int a = balance_blocks(max_tokens < wave ? max_tokens : wave, num_experts);
-    const int b = balance_blocks(max_tokens, num_experts);
+    const int a = gate_blocks(max_tokens < wave ? max_tokens : wave, num_experts, kGateMaxBlocks);
+    const int b = gate_blocks(max_tokens, num_experts, kGateMaxBlocks);
     *bytes = 256 + sizeof(float) * (size_t)((a > b ? a : b) + kGateMaxFan) *
                        (size_t)gate_partial_words(num_experts);
     return ok();
@@ -372,7 +365,7 @@ epdc_status epdc_gate(const epdc_gate_args *args, void *stream, float *weights, 
     if (balance) {
         a.ticket = static_cast<uint32_t *>(scratch);
         a.partial = reinterpret_cast<float *>(static_cast<uint8_t *>(scratch) + 256);
-        const int grid = balance_blocks(a.tokens, a.experts);
+        const int grid = gate_blocks(a.tokens, a.experts, kGateMaxBlocks);
         const size_t lds = sizeof(float) * ((size_t)a.experts + 1 +
                                             kGateThreads / 64 * (size_t)a.experts +
                                             kGateThreads / gate_lanes(a.tokens, a.experts));
