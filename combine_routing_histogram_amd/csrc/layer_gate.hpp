@@ -576,6 +576,11 @@ __global__ __launch_bounds__(kGateThreads, kV < 32 ? 4 : 2) void k_gate(const Ga
     // Every block's stores are at the device's point of coherence before it takes
     // a ticket.  The last of each `fan` blocks adds their rows, the last of
     // those the sums: with one level its last block alone read 256 rows, 40 us more.
+    // Stores, tickets and loads are relaxed atomics of the agent's scope.  That the
+    // wait for a wave's own stores orders them is no promise of the language but
+    // of gfx950: such accesses are made in the memory that all XCDs share, so a
+    // release would only add the write-back of an L2 that holds none of them,
+    // and an acquire the drop of lines that nothing reads.
     const auto done = [&](uint32_t *ticket, uint32_t count) {
         __builtin_amdgcn_s_waitcnt(0);
         __syncthreads();

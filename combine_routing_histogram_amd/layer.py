@@ -102,11 +102,12 @@ def make_gate_args(num_tokens: int, num_experts: int, topk: int, score: int = EP
 
 def make_product_args(rows: int, num_experts: int, in_features: int, out_features: int,
                       dtype: int = EPDC_DT_BF16, activation: int = EPDC_ACT_NONE,
-                      expected_rows: int = 0, input: int = 0, scales: int = 0, weight: int = 0, weight_scales: int = 0, bias: int = 0,
+                      expected_rows: int = 0, input: int = 0, scales: int = 0, weight: int = 0,
+                      weight_scales: int = 0, bias: int = 0,
                       expert_off: int = 0) -> epdc_product_args:
     return epdc_product_args(rows, num_experts, in_features, out_features, dtype, activation,
-                             expected_rows, input or None, scales or None, weight or None, weight_scales or None,
-                             bias or None, expert_off or None)
+                             expected_rows, input or None, scales or None, weight or None,
+                             weight_scales or None, bias or None, expert_off or None)
 
 
 # ---- one wrapper per entry point --------------------------------------------------
