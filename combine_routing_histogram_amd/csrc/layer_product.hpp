@@ -276,13 +276,17 @@ __device__ inline __amdgpu_buffer_rsrc_t buffer_at(const uint8_t *base, uint32_t
 // because the compiler, which cannot tell the two buffers of a tile apart,
 // else waits for every such load before a transposing LDS read; when they have
 // landed is wait_and_meet's business.  Nothing returns to registers.  M0 holds
-// the LDS address.  It is reserved to the compiler, which takes it neither as
-// a clobber nor reliably as an operand of asm; so it is set in the same block as
-// its use, and the compiler's own code may not use it (tests/test_layer_asm.py).
+// the LDS address; it is reserved to the compiler, which takes no clobber of
+// it, so the compiler's own code may not use it.  The descriptor can come from
+// v_readfirstlane just before: a memory instruction may read a scalar register five
+// wait states after a vector instruction wrote it, which the compiler sees to
+// in its own code but not in asm; s_mov and s_nop 3 are five.  Without them a
+// load can take the last step's bound.  tests/test_layer_asm.py reads the
+// listing for both.
 __device__ __forceinline__ void load_direct(__amdgpu_buffer_rsrc_t at, uint32_t off, uint8_t *lds)
 {
     const int to = uniform((int)(uint32_t)(uintptr_t)(lds_byte *)lds);
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to),
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to),
                  "v"(off), "s"(at));
 }
 
