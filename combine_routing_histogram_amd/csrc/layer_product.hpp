@@ -1011,7 +1011,7 @@ __device__ __forceinline__ void product_tile(const ProductArgs &a, int block, ui
     constexpr int kBatch = kMI < 4 ? kMI : 4;  // row blocks whose residuals are in flight
 #pragma unroll
     for (int i0 = 0; i0 < kMI; i0 += kBatch) {
-        bf16x8 res[kBatch][2];
+        bf16x8 res[kBatch][2] = {};  // an unset vector as an argument would be undefined
         if (kProduct == kForward && a.residual) {
 #pragma unroll
             for (int i = 0; i < kBatch; ++i)
