@@ -545,11 +545,12 @@ epdc_status epdc_expert_backward(const epdc_product_args *args, void *stream,
         g.input.contract = of;
         g.input.q = static_cast<const uint8_t *>(args->weight);
         g.input.out = static_cast<uint8_t *>(grad_input);
-        s = few ? plan_tiles<kGradInput, 1>(g.input, &g.input_blocks)
-                : plan_tiles<kGradInput, 4>(g.input, &g.input_blocks);
+        int input_blocks;
+        s = few ? plan_tiles<kGradInput, 1>(g.input, &input_blocks)
+                : plan_tiles<kGradInput, 4>(g.input, &input_blocks);
         if (s != EPDC_SUCCESS)
             return s;
-        blocks += g.input_blocks;
+        blocks += input_blocks;
     }
     if (grad_bias) {
         g.bias.rows = args->rows;
@@ -561,7 +562,8 @@ epdc_status epdc_expert_backward(const epdc_product_args *args, void *stream,
         g.bias.preact = static_cast<const uint16_t *>(preact);
         g.bias.grad_bias = grad_bias;
         g.bias_cols = (of + kWave * 8 - 1) / (kWave * 8);
-        blocks += (int64_t)args->num_experts * g.bias_cols;
+        g.bias_blocks = (args->num_experts * g.bias_cols + kXcds - 1) / kXcds * kXcds;
+        blocks += g.bias_blocks;
     }
     if (blocks > kMaxThreads / (kTileWaves * kWave))
         return fail(EPDC_ERR_INVALID_ARGS, "more tiles than a launch can hold");

@@ -1324,29 +1324,55 @@ __device__ inline void bias_grad(const BiasGradArgs &a, int e, int col_block, ui
     const bool up = gated && c >= gcols;  // out_features is a multiple of 16: never both in 8
     const int gc = up ? c - gcols : c;
     float s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (c < a.cols) {
-#pragma unroll 4
-        for (int r = r0 + wave; r < r1; r += kBiasSlices) {
-            const bf16x8 g =
-                *reinterpret_cast<const bf16x8 *>(a.grad_out + (size_t)r * gcols + gc);
-            if (a.act == kActNone) {
+    // kRows rows' loads before the first is used; kFactors: 0 grad_out alone, 1 with z,
+    // 2 with the gate's z and the up row
+    const auto add_rows = [&](auto rows, auto factors, int r) {
+        constexpr int kRows = decltype(rows)::value, kFactors = decltype(factors)::value;
+        bf16x8 v[kRows][kFactors + 1];
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    s[i] += (float)g[i];
-                continue;
-            }
-            const uint16_t *z = a.preact + (size_t)r * a.cols + gc;
-            const bf16x8 z0 = *reinterpret_cast<const bf16x8 *>(z);
-            bf16x8 z1 = z0;
-            if (gated && !up)
-                z1 = *reinterpret_cast<const bf16x8 *>(z + gcols);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float d = (float)g[i], x = (float)z0[i];
-                s[i] += up ? d * act_one(a.act, x)
-                           : d * act_one_grad(a.act, x) * (gated ? (float)z1[i] : 1.0f);
+        for (int b = 0; b < kRows; ++b) {
+            const size_t row = (size_t)(r + b * kBiasSlices);
+            v[b][0] = *reinterpret_cast<const bf16x8 *>(a.grad_out + row * gcols + gc);
+            if constexpr (kFactors >= 1) {
+                const uint16_t *z = a.preact + row * a.cols + gc;
+                v[b][1] = *reinterpret_cast<const bf16x8 *>(z);
+                if constexpr (kFactors >= 2)
+                    v[b][2] = *reinterpret_cast<const bf16x8 *>(z + gcols);
             }
         }
+#pragma unroll
+        for (int b = 0; b < kRows; ++b)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float d = (float)v[b][0][i];
+                if constexpr (kFactors == 0) {
+                    s[i] += d;
+                } else {
+                    const float x = (float)v[b][1][i];
+                    if constexpr (kFactors == 1)
+                        s[i] += d * (up ? act_one(a.act, x) : act_one_grad(a.act, x));
+                    else
+                        s[i] += d * act_one_grad(a.act, x) * (float)v[b][2][i];
+                }
+            }
+    };
+    // (One row at a time, every step of a busy expert waits for memory: the biases
+    // alone, 3808 rows of 4096 with SwiGLU, 792 us, so 410 to 450, most of it act'.)
+    const auto add_all = [&](auto factors) {
+        constexpr int kRows = 4;
+        int r = r0 + wave;
+        for (; r + (kRows - 1) * kBiasSlices < r1; r += kRows * kBiasSlices)
+            add_rows(Count<kRows>(), factors, r);
+        for (; r < r1; r += kBiasSlices)
+            add_rows(Count<1>(), factors, r);
+    };
+    if (c < a.cols) {
+        if (a.act == kActNone)
+            add_all(Count<0>());
+        else if (gated && !up)
+            add_all(Count<2>());
+        else
+            add_all(Count<1>());
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -1362,16 +1388,17 @@ __device__ inline void bias_grad(const BiasGradArgs &a, int e, int col_block, ui
     a.grad_bias[(size_t)e * a.cols + col_block * kWave * 8 + col] = sum;
 }
 
-// The gradients that follow from dz in one launch: first the blocks of the weights'
-// tiles, then the rows', then the biases' column blocks, any of them none.  Each
-// XCD's run of a part starts afresh, so a part holds a multiple of 8 blocks
-// unless it is the last.  (One after the other, 122 rows of 256 x 520 over 8
+// The gradients that follow from dz in one launch: first the biases' column blocks,
+// which take longest where one expert is busy (at the end 32768 rows of 4096 x 4096
+// over 64 experts, skewed, took 325 us more with biases, so 100), then the blocks
+// of the weights' tiles, then the rows', any of them none.  Each XCD's run of a part starts afresh, so
+// a part holds a multiple of 8 blocks.  (One after the other, 122 rows of 256 x 520 over 8
 // experts took 36 us, of which each launch was 6 to 10; together 15.  32768 rows
 // of 4096 x 4096 over 64 experts, skewed: 2.4 ms, 0.92 PFLOP/s.)
 struct GradArgs {
     ProductArgs weight, input;
     BiasGradArgs bias;
-    int32_t weight_blocks, input_blocks, bias_cols;  // bias_cols: column blocks of an expert
+    int32_t bias_blocks, weight_blocks, bias_cols;  // bias_cols: column blocks of an expert
 };
 
 template <int kInputGroups>
@@ -1382,18 +1409,17 @@ __global__ __launch_bounds__(kTileWaves *kWave) void k_product_grads(const GradA
     static_assert(kBytes >= kBiasLds, "the smaller parts fit");
     __shared__ __align__(1024) uint8_t lds[kBytes];
     int block = blockIdx.x;
-    if (block < a.weight_blocks) {
+    if (block < a.bias_blocks) {
+        const int e = block / a.bias_cols;
+        if (e < a.bias.experts)
+            bias_grad(a.bias, e, block - e * a.bias_cols, lds);
+        return;
+    }
+    block -= a.bias_blocks;
+    if (block < a.weight_blocks)
         product_tile<kGradWeight, false, 4>(a.weight, block, lds);
-        return;
-    }
-    block -= a.weight_blocks;
-    if (block < a.input_blocks) {
-        product_tile<kGradInput, false, kInputGroups>(a.input, block, lds);
-        return;
-    }
-    block -= a.input_blocks;
-    const int e = block / a.bias_cols;
-    bias_grad(a.bias, e, block - e * a.bias_cols, lds);
+    else
+        product_tile<kGradInput, false, kInputGroups>(a.input, block - a.weight_blocks, lds);
 #endif
 }
 
