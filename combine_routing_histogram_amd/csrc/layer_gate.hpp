@@ -26,8 +26,8 @@ static_assert(kGateMaxBlocks <= kGateMaxFan * kGateMaxFan, "two levels of sums")
 // a token's chain of top-k steps is longer and few tokens leave most SIMDs with
 // one wave or none; with many the whole waves' steps are mostly idle lanes.
 // Forward and backward with a balance, 64 lanes against 16: 256 experts, 2048
-// tokens 24 and 30 us, 4096: 31 and 32, 8192: 45 and 33; 128 experts, 4093
-// tokens: 26 and 23.
+// tokens 23 and 30 us, 4096: 29 and 31, 8192: 38 and 33; 128 experts, 2048
+// tokens: 20 and 22, 4093: 25 and 23.
 __host__ __device__ inline int64_t gate_wave_tokens(int experts) { return 16 * (int64_t)experts; }
 
 __host__ __device__ inline int gate_lanes(int64_t tokens, int experts)
@@ -664,7 +664,7 @@ __global__ __launch_bounds__(kGateThreads, kV < 32 ? 4 : 2) void k_gate(const Ga
 
 // One pass over the logits: with p the scores' softmax (sigmoid: s / sum s),
 //   d/dl_j of scale * r(chosen)  and of  E/n sum_e f_e p_e  and of  lse^2 / n.
-// (32768 x 256 fp32: 32 us, 2.1 TB/s; 4093 x 128 bf16: 7 us.)
+// (32768 x 256 fp32: 33 us, 2.0 TB/s; 4093 x 128 bf16: 6 us.)
 template <int kLanes, int kV>
 __global__ __launch_bounds__(kGateThreads, kV < 32 ? 4 : 2) void k_gate_backward(const GateArgs a)
 {
@@ -816,8 +816,8 @@ constexpr int kCombineGradThreads = 512;
 // A block per token: a thread reads a vector of the token's gradient once and
 // serves the K rows with it -- the row's vector for the dot product in, the
 // scaled gradient out.  Bytes are the bound (one row read and one written per
-// pair): 4096 x 7168 bf16, top-8, 998 MB in 177 to 196 us, 5.1 to 5.6 TB/s of the
-// 5.7 that copies reach; with 1024 threads 225 us where 512 took 195.
+// pair): 4096 x 7168 bf16, top-8, 998 MB in 193 to 196 us, 5.1 TB/s of the 5.7
+// that copies reach; with 1024 threads 225 us where 512 took 195.
 template <int kTopk>
 __global__ __launch_bounds__(kCombineGradThreads) void k_combine_grad(const CombineGradArgs a)
 {

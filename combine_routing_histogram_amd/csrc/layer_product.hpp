@@ -598,9 +598,10 @@ __device__ inline void finish_forward8(const ProductArgs &a, int row, int col, f
 // at every barrier: loads alone took 1483 us for 32768 x 7168 x 4096 where these
 // take 1188, and the multiplications alone 1344.)
 //
-// Reached, 1440 us for 32768 x 7168 x 4096 bf16 over 8 even experts: 1.34 PFLOP/s
-// of the 1.43 of a library product.  Skewed over 64 experts 1.75 to 1.93 ms, e4m3
-// 1.18 to 1.22: the last tiles and row groups that are not full.
+// Reached, 1420 to 1470 us for 32768 x 7168 x 4096 bf16 over 8 even experts: 1.31 to
+// 1.35 PFLOP/s of the 1.43 of a library product; e4m3 950 to 980 us.  Skewed over
+// 64 experts 1.80 to 1.91 ms, e4m3 1.17 to 1.21: the last tiles and row groups that
+// are not full.
 
 constexpr int kTileWaves = 8, kTileWavesM = 2, kTileWavesN = 4, kTileCols = 256;
 
@@ -1265,7 +1266,7 @@ constexpr int kActRows = 4;
 
 // dz = grad_out * act'(preact), 8 columns per lane; gated: both halves.  dz is
 // rounded to bf16 because the two products that follow take bf16 operands.
-// Bytes are the bound: 32768 rows of 4096, gated, 671 MB in 115 us, 5.8 TB/s.
+// Bytes are the bound: 32768 rows of 4096, gated, 671 MB in 122 us, 5.5 TB/s.
 __global__ __launch_bounds__(kActRows *kWave) void k_act_grad(const ActGradArgs a)
 {
     const int r0 = clamp_row(a.expert_off, 0, a.rows);
@@ -1394,7 +1395,7 @@ __device__ inline void bias_grad(const BiasGradArgs &a, int e, int col_block, ui
 // of the weights' tiles, then the rows', any of them none.  Each XCD's run of a part starts afresh, so
 // a part holds a multiple of 8 blocks.  (One after the other, 122 rows of 256 x 520 over 8
 // experts took 36 us, of which each launch was 6 to 10; together 15.  32768 rows
-// of 4096 x 4096 over 64 experts, skewed: 2.4 ms, 0.92 PFLOP/s.)
+// of 4096 x 4096 over 64 experts, skewed: 2.3 to 2.4 ms, 0.92 to 0.95 PFLOP/s.)
 struct GradArgs {
     ProductArgs weight, input;
     BiasGradArgs bias;
