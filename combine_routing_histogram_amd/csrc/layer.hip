@@ -430,8 +430,9 @@ epdc_status epdc_expert_product(const epdc_product_args *args, void *stream, con
     const Array to = {"out", out, (int64_t)args->rows * cols * 2},
                 z = {"preact", preact, (int64_t)args->rows * args->out_features * 2},
                 res = {"residual", residual, to.bytes};
+    // out may be the residual: what is added to an element is read before it is written
     s = check_apart(to, {in.input, in.scales, in.weight, in.weight_scales, in.bias, in.offsets, z,
-                         residual == out ? Array{} : res});  // an element's own residual is read first
+                         residual == out ? Array{} : res});
     if (s == EPDC_SUCCESS)
         s = check_apart(z, {in.input, in.scales, in.weight, in.weight_scales, in.bias, in.offsets,
                             res});

@@ -55,8 +55,9 @@ def test_forward_e4m3_scales(over, size):
 
 # with SwiGLU and every output
 BACKWARD = [("grad_input", "grad_out", 0), ("grad_input", "preact", 16), ("grad_input", "dz", 16),
-            ("grad_input", "weight", 0), ("grad_input", "input", 0), ("grad_weight", "weight", 0),
-            ("grad_weight", "input", 0), ("grad_weight", "dz", 0), ("grad_weight", "grad_input", 16),
+            ("grad_input", "weight", 0), ("grad_input", "input", 0),
+            ("grad_weight", "weight", 0), ("grad_weight", "input", 0),
+            ("grad_weight", "dz", 0), ("grad_weight", "grad_input", 16),
             ("grad_bias", "grad_weight", 16), ("grad_bias", "grad_out", 0),
             ("grad_bias", "preact", 0), ("grad_bias", "dz", 0), ("dz", "grad_out", 0),
             ("dz", "preact", 0), ("dz", "input", 0), ("dz", "weight", 0)]
