@@ -26,6 +26,8 @@ PROBE_LIB = os.path.join(PKG, "libepdc_probe.so")
 LAYER_SRC = os.path.join(PKG, "csrc", "layer.hip")
 LAYER_DEPS = [LAYER_SRC, os.path.join(PKG, "csrc", "layer_product.hpp"),
               os.path.join(PKG, "csrc", "layer_gate.hpp"),
+              os.path.join(PKG, "csrc", "layer_rows.hpp"),
+              os.path.join(PKG, "csrc", "layer_few.hpp"),
               os.path.join(ROOT, "include", "epdc_layer.h"),
               os.path.join(ROOT, "include", "epdc.h")]
 LAYER_LIB = os.path.join(PKG, "libepdc_layer.so")

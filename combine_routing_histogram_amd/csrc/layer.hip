@@ -4,6 +4,8 @@
 #include "epdc_layer.h"
 #include "layer_product.hpp"
 #include "layer_gate.hpp"
+#include "layer_rows.hpp"
+#include "layer_few.hpp"
 
 #include <hip/hip_runtime.h>
 
@@ -73,6 +75,8 @@ epdc_status launch(const char *name, F &&f)
 
 constexpr int kMaxFeatures = 1 << 20;
 constexpr int64_t kMaxExpertBytes = (int64_t)0x7fff0000;
+// int8: sums of products, of up to 2^14 each, stay below 2^31
+constexpr int kMaxInt8Features = (1 << 17) - 16;
 constexpr int64_t kMaxThreads = (int64_t)0xffffffff;  // of a launch, in all its blocks
 
 int gate_blocks(int64_t tokens, int experts, int limit)
@@ -163,6 +167,30 @@ void launch_gate_backward(int grid, hipStream_t st, const GateArgs &a)
 
 // ---- products -----------------------------------------------------------------
 
+bool product_type(int32_t dtype, int *type)
+{
+    switch (dtype) {
+    case EPDC_DT_BF16: *type = kTypeBf16; return true;
+    case EPDC_DT_E4M3: *type = kTypeE4m3; return true;
+    case EPDC_DT_INT8: *type = kTypeInt8; return true;
+    default: return false;
+    }
+}
+
+// What a contraction is a multiple of: 16 bytes; e4m3 a block of scales.
+int unit_features(int type) { return type == kTypeE4m3 ? 128 : type == kTypeInt8 ? 16 : 8; }
+
+// Scales of `rows` rows (one per row or per 128 columns) and of a weight.
+int64_t row_scales(int type, int64_t rows, int64_t features)
+{
+    return type == kTypeE4m3 ? rows * (features / 128) : type == kTypeInt8 ? rows : 0;
+}
+int64_t weight_scales(int type, int64_t experts, int64_t out, int64_t in)
+{
+    return type == kTypeE4m3 ? experts * ((out + 127) / 128) * (in / 128)
+                             : type == kTypeInt8 ? experts * out : 0;
+}
+
 epdc_status check_product(const epdc_product_args *p)
 {
     if (!p)
@@ -175,18 +203,19 @@ epdc_status check_product(const epdc_product_args *p)
         return fail(EPDC_ERR_INVALID_ARGS, "expected_rows must be >= 0");
     if (p->activation < EPDC_ACT_NONE || p->activation > EPDC_ACT_GEGLU)
         return fail(EPDC_ERR_INVALID_ARGS, "unknown activation %d", p->activation);
-    if (p->dtype != EPDC_DT_BF16 && p->dtype != EPDC_DT_E4M3)
-        return fail(EPDC_ERR_INVALID_ARGS, "operands must be bf16 or e4m3");
-    const bool e4m3 = p->dtype == EPDC_DT_E4M3;
-    const int unit_in = e4m3 ? 128 : 8, unit_out = act_gated(p->activation) ? 16 : 8;
-    if (p->in_features < unit_in || p->in_features > kMaxFeatures || p->in_features % unit_in)
-        return fail(EPDC_ERR_INVALID_ARGS, "in_features must be a multiple of %d, at most 2^20",
-                    unit_in);
+    int type;
+    if (!product_type(p->dtype, &type))
+        return fail(EPDC_ERR_INVALID_ARGS, "operands must be bf16 or e4m3 or int8");
+    const int unit_in = unit_features(type), unit_out = act_gated(p->activation) ? 16 : 8;
+    const int most_in = type == kTypeInt8 ? kMaxInt8Features : kMaxFeatures;
+    if (p->in_features < unit_in || p->in_features > most_in || p->in_features % unit_in)
+        return fail(EPDC_ERR_INVALID_ARGS, "in_features must be a multiple of %d, at most %d",
+                    unit_in, most_in);
     if (p->out_features < unit_out || p->out_features > kMaxFeatures ||
         p->out_features % unit_out)
         return fail(EPDC_ERR_INVALID_ARGS, "out_features must be a multiple of %d, at most 2^20",
                     unit_out);
-    if ((int64_t)p->in_features * p->out_features * (e4m3 ? 1 : 2) > kMaxExpertBytes)
+    if ((int64_t)p->in_features * p->out_features * element_bytes(type) > kMaxExpertBytes)
         return fail(EPDC_ERR_INVALID_ARGS, "one expert's weight must be smaller than 2 GiB");
     if (!p->expert_off)
         return fail(EPDC_ERR_INVALID_ARGS, "expert_off is required");
@@ -205,11 +234,13 @@ struct Operands {
 Operands operands(const epdc_product_args &p)
 {
     const int64_t rows = p.rows, experts = p.num_experts, in = p.in_features, of = p.out_features;
-    const int64_t elem = p.dtype == EPDC_DT_E4M3 ? 1 : 2, blocks = in / 128;
+    int type = kTypeBf16;
+    product_type(p.dtype, &type);
+    const int64_t elem = element_bytes(type);
     return {{"input", p.input, rows * in * elem},
-            {"scales", p.scales, rows * blocks * 4},
+            {"scales", p.scales, row_scales(type, rows, in) * 4},
             {"weight", p.weight, experts * of * in * elem},
-            {"weight_scales", p.weight_scales, experts * ((of + 127) / 128) * blocks * 4},
+            {"weight_scales", p.weight_scales, weight_scales(type, experts, of, in) * 4},
             {"bias", p.bias, experts * of * 4},
             {"expert_off", p.expert_off, (experts + 1) * 4}};
 }
@@ -255,7 +286,7 @@ epdc_status plan_tiles(ProductArgs &a, int *grid)
     return grid_of(tiles, kTileWaves * kWave, grid);
 }
 
-template <bool kE4m3, int kGroups>
+template <int kType, int kGroups>
 epdc_status launch_tile(hipStream_t st, ProductArgs &a)
 {
     int grid;
@@ -263,11 +294,11 @@ epdc_status launch_tile(hipStream_t st, ProductArgs &a)
     if (s != EPDC_SUCCESS)
         return s;
     return launch("k_product_tile", [&] {
-        k_product_tile<kE4m3, kGroups><<<grid, kTileWaves * kWave, 0, st>>>(a);
+        k_product_tile<kType, kGroups><<<grid, kTileWaves * kWave, 0, st>>>(a);
     });
 }
 
-template <bool kE4m3, int kMI>
+template <int kType, int kMI>
 epdc_status launch_stream(hipStream_t st, ProductArgs &a)
 {
     a.col_tiles = (a.out_cols + 15) / 16;
@@ -278,15 +309,16 @@ epdc_status launch_stream(hipStream_t st, ProductArgs &a)
         return s;
     return launch("k_product_stream", [&] {
         if (act_gated(a.act))
-            k_product_stream<kE4m3, kMI, true><<<grid, kStreamWaves * kWave, 0, st>>>(a);
+            k_product_stream<kType, kMI, true><<<grid, kStreamWaves * kWave, 0, st>>>(a);
         else
-            k_product_stream<kE4m3, kMI, false><<<grid, kStreamWaves * kWave, 0, st>>>(a);
+            k_product_stream<kType, kMI, false><<<grid, kStreamWaves * kWave, 0, st>>>(a);
     });
 }
 
-template <bool kE4m3>
+template <int kType>
 epdc_status launch_forward(hipStream_t st, ProductArgs &a, int64_t mean)
 {
+    constexpr bool kE4m3 = kType == kTypeE4m3;
     // By mean rows per expert, all that is known here of the experts' counts.  The
     // streamed form reads the weights fastest but once per 16 (32) rows of an
     // expert, the tiles once per 64 (256) at 85% of that rate.  Measured over 64
@@ -297,14 +329,14 @@ epdc_status launch_forward(hipStream_t st, ProductArgs &a, int64_t mean)
     // 429, 441; 80: 462, 449; 128: 520, 475.  e4m3: 40: 242, 243; 64: 250, 249; 80:
     // 280, 254; 128: 328, 270.
     if (mean <= (kE4m3 ? 12 : 10))
-        return launch_stream<kE4m3, 1>(st, a);
+        return launch_stream<kType, 1>(st, a);
     if constexpr (!kE4m3) {
         if (mean <= 24)
-            return launch_stream<kE4m3, 2>(st, a);
+            return launch_stream<kType, 2>(st, a);
     }
     if (mean <= 64)
-        return launch_tile<kE4m3, 1>(st, a);
-    return launch_tile<kE4m3, 4>(st, a);
+        return launch_tile<kType, 1>(st, a);
+    return launch_tile<kType, 4>(st, a);
 }
 
 void launch_combine_grad(int grid, hipStream_t st, const CombineGradArgs &a)
@@ -317,6 +349,133 @@ void launch_combine_grad(int grid, hipStream_t st, const CombineGradArgs &a)
     case 8: k_combine_grad<8><<<grid, kCombineGradThreads, 0, st>>>(a); break;
     default: k_combine_grad<0><<<grid, kCombineGradThreads, 0, st>>>(a); break;
     }
+}
+
+// ---- rows -----------------------------------------------------------------------
+
+// Blocks for `rows` rows, kTeams of them to a block at a time.
+int row_blocks(int64_t rows, int threads, int teams)
+{
+    const int64_t most = kMaxThreads / threads < (1 << 20) ? kMaxThreads / threads : 1 << 20;
+    const int64_t b = (rows + teams - 1) / teams;
+    return (int)(b < most ? b : most);
+}
+
+template <int kWaves>
+int team_blocks(int64_t rows)
+{
+    constexpr int kThreads = team_threads(kWaves);
+    return row_blocks(rows, kThreads, kThreads / (kWaves * kWave));
+}
+
+// f(waves of a team, vectors of a lane): the fewest lanes that hold a row of `vecs`
+// vectors, four of them at most.
+template <typename F>
+void row_form(int vecs, F &&f)
+{
+    if (vecs <= 64)
+        f(Count<1>(), Count<1>());
+    else if (vecs <= 256)
+        f(Count<4>(), Count<1>());
+    else if (vecs <= 512)
+        f(Count<4>(), Count<2>());
+    else if (vecs <= 1024)
+        f(Count<4>(), Count<4>());
+    else if (vecs <= 2048)
+        f(Count<16>(), Count<2>());
+    else
+        f(Count<16>(), Count<4>());
+}
+
+epdc_status check_norm(const epdc_norm_args *n)
+{
+    if (!n)
+        return fail(EPDC_ERR_INVALID_ARGS, "args is NULL");
+    if (n->rows < 0 || n->rows > (1 << 30))
+        return fail(EPDC_ERR_INVALID_ARGS, "rows must be in [0, 2^30]");
+    if (n->features < 8 || n->features > kMaxNormFeatures || n->features % 8)
+        return fail(EPDC_ERR_INVALID_ARGS, "features must be a multiple of 8, at most %d",
+                    kMaxNormFeatures);
+    if (n->weight_dtype != EPDC_DT_BF16 && n->weight_dtype != EPDC_DT_FP32)
+        return fail(EPDC_ERR_INVALID_ARGS, "weight must be bf16 or fp32");
+    if (!(n->eps >= 0.0f) || n->eps > 3.4e38f)
+        return fail(EPDC_ERR_INVALID_ARGS, "eps must be finite and not negative");
+    if (!aligned(n->input, 16) || !aligned(n->residual, 16) || !aligned(n->weight, 16))
+        return fail(EPDC_ERR_INVALID_ARGS, "input, residual and weight must be 16-byte aligned");
+    if (n->rows > 0 && (!n->input || !n->weight))
+        return fail(EPDC_ERR_INVALID_ARGS, "input and weight are required");
+    return EPDC_SUCCESS;
+}
+
+NormArgs norm_args(const epdc_norm_args &n)
+{
+    NormArgs a = {};
+    a.rows = n.rows;
+    a.vecs = n.features / 8;
+    a.weight_bf16 = n.weight_dtype == EPDC_DT_BF16;
+    a.features = (float)n.features;
+    a.eps = n.eps;
+    a.input = static_cast<const uint8_t *>(n.input);
+    a.residual = static_cast<const uint8_t *>(n.residual);
+    a.weight = static_cast<const uint8_t *>(n.weight);
+    return a;
+}
+
+template <int kCodes>
+void launch_norm(hipStream_t st, const NormArgs &a)
+{
+    row_form(a.vecs, [&](auto waves, auto vecs) {
+        constexpr int kWaves = decltype(waves)::value;
+        k_rms_norm<kWaves, decltype(vecs)::value, kCodes>
+            <<<team_blocks<kWaves>(a.rows), team_threads(kWaves), 0, st>>>(a);
+    });
+}
+
+// Teams that share the rows of a gradient: each leaves a row of fp32 sums, so no
+// more of them than keep the chip full.
+constexpr int kNormGradTeams = 512;
+
+int norm_grad_blocks(int64_t rows, int teams)
+{
+    const int64_t most = kNormGradTeams / teams, b = (rows + teams - 1) / teams;
+    return (int)(b < most ? b : most);
+}
+
+// Columns of a scale of a format of codes; 0 for none of them.
+int code_unit(int32_t dtype)
+{
+    return dtype == EPDC_DT_E4M3 ? kCodeBlock : dtype == EPDC_DT_INT8 ? 16 : 0;
+}
+
+template <int kWaves, int kV>
+void launch_int8(hipStream_t st, const QuantArgs &a)
+{
+    k_quantize_int8<kWaves, kV><<<team_blocks<kWaves>(a.rows), team_threads(kWaves), 0, st>>>(a);
+}
+
+// ---- a layer for few tokens -----------------------------------------------------------
+
+template <int kType, int kMI>
+epdc_status launch_few(hipStream_t st, const FewArgs &a)
+{
+    const int pairs = a.tokens * a.topk, most = pairs < a.experts ? pairs : a.experts;
+    const int up = most * ((a.inner + 15) / 16), down = (a.hidden + 15) / 16;
+    epdc_status s = launch("k_few_up", [&] {
+        if (act_gated(a.act))
+            k_few_up<kType, kMI, true><<<up, kFewUpWaves * kWave, 0, st>>>(a);
+        else
+            k_few_up<kType, kMI, false><<<up, kFewUpWaves * kWave, 0, st>>>(a);
+    });
+    if (s == EPDC_SUCCESS)
+        s = launch("k_few_down",
+                   [&] { k_few_down<kType, kMI><<<down, kFewDownWaves * kWave, 0, st>>>(a); });
+    return s;
+}
+
+template <int kType>
+epdc_status launch_few_rows(hipStream_t st, const FewArgs &a)
+{
+    return a.tokens <= 16 ? launch_few<kType, 1>(st, a) : launch_few<kType, 2>(st, a);
 }
 
 }  // namespace
@@ -414,10 +573,12 @@ epdc_status epdc_expert_product(const epdc_product_args *args, void *stream, con
     epdc_status s = check_product(args);
     if (s != EPDC_SUCCESS)
         return s;
-    const bool e4m3 = args->dtype == EPDC_DT_E4M3;
-    if (e4m3 != (args->scales != nullptr) || e4m3 != (args->weight_scales != nullptr))
+    int type = kTypeBf16;
+    product_type(args->dtype, &type);
+    const bool scaled = type != kTypeBf16;
+    if (scaled != (args->scales != nullptr) || scaled != (args->weight_scales != nullptr))
         return fail(EPDC_ERR_INVALID_ARGS,
-                    "scales and weight_scales belong to e4m3 operands, both of them");
+                    "scales and weight_scales belong to e4m3 and int8 operands, both of them");
     if (args->rows > 0 && (!args->input || !args->weight || !out))
         return fail(EPDC_ERR_INVALID_ARGS, "input, weight and out are required");
     if (!aligned(residual, 16) || !aligned(out, 16) || !aligned(preact, 16))
@@ -442,7 +603,7 @@ epdc_status epdc_expert_product(const epdc_product_args *args, void *stream, con
     a.rows = args->rows;
     a.experts = args->num_experts;
     a.contract = args->in_features;
-    a.p_bytes = a.q_bytes = args->in_features * (e4m3 ? 1 : 2);
+    a.p_bytes = a.q_bytes = args->in_features * element_bytes(type);
     a.weight_rows = args->out_features;
     a.act = args->activation;
     a.out_cols = cols;
@@ -457,7 +618,9 @@ epdc_status epdc_expert_product(const epdc_product_args *args, void *stream, con
     a.preact = static_cast<uint16_t *>(preact);
     hipStream_t st = static_cast<hipStream_t>(stream);
     const int64_t mean = mean_rows(*args);
-    s = e4m3 ? launch_forward<true>(st, a, mean) : launch_forward<false>(st, a, mean);
+    s = type == kTypeE4m3   ? launch_forward<kTypeE4m3>(st, a, mean)
+        : type == kTypeInt8 ? launch_forward<kTypeInt8>(st, a, mean)
+                            : launch_forward<kTypeBf16>(st, a, mean);
     return s == EPDC_SUCCESS ? ok() : s;
 }
 
@@ -653,6 +816,293 @@ epdc_status epdc_combine_backward(void *stream, int32_t num_tokens, int32_t topk
             return s;
     }
     return ok();
+}
+
+epdc_status epdc_rms_norm(const epdc_norm_args *args, void *stream, void *out, void *sum,
+                          void *codes, float *scales, int32_t codes_dtype)
+{
+    epdc_status s = check_norm(args);
+    if (s != EPDC_SUCCESS)
+        return s;
+    const int unit = code_unit(codes_dtype);
+    if (codes_dtype != EPDC_DT_BF16 && !unit)
+        return fail(EPDC_ERR_INVALID_ARGS, "codes must be e4m3 or int8, or bf16 for none");
+    if (unit && args->features % unit)
+        return fail(EPDC_ERR_INVALID_ARGS, "features must be a multiple of %d for these codes",
+                    unit);
+    if (!unit && (codes || scales))
+        return fail(EPDC_ERR_INVALID_ARGS, "codes and scales belong to e4m3 and int8");
+    if (!aligned(out, 16) || !aligned(sum, 16) || !aligned(codes, 16) || !aligned(scales, 4))
+        return fail(EPDC_ERR_INVALID_ARGS,
+                    "out, sum and codes must be 16-byte aligned, scales 4-byte aligned");
+    if (args->rows == 0)
+        return ok();
+    if (unit && (!codes || !scales))
+        return fail(EPDC_ERR_INVALID_ARGS, "codes and scales are required");
+    if (!out && !unit)
+        return fail(EPDC_ERR_INVALID_ARGS, "out or codes are required");
+    const int64_t n = (int64_t)args->rows * args->features;
+    const Array x = {"input", args->input, n * 2}, r = {"residual", args->residual, n * 2},
+                w = {"weight", args->weight,
+                     (int64_t)args->features * (args->weight_dtype == EPDC_DT_BF16 ? 2 : 4)};
+    const Array o = {"out", out, n * 2}, t = {"sum", sum, n * 2}, c = {"codes", codes, n},
+                f = {"scales", scales,
+                     4 * (codes_dtype == EPDC_DT_E4M3 ? n / kCodeBlock : (int64_t)args->rows)};
+    // a row is read whole before any of it is written: sum may take the place of what it adds
+    s = check_apart(t, {sum == args->input ? Array{} : x, sum == args->residual ? Array{} : r, w,
+                        o, c, f});
+    if (s == EPDC_SUCCESS)
+        s = check_apart(o, {x, r, w, c, f});
+    if (s == EPDC_SUCCESS)
+        s = check_apart(c, {x, r, w, f});
+    if (s == EPDC_SUCCESS)
+        s = check_apart(f, {x, r, w});
+    if (s != EPDC_SUCCESS)
+        return s;
+    NormArgs a = norm_args(*args);
+    a.out = static_cast<uint8_t *>(out);
+    a.sum = static_cast<uint8_t *>(sum);
+    a.codes = static_cast<uint8_t *>(codes);
+    a.scales = scales;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    s = launch("k_rms_norm", [&] {
+        if (codes_dtype == EPDC_DT_E4M3)
+            launch_norm<kCodesE4m3>(st, a);
+        else if (codes_dtype == EPDC_DT_INT8)
+            launch_norm<kCodesInt8>(st, a);
+        else
+            launch_norm<kCodesNone>(st, a);
+    });
+    return s == EPDC_SUCCESS ? ok() : s;
+}
+
+epdc_status epdc_rms_norm_scratch_bytes(int32_t features, size_t *bytes)
+{
+    if (features < 8 || features > kMaxNormFeatures || features % 8 || !bytes)
+        return fail(EPDC_ERR_INVALID_ARGS,
+                    "features, a multiple of 8 and at most %d, and bytes are required",
+                    kMaxNormFeatures);
+    *bytes = sizeof(float) * (size_t)kNormGradTeams * (size_t)features;
+    return ok();
+}
+
+epdc_status epdc_rms_norm_backward(const epdc_norm_args *args, void *stream, const void *grad_out,
+                                   const void *grad_sum, void *grad_input, float *grad_weight,
+                                   void *scratch)
+{
+    epdc_status s = check_norm(args);
+    if (s != EPDC_SUCCESS)
+        return s;
+    if (args->residual)
+        return fail(EPDC_ERR_INVALID_ARGS, "the gradient takes the sum as input, and no residual");
+    if ((grad_weight != nullptr) != (scratch != nullptr))
+        return fail(EPDC_ERR_INVALID_ARGS, "grad_weight and scratch must both be given or both NULL");
+    if (args->rows > 0 && (!grad_out || !grad_input))
+        return fail(EPDC_ERR_INVALID_ARGS, "grad_out and grad_input are required");
+    if (!aligned(grad_out, 16) || !aligned(grad_sum, 16) || !aligned(grad_input, 16) ||
+        !aligned(grad_weight, 16) || !aligned(scratch, 16))
+        return fail(EPDC_ERR_INVALID_ARGS, "every array must be 16-byte aligned");
+    const int64_t n = (int64_t)args->rows * args->features;
+    const bool rows = args->rows > 0;
+    const Array x = {"input", rows ? args->input : nullptr, n * 2},
+                w = {"weight", rows ? args->weight : nullptr,
+                     (int64_t)args->features * (args->weight_dtype == EPDC_DT_BF16 ? 2 : 4)},
+                dy = {"grad_out", rows ? grad_out : nullptr, n * 2},
+                ds = {"grad_sum", rows ? grad_sum : nullptr, n * 2};
+    const Array dx = {"grad_input", rows ? grad_input : nullptr, n * 2},
+                dw = {"grad_weight", grad_weight, (int64_t)args->features * 4},
+                part = {"scratch", scratch, (int64_t)kNormGradTeams * args->features * 4};
+    // a row's gradient may take the place of what flows in: the thread that writes an
+    // element has read it
+    s = check_apart(dx, {x, w, grad_input == grad_out ? Array{} : dy,
+                         grad_input == grad_sum ? Array{} : ds, dw, part});
+    if (s == EPDC_SUCCESS)
+        s = check_apart(dw, {x, w, dy, ds, part});
+    if (s == EPDC_SUCCESS)
+        s = check_apart(part, {x, w, dy, ds});
+    if (s != EPDC_SUCCESS)
+        return s;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    NormArgs a = norm_args(*args);
+    a.grad_out = static_cast<const uint8_t *>(grad_out);
+    a.grad_sum = static_cast<const uint8_t *>(grad_sum);
+    a.grad_input = static_cast<uint8_t *>(grad_input);
+    a.partial = static_cast<float *>(scratch);
+    int teams = 0;
+    if (rows) {
+        s = launch("k_rms_norm_grad", [&] {
+            row_form(a.vecs, [&](auto waves, auto vecs) {
+                constexpr int kWaves = decltype(waves)::value, kThreads = team_threads(kWaves);
+                constexpr int kTeams = kThreads / (kWaves * kWave);
+                const int grid = norm_grad_blocks(a.rows, kTeams);
+                teams = grid * kTeams;
+                k_rms_norm_grad<kWaves, decltype(vecs)::value><<<grid, kThreads, 0, st>>>(a);
+            });
+        });
+        if (s != EPDC_SUCCESS)
+            return s;
+    }
+    if (grad_weight) {
+        NormWeightGradArgs g = {};
+        g.teams = teams;
+        g.quads = args->features / 4;
+        g.partial = a.partial;
+        g.grad_weight = grad_weight;
+        const int grid = (g.quads + kWeightGradQuads - 1) / kWeightGradQuads;
+        s = launch("k_norm_weight_grad", [&] {
+            k_norm_weight_grad<<<grid, kWeightGradQuads * kWeightGradLanes, 0, st>>>(g);
+        });
+        if (s != EPDC_SUCCESS)
+            return s;
+    }
+    return ok();
+}
+
+epdc_status epdc_quantize_rows(void *stream, int32_t rows, int32_t features, int32_t codes_dtype,
+                               const void *input, const int32_t *expert_off, int32_t num_experts,
+                               void *codes, float *scales)
+{
+    const int unit = code_unit(codes_dtype);
+    if (!unit)
+        return fail(EPDC_ERR_INVALID_ARGS, "codes must be e4m3 or int8");
+    if (rows < 0 || rows > (1 << 30))
+        return fail(EPDC_ERR_INVALID_ARGS, "rows must be in [0, 2^30]");
+    if (features < unit || features > kMaxQuantFeatures || features % unit)
+        return fail(EPDC_ERR_INVALID_ARGS, "features must be a multiple of %d, at most %d", unit,
+                    kMaxQuantFeatures);
+    if (expert_off && (num_experts < 1 || num_experts > kMaxExperts))
+        return fail(EPDC_ERR_INVALID_ARGS, "num_experts must be in [1, %d]", kMaxExperts);
+    if (rows > 0 && (!input || !codes || !scales))
+        return fail(EPDC_ERR_INVALID_ARGS, "input, codes and scales are required");
+    if (!aligned(input, 16) || !aligned(codes, 16) || !aligned(scales, 4) ||
+        !aligned(expert_off, 4))
+        return fail(EPDC_ERR_INVALID_ARGS,
+                    "input and codes must be 16-byte aligned, the other arrays 4-byte aligned");
+    if (rows == 0)
+        return ok();
+    const int64_t n = (int64_t)rows * features;
+    const Array x = {"input", input, n * 2},
+                off = {"expert_off", expert_off, ((int64_t)num_experts + 1) * 4},
+                c = {"codes", codes, n},
+                f = {"scales", scales,
+                     4 * (codes_dtype == EPDC_DT_E4M3 ? n / kCodeBlock : (int64_t)rows)};
+    epdc_status s = check_apart(c, {x, off, f});
+    if (s == EPDC_SUCCESS)
+        s = check_apart(f, {x, off});
+    if (s != EPDC_SUCCESS)
+        return s;
+    QuantArgs a = {};
+    a.rows = rows;
+    a.experts = num_experts;
+    a.vecs = features / 16;
+    a.expert_off = expert_off;
+    a.input = static_cast<const uint8_t *>(input);
+    a.codes = static_cast<uint8_t *>(codes);
+    a.scales = scales;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    if (codes_dtype == EPDC_DT_E4M3) {
+        const int64_t blocks = ((int64_t)rows * a.vecs + kQuantThreads - 1) / kQuantThreads;
+        s = launch("k_quantize_e4m3", [&] {
+            k_quantize_e4m3<<<row_blocks(blocks, kQuantThreads, 1), kQuantThreads, 0, st>>>(a);
+        });
+    } else {
+        s = launch("k_quantize_int8", [&] {
+            if (a.vecs <= 64)
+                launch_int8<1, 1>(st, a);
+            else if (a.vecs <= 256)
+                launch_int8<4, 1>(st, a);
+            else if (a.vecs <= 512)
+                launch_int8<4, 2>(st, a);
+            else if (a.vecs <= 2048)
+                launch_int8<16, 2>(st, a);
+            else
+                launch_int8<16, 8>(st, a);
+        });
+    }
+    return s == EPDC_SUCCESS ? ok() : s;
+}
+
+epdc_status epdc_few_tokens(const epdc_few_args *args, void *stream, void *h, void *out)
+{
+    if (!args)
+        return fail(EPDC_ERR_INVALID_ARGS, "args is NULL");
+    const epdc_few_args &p = *args;
+    if (p.num_tokens < 0 || p.num_tokens > kFewTokens)
+        return fail(EPDC_ERR_INVALID_ARGS, "num_tokens must be in [0, %d]", kFewTokens);
+    if (p.topk < 1 || p.topk > kMaxTopk)
+        return fail(EPDC_ERR_INVALID_ARGS, "topk must be in [1, %d]", kMaxTopk);
+    if (p.num_experts < 1 || p.num_experts > kMaxExperts || p.first_expert < 0 ||
+        p.first_expert > kMaxExperts)
+        return fail(EPDC_ERR_INVALID_ARGS,
+                    "num_experts must be in [1, %d] and first_expert in [0, %d]", kMaxExperts,
+                    kMaxExperts);
+    if (p.activation < EPDC_ACT_NONE || p.activation > EPDC_ACT_GEGLU)
+        return fail(EPDC_ERR_INVALID_ARGS, "unknown activation %d", p.activation);
+    int type;
+    if (!product_type(p.dtype, &type))
+        return fail(EPDC_ERR_INVALID_ARGS, "weights must be bf16, e4m3 or int8");
+    const int unit = unit_features(type);
+    if (p.hidden < unit || p.hidden > kMaxFeatures || p.hidden % unit || p.inner < unit ||
+        p.inner > kMaxFeatures || p.inner % unit)
+        return fail(EPDC_ERR_INVALID_ARGS, "hidden and inner must be multiples of %d, at most %d",
+                    unit, kMaxFeatures);
+    const bool gated = act_gated(p.activation);
+    const int64_t T = p.num_tokens, pairs = T * p.topk, E = p.num_experts, H = p.hidden,
+                  I = p.inner, up = gated ? 2 * I : I, elem = element_bytes(type);
+    if (up * H * elem > kMaxExpertBytes || pairs * I * 2 > kMaxExpertBytes)
+        return fail(EPDC_ERR_INVALID_ARGS,
+                    "one expert's weight, and the rows of h, must be smaller than 2 GiB");
+    const bool scaled = type != kTypeBf16;
+    if (scaled != (p.w1_scales != nullptr) || scaled != (p.w2_scales != nullptr))
+        return fail(EPDC_ERR_INVALID_ARGS,
+                    "w1_scales and w2_scales belong to e4m3 and int8 weights, both of them");
+    if (T > 0 && (!p.input || !p.indices || !p.w1 || !p.w2 || !h || !out))
+        return fail(EPDC_ERR_INVALID_ARGS, "input, indices, w1, w2, h and out are required");
+    if (!aligned(p.input, 16) || !aligned(p.w1, 16) || !aligned(p.w2, 16) || !aligned(h, 16) ||
+        !aligned(out, 16) || !aligned(p.weights, 4) || !aligned(p.indices, 4) ||
+        !aligned(p.w1_scales, 4) || !aligned(p.w2_scales, 4) || !aligned(p.bias1, 4) ||
+        !aligned(p.bias2, 4))
+        return fail(EPDC_ERR_INVALID_ARGS, "input, w1, w2, h and out must be 16-byte aligned, the "
+                                           "other arrays 4-byte aligned");
+    if (T == 0)
+        return ok();
+    const Array x = {"input", p.input, T * H * 2}, rw = {"weights", p.weights, pairs * 4},
+                ids = {"indices", p.indices, pairs * 4}, w1 = {"w1", p.w1, E * up * H * elem},
+                w2 = {"w2", p.w2, E * H * I * elem},
+                s1 = {"w1_scales", p.w1_scales, weight_scales(type, E, up, H) * 4},
+                s2 = {"w2_scales", p.w2_scales, weight_scales(type, E, H, I) * 4},
+                b1 = {"bias1", p.bias1, E * up * 4}, b2 = {"bias2", p.bias2, E * H * 4};
+    const Array mid = {"h", h, pairs * I * 2}, to = {"out", out, T * H * 2};
+    epdc_status s = check_apart(mid, {x, rw, ids, w1, w2, s1, s2, b1, b2, to});
+    // the input is not read any more when out is written
+    if (s == EPDC_SUCCESS)
+        s = check_apart(to, {out == p.input ? Array{} : x, rw, ids, w1, w2, s1, s2, b1, b2});
+    if (s != EPDC_SUCCESS)
+        return s;
+    FewArgs a = {};
+    a.tokens = p.num_tokens;
+    a.topk = p.topk;
+    a.experts = p.num_experts;
+    a.first_expert = p.first_expert;
+    a.hidden = p.hidden;
+    a.inner = p.inner;
+    a.act = p.activation;
+    a.x = static_cast<const uint8_t *>(p.input);
+    a.weights = p.weights;
+    a.indices = p.indices;
+    a.w1 = static_cast<const uint8_t *>(p.w1);
+    a.w2 = static_cast<const uint8_t *>(p.w2);
+    a.s1 = p.w1_scales;
+    a.s2 = p.w2_scales;
+    a.b1 = p.bias1;
+    a.b2 = p.bias2;
+    a.h = static_cast<uint8_t *>(h);
+    a.out = static_cast<uint8_t *>(out);
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    s = type == kTypeE4m3   ? launch_few_rows<kTypeE4m3>(st, a)
+        : type == kTypeInt8 ? launch_few_rows<kTypeInt8>(st, a)
+                            : launch_few_rows<kTypeBf16>(st, a);
+    return s == EPDC_SUCCESS ? ok() : s;
 }
 
 const char *epdc_layer_last_error(void) { return g_last_error.c_str(); }

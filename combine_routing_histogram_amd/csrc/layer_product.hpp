@@ -33,6 +33,11 @@ constexpr int kStepBytes = 128;  // contraction bytes of one LDS row (untranspos
 
 enum Product { kForward, kGradInput, kGradWeight };
 
+// Types of a product's operands.
+enum Type { kTypeBf16, kTypeE4m3, kTypeInt8 };
+
+constexpr int element_bytes(int type) { return type == kTypeBf16 ? 2 : 1; }
+
 enum Act { kActNone, kActRelu, kActGelu, kActSilu, kActSwiglu, kActGeglu };
 
 struct ProductArgs {
@@ -49,7 +54,7 @@ struct ProductArgs {
     int32_t act;
     int32_t out_fp32;    // kGradWeight: out holds fp32
     const uint8_t *p, *q;
-    const float *scales, *weight_scales;  // e4m3
+    const float *scales, *weight_scales;  // e4m3: per 128 columns; int8: per row
     const float *bias;
     const uint16_t *residual;
     const int32_t *expert_off;
@@ -429,6 +434,31 @@ __device__ inline f32x4 mfma_e4m3(i32x8 a, i32x8 b, f32x4 c)
                                                             0x7f7f7f7f);
 }
 
+// int8 x int8 over 64 contraction elements, exact in 32-bit integers
+__device__ inline i32x4 mfma_int8(i32x4 a, i32x4 b, i32x4 c)
+{
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
+}
+
+// 64 bytes of contraction: their products added to an accumulator of the type
+__device__ inline void multiply_add(i32x4 a, i32x4 b, f32x4 &c) { c = mfma_bf16(a, b, c); }
+__device__ inline void multiply_add(i32x4 a, i32x4 b, i32x4 &c) { c = mfma_int8(a, b, c); }
+
+template <int kType>
+struct AccumulatorOf {
+    typedef f32x4 type;
+};
+template <>
+struct AccumulatorOf<kTypeInt8> {
+    typedef i32x4 type;
+};
+
+__device__ inline f32x4 to_f32(f32x4 v) { return v; }
+__device__ inline f32x4 to_f32(i32x4 v)
+{
+    return f32x4{(float)v[0], (float)v[1], (float)v[2], (float)v[3]};
+}
+
 __device__ inline i32x8 join(i32x4 a, i32x4 b)
 {
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
@@ -631,8 +661,9 @@ struct TileWork {
 };
 
 // The operands of a tile with kA 64-row groups of rows, and their loads.
-template <int kProduct, bool kE4m3, int kGroups, int kA>
+template <int kProduct, int kType, int kGroups, int kA>
 struct TileOperands {
+    static constexpr bool kE4m3 = kType == kTypeE4m3;
     typedef TileLds<kE4m3, kGroups> Lds;
     static constexpr int kG0 = (kGroups + 1) / 2, kG1 = kGroups / 2;  // groups of P0, P1
     static constexpr int kA0 = (kA + 1) / 2, kA1 = kA / 2;            // those with rows
@@ -645,8 +676,8 @@ struct TileOperands {
     // loads of a pair of units; the few of scales are not counted, so now and
     // then a wave waits for one load more than it needs
     static constexpr int kAll0 = kL0 + QTile::kLoads, kAll1 = (kA1 ? kL1 : 0) + QTile::kLoads;
-    static constexpr int kStep = kE4m3 ? 128 : 64;  // contraction elements per step
-    static constexpr int kElem = kE4m3 ? 1 : 2;
+    static constexpr int kElem = element_bytes(kType);
+    static constexpr int kStep = kStepBytes / kElem;  // contraction elements per step
 
     PTile0 p0;
     PTile1 p1;
@@ -746,14 +777,16 @@ struct TileOperands {
     }
 };
 
-template <int kProduct, bool kE4m3, int kGroups>
+template <int kProduct, int kType, int kGroups>
 __device__ __forceinline__ void product_tile(const ProductArgs &a, int block, uint8_t *lds)
 {
+    constexpr bool kE4m3 = kType == kTypeE4m3, kInt8 = kType == kTypeInt8;
+    typedef typename AccumulatorOf<kType>::type Acc;
     typedef TileLds<kE4m3, kGroups> Lds;
     constexpr int kBM = kGroups * 64;
     constexpr int kP1At = Lds::kP1, kQ0At = Lds::kQ0, kQ1At = Lds::kQ1, kStage = Lds::kStage;
     constexpr int kScaleAt = Lds::kScales, kScaleBytes = Lds::kScaleBytes;
-    constexpr int kStep = kE4m3 ? 128 : 64;
+    constexpr int kStep = kStepBytes / element_bytes(kType);
 
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x / kWave);
     const int wm = wave / kTileWavesN, wn = wave % kTileWavesN;
@@ -784,10 +817,10 @@ __device__ __forceinline__ void product_tile(const ProductArgs &a, int block, ui
     w.col0 = t.col_tile * (gated ? kTileCols / 2 : kTileCols);
 
     constexpr int kMI = kGroups * 2;
-    f32x4 acc[kMI][4];
+    Acc acc[kMI][4];
     auto sweep = [&](auto groups) {
         constexpr int kA = decltype(groups)::value;  // 64-row groups that hold rows
-        typedef TileOperands<kProduct, kE4m3, kGroups, kA> Operands;
+        typedef TileOperands<kProduct, kType, kGroups, kA> Operands;
         typedef typename Operands::PTile0 PTile0;
         typedef typename Operands::PTile1 PTile1;
         typedef typename Operands::QTile QTile;
@@ -803,7 +836,7 @@ __device__ __forceinline__ void product_tile(const ProductArgs &a, int block, ui
         for (int i = 0; i < kMI; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                acc[i][j] = f32x4{0, 0, 0, 0};
+                acc[i][j] = Acc{0, 0, 0, 0};
         // scale of row r (column group: row kGroups * 64 + c / 4) in step s
         const auto scale = [&](int s, int r) {
             return reinterpret_cast<const float *>(lds + kScaleAt +
@@ -845,7 +878,7 @@ __device__ __forceinline__ void product_tile(const ProductArgs &a, int block, ui
                     sc[j] = scale(s, kGroups * 64 + h * 32 + c / 4 + (lane >> 4));
             }
         };
-        // bf16: row blocks i0 ... of acc by columns j0, j0 + 1
+        // bf16 and int8: row blocks i0 ... of acc by columns j0, j0 + 1
         const auto multiply = [&](auto count, int i0, int j0, const auto &p, const auto &q) {
             constexpr int kI = decltype(count)::value;
 #pragma unroll
@@ -854,8 +887,7 @@ __device__ __forceinline__ void product_tile(const ProductArgs &a, int block, ui
                 for (int i = 0; i < kI; ++i)
 #pragma unroll
                     for (int j = 0; j < 2; ++j)
-                        acc[i0 + i][j0 + j] =
-                            mfma_bf16(q[j][half], p[i][half], acc[i0 + i][j0 + j]);
+                        multiply_add(q[j][half], p[i][half], acc[i0 + i][j0 + j]);
         };
         // e4m3: the products of a step's 128 features are scaled as they are added
         // to acc, four multiply-adds per matrix instruction.  They follow kLag
@@ -869,7 +901,7 @@ __device__ __forceinline__ void product_tile(const ProductArgs &a, int block, ui
             late_scale[k] = 0.0f;
         }
         const auto add_late = [&](auto row, auto col) {
-            f32x4 &to = acc[decltype(row)::value][decltype(col)::value];
+            Acc &to = acc[decltype(row)::value][decltype(col)::value];
 #pragma unroll
             for (int v = 0; v < 4; ++v)
                 to[v] = __builtin_fmaf(late[0][v], late_scale[0], to[v]);
@@ -975,10 +1007,10 @@ __device__ __forceinline__ void product_tile(const ProductArgs &a, int block, ui
     // residual took 425 us of which 113 were this.)
     f32x4 *out = reinterpret_cast<f32x4 *>(lds + wave * Lds::kOutWave);
     const int lr = lane >> 2, v = lane & 3;  // of 8 columns, when read back
-    const auto through = [&](const f32x4 &lo, const f32x4 &hi, float(&z)[8]) {
+    const auto through = [&](const Acc &lo, const Acc &hi, float(&z)[8]) {
         const int row = lane & 15, quad = lane >> 4;
-        out[row * 8 + (quad ^ (row & 7))] = lo;
-        out[row * 8 + ((quad + 4) ^ (row & 7))] = hi;
+        out[row * 8 + (quad ^ (row & 7))] = to_f32(lo);
+        out[row * 8 + ((quad + 4) ^ (row & 7))] = to_f32(hi);
         // lanes read what others wrote: a wave's LDS accesses keep their order,
         // and here the compiler has to keep it too (it moved the writes of
         // lanes with nothing to store under their condition)
@@ -1006,6 +1038,20 @@ __device__ __forceinline__ void product_tile(const ProductArgs &a, int block, ui
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     bias[h][i] = b[i / 4][i % 4];
+            }
+        }
+    }
+    // int8: the channels' scales, by columns as the biases
+    float channel[2][8] = {};
+    if constexpr (kInt8) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int c = gated ? col[0] + h * a.out_cols : col[h];
+            if ((gated ? col[0] : col[h]) < a.out_cols) {
+                const float *sw = a.weight_scales + (size_t)t.expert * a.weight_rows + c;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    channel[h][i] = sw[i];
             }
         }
     }
@@ -1041,6 +1087,14 @@ __device__ __forceinline__ void product_tile(const ProductArgs &a, int block, ui
                 }
                 if (r >= t.rows || col[h] >= a.out_cols)
                     continue;
+                if constexpr (kInt8) {
+                    const float sx = a.scales[t.row0 + r];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        z[k] *= sx * channel[h][k];
+                        up[k] *= sx * channel[1][k];
+                    }
+                }
                 if constexpr (kProduct == kForward) {
                     finish_forward8(a, t.row0 + r, col[h], z, up, bias[h], bias[1],
                                     res[i][h]);
@@ -1068,15 +1122,14 @@ __device__ __forceinline__ void product_tile(const ProductArgs &a, int block, ui
 }
 #endif
 
-template <bool kE4m3, int kGroups>
+template <int kType, int kGroups>
 __global__ __launch_bounds__(kTileWaves *kWave) void k_product_tile(const ProductArgs a)
 {
 #ifdef __HIP_DEVICE_COMPILE__
-    __shared__ __align__(1024) uint8_t lds[TileLds<kE4m3, kGroups>::kBytes];
-    product_tile<kForward, kE4m3, kGroups>(a, blockIdx.x, lds);
+    __shared__ __align__(1024) uint8_t lds[TileLds<kType == kTypeE4m3, kGroups>::kBytes];
+    product_tile<kForward, kType, kGroups>(a, blockIdx.x, lds);
 #endif
 }
-
 
 // ---------------------------------------------------------------------------
 // Few rows per expert: the weights stream past them
@@ -1094,11 +1147,13 @@ __global__ __launch_bounds__(kTileWaves *kWave) void k_product_tile(const Produc
 
 constexpr int kStreamWaves = 4;
 
-template <bool kE4m3, int kMI, bool kGated>
+template <int kType, int kMI, bool kGated>
 __global__ __launch_bounds__(kStreamWaves *kWave) void k_product_stream(const ProductArgs a)
 {
     constexpr int kQ = kGated ? 2 : 1;
-    __shared__ __align__(16) f32x4 part[kStreamWaves][kMI * kQ][kWave];
+    constexpr bool kE4m3 = kType == kTypeE4m3, kInt8 = kType == kTypeInt8;
+    typedef typename AccumulatorOf<kType>::type Acc;
+    __shared__ __align__(16) Acc part[kStreamWaves][kMI * kQ][kWave];
     __shared__ TileIndex index;
     __shared__ __align__(16) uint8_t turn[kStreamWaves][2][kQ][16 * kStepBytes];
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x / kWave);
@@ -1110,7 +1165,7 @@ __global__ __launch_bounds__(kStreamWaves *kWave) void k_product_stream(const Pr
     const int at = (lane >> 4) * 16;  // this lane's bytes of each half step
     const uint8_t *qp[kQ][2], *pp[kMI];
     const float *sx[kMI], *sw[kQ];
-    const int bytes = a.contract * (kE4m3 ? 1 : 2), blocks = a.contract / 128;
+    const int bytes = a.contract * element_bytes(kType), blocks = a.contract / 128;
 #pragma unroll
     for (int q = 0; q < kQ; ++q) {
         int c;
@@ -1135,12 +1190,12 @@ __global__ __launch_bounds__(kStreamWaves *kWave) void k_product_stream(const Pr
         if constexpr (kE4m3)
             sx[i] = a.scales + (size_t)r * blocks;
     }
-    f32x4 acc[kMI][kQ];
+    Acc acc[kMI][kQ];
 #pragma unroll
     for (int i = 0; i < kMI; ++i)
 #pragma unroll
         for (int q = 0; q < kQ; ++q)
-            acc[i][q] = f32x4{0, 0, 0, 0};
+            acc[i][q] = Acc{0, 0, 0, 0};
 
     auto one = [&](const i32x4 (&w)[kQ][2], const i32x4 (&x)[kMI][2], int s) {
 #pragma unroll
@@ -1155,8 +1210,8 @@ __global__ __launch_bounds__(kStreamWaves *kWave) void k_product_stream(const Pr
                     for (int v = 0; v < 4; ++v)
                         acc[i][q][v] = __builtin_fmaf(d[v], f, acc[i][q][v]);
                 } else {
-                    acc[i][q] = mfma_bf16(w[q][0], x[i][0], acc[i][q]);
-                    acc[i][q] = mfma_bf16(w[q][1], x[i][1], acc[i][q]);
+                    multiply_add(w[q][0], x[i][0], acc[i][q]);
+                    multiply_add(w[q][1], x[i][1], acc[i][q]);
                 }
             }
         }
@@ -1239,15 +1294,29 @@ __global__ __launch_bounds__(kStreamWaves *kWave) void k_product_stream(const Pr
     __syncthreads();
     // wave i finishes row block i, adding the waves' parts in order
     for (int i = wave; i < kMI; i += kStreamWaves) {
+        Acc sum[kQ];
         f32x4 z[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}};
 #pragma unroll
-        for (int q = 0; q < kQ; ++q)
+        for (int q = 0; q < kQ; ++q) {
+            sum[q] = Acc{0, 0, 0, 0};
 #pragma unroll
             for (int w = 0; w < kStreamWaves; ++w)
-                z[q] += part[w][i * kQ + q][lane];
+                sum[q] += part[w][i * kQ + q][lane];
+            z[q] = to_f32(sum[q]);
+        }
         const int r = i * 16 + (lane & 15), c = col0 + (lane >> 4) * 4;
-        if (r < t.rows && c < a.out_cols)
+        if (r < t.rows && c < a.out_cols) {
+            if constexpr (kInt8) {
+                const float sx = a.scales[t.row0 + r];
+                const float *sw = a.weight_scales + (size_t)t.expert * a.weight_rows + c;
+#pragma unroll
+                for (int q = 0; q < kQ; ++q)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v)
+                        z[q][v] *= sx * sw[q * a.out_cols + v];
+            }
             finish_forward(a, t.expert, t.row0 + r, c, z[0], z[1]);
+        }
     }
 }
 
@@ -1418,9 +1487,9 @@ __global__ __launch_bounds__(kTileWaves *kWave) void k_product_grads(const GradA
     }
     block -= a.bias_blocks;
     if (block < a.weight_blocks)
-        product_tile<kGradWeight, false, 4>(a.weight, block, lds);
+        product_tile<kGradWeight, kTypeBf16, 4>(a.weight, block, lds);
     else
-        product_tile<kGradInput, false, kInputGroups>(a.input, block - a.weight_blocks, lds);
+        product_tile<kGradInput, kTypeBf16, kInputGroups>(a.input, block - a.weight_blocks, lds);
 #endif
 }
 

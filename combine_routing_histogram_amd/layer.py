@@ -1,7 +1,8 @@
 """ctypes binding of libepdc_layer.so (include/epdc_layer.h): the gate, the
-experts' matrix products and the gradients.  One Python function per C entry
-point with the same name; arguments are plain integers (device addresses,
-sizes, a hipStream_t as an integer) and the two argument structures.  A
+experts' matrix products, the norm, rows in 8 bits, the layer for few tokens and
+the gradients.  One Python function per C entry point with the same name;
+arguments are plain integers (device addresses, sizes, a hipStream_t as an
+integer) and the argument structures.  A
 non-SUCCESS status raises; there is no fallback.
 """
 from __future__ import annotations
@@ -21,6 +22,7 @@ HEADER = os.path.join(ROOT, "include", "epdc_layer.h")
 EPDC_DT_BF16 = 0
 EPDC_DT_FP32 = 1
 EPDC_DT_E4M3 = 2
+EPDC_DT_INT8 = 3
 EPDC_GATE_SOFTMAX = 0
 EPDC_GATE_SIGMOID = 1
 EPDC_ACT_NONE = 0
@@ -48,8 +50,22 @@ class epdc_product_args(ctypes.Structure):
                                  "expert_off")]
 
 
+class epdc_norm_args(ctypes.Structure):
+    _fields_ = [(n, I32) for n in ("rows", "features", "weight_dtype")] + \
+               [("eps", ctypes.c_float)] + [(n, P) for n in ("input", "residual", "weight")]
+
+
+class epdc_few_args(ctypes.Structure):
+    _fields_ = [(n, I32) for n in ("num_tokens", "topk", "num_experts", "first_expert", "hidden",
+                                   "inner", "dtype", "activation")] + \
+               [(n, P) for n in ("input", "weights", "indices", "w1", "w2", "w1_scales",
+                                 "w2_scales", "bias1", "bias2")]
+
+
 PGATE = ctypes.POINTER(epdc_gate_args)
 PPROD = ctypes.POINTER(epdc_product_args)
+PNORM = ctypes.POINTER(epdc_norm_args)
+PFEW = ctypes.POINTER(epdc_few_args)
 
 _SIGNATURES = {
     "epdc_gate_scratch_bytes": (I32, [I32, I32, ctypes.POINTER(SZ)]),
@@ -58,6 +74,11 @@ _SIGNATURES = {
     "epdc_expert_product": (I32, [PPROD, P, P, P, P]),
     "epdc_expert_backward": (I32, [PPROD, P, P, P, P, P, P, I32, P]),
     "epdc_combine_backward": (I32, [P, I32, I32, I32, P, P, P, P, P, P]),
+    "epdc_rms_norm": (I32, [PNORM, P, P, P, P, P, I32]),
+    "epdc_rms_norm_scratch_bytes": (I32, [I32, ctypes.POINTER(SZ)]),
+    "epdc_rms_norm_backward": (I32, [PNORM, P, P, P, P, P, P]),
+    "epdc_quantize_rows": (I32, [P, I32, I32, I32, P, P, I32, P, P]),
+    "epdc_few_tokens": (I32, [PFEW, P, P, P]),
     "epdc_layer_last_error": (ctypes.c_char_p, []),
 }
 
@@ -110,6 +131,23 @@ def make_product_args(rows: int, num_experts: int, in_features: int, out_feature
                              weight_scales or None, bias or None, expert_off or None)
 
 
+def make_norm_args(rows: int, features: int, weight_dtype: int = EPDC_DT_BF16, eps: float = 1e-6,
+                   input: int = 0, residual: int = 0, weight: int = 0) -> epdc_norm_args:
+    return epdc_norm_args(rows, features, weight_dtype, eps, input or None, residual or None,
+                          weight or None)
+
+
+def make_few_args(num_tokens: int, topk: int, num_experts: int, hidden: int, inner: int,
+                  dtype: int = EPDC_DT_BF16, activation: int = EPDC_ACT_NONE,
+                  first_expert: int = 0, input: int = 0, weights: int = 0, indices: int = 0,
+                  w1: int = 0, w2: int = 0, w1_scales: int = 0, w2_scales: int = 0,
+                  bias1: int = 0, bias2: int = 0) -> epdc_few_args:
+    return epdc_few_args(num_tokens, topk, num_experts, first_expert, hidden, inner, dtype,
+                         activation, input or None, weights or None, indices or None, w1 or None,
+                         w2 or None, w1_scales or None, w2_scales or None, bias1 or None,
+                         bias2 or None)
+
+
 # ---- one wrapper per entry point --------------------------------------------------
 
 def epdc_gate_scratch_bytes(max_tokens: int, num_experts: int) -> int:
@@ -151,6 +189,36 @@ def epdc_combine_backward(stream: int, num_tokens: int, topk: int, hidden: int, 
     _check(lib().epdc_combine_backward(stream or None, num_tokens, topk, hidden, slot_of or None,
                                        grad_output or None, input or None, weights or None,
                                        grad_input or None, grad_weights or None))
+
+
+def epdc_rms_norm(args: epdc_norm_args, stream: int, out: int, sum: int, codes: int, scales: int,
+                  codes_dtype: int) -> None:
+    _check(lib().epdc_rms_norm(ctypes.byref(args), stream or None, out or None, sum or None,
+                               codes or None, scales or None, codes_dtype))
+
+
+def epdc_rms_norm_scratch_bytes(features: int) -> int:
+    n = SZ(0)
+    _check(lib().epdc_rms_norm_scratch_bytes(features, ctypes.byref(n)))
+    return n.value
+
+
+def epdc_rms_norm_backward(args: epdc_norm_args, stream: int, grad_out: int, grad_sum: int,
+                           grad_input: int, grad_weight: int, scratch: int) -> None:
+    _check(lib().epdc_rms_norm_backward(ctypes.byref(args), stream or None, grad_out or None,
+                                        grad_sum or None, grad_input or None, grad_weight or None,
+                                        scratch or None))
+
+
+def epdc_quantize_rows(stream: int, rows: int, features: int, codes_dtype: int, input: int,
+                       expert_off: int, num_experts: int, codes: int, scales: int) -> None:
+    _check(lib().epdc_quantize_rows(stream or None, rows, features, codes_dtype, input or None,
+                                    expert_off or None, num_experts, codes or None,
+                                    scales or None))
+
+
+def epdc_few_tokens(args: epdc_few_args, stream: int, h: int, out: int) -> None:
+    _check(lib().epdc_few_tokens(ctypes.byref(args), stream or None, h or None, out or None))
 
 
 def epdc_layer_last_error() -> str:

@@ -70,6 +70,12 @@ GATE_SCORES = {"softmax": L.EPDC_GATE_SOFTMAX, "sigmoid": L.EPDC_GATE_SIGMOID}
 ACTIVATIONS = {"none": L.EPDC_ACT_NONE, "relu": L.EPDC_ACT_RELU, "gelu": L.EPDC_ACT_GELU,
                "silu": L.EPDC_ACT_SILU, "swiglu": L.EPDC_ACT_SWIGLU, "geglu": L.EPDC_ACT_GEGLU}
 GATED = ("swiglu", "geglu")
+# rows in 8 bits: (type of the codes, columns that features are a multiple of)
+CODES = {"fp8_e4m3_b128": (L.EPDC_DT_E4M3, torch.float8_e4m3fn, 128),
+         "int8_row": (L.EPDC_DT_INT8, torch.int8, 16)}
+WEIGHT_DTYPES = {torch.bfloat16: L.EPDC_DT_BF16, torch.float8_e4m3fn: L.EPDC_DT_E4M3,
+                 torch.int8: L.EPDC_DT_INT8}
+FEW_TOKENS = 64     # the most that few_token_layer takes
 
 
 @dataclasses.dataclass(frozen=True)
@@ -688,27 +694,25 @@ class EpDispatchCombineOp:
         if n < 1 or first_expert < 0 or first_expert + n > cfg.num_experts:
             raise ValueError(f"experts [{first_expert}, {first_expert + n}) are not within "
                              f"[0, {cfg.num_experts})")
-        if weight.dtype == torch.bfloat16:
-            dtype = L.EPDC_DT_BF16
-        elif weight.dtype == torch.float8_e4m3fn:
-            dtype = L.EPDC_DT_E4M3
-        else:
-            raise ValueError(f"weight must be bfloat16 or float8_e4m3fn, got {weight.dtype}")
+        dtype = WEIGHT_DTYPES.get(weight.dtype)
+        if dtype is None:
+            raise ValueError("weight must be bfloat16, float8_e4m3fn or int8, got "
+                             f"{weight.dtype}")
         self._need(input, "input", weight.dtype)
         if input.dim() != 2 or input.shape[1] != in_f or input.shape[0] < rows:
             raise ValueError(f"input must be [>= {rows}, {in_f}], got {tuple(input.shape)}")
-        if dtype == L.EPDC_DT_E4M3:
-            if scales is None or weight_scales is None:
-                raise ValueError("e4m3 operands need scales and weight_scales")
-            blocks = in_f // 128
+        self._need_weight_scales(weight, weight_scales, "weight_scales")
+        if dtype == L.EPDC_DT_BF16:
+            if scales is not None:
+                raise ValueError("scales and weight_scales belong to e4m3 and int8 operands")
+        else:
+            if scales is None:
+                raise ValueError("e4m3 and int8 operands need scales and weight_scales")
+            blocks = in_f // 128 if dtype == L.EPDC_DT_E4M3 else 1
             self._need(scales, "scales", torch.float32)
             if scales.dim() != 2 or scales.shape[0] < rows or scales.shape[1] != blocks:
                 raise ValueError(f"scales must be [>= {rows}, {blocks}], got "
                                  f"{tuple(scales.shape)}")
-            self._need(weight_scales, "weight_scales", torch.float32,
-                       (n, (out_f + 127) // 128, blocks))
-        elif scales is not None or weight_scales is not None:
-            raise ValueError("scales and weight_scales belong to e4m3 operands")
         if bias is not None:
             self._need(bias, "bias", torch.float32, (n, out_f))
         off, _ = B.epdc_get_offsets(self._op)
@@ -717,6 +721,20 @@ class EpDispatchCombineOp:
                                    expected, input.data_ptr(), _ptr(scales),
                                    weight.data_ptr(), _ptr(weight_scales), _ptr(bias),
                                    off + 4 * first_expert)
+
+    def _need_weight_scales(self, weight, scales, name) -> None:
+        """The scales of a weight [n, out, in]: per block of 128 x 128 for e4m3, per channel
+        for int8, none for bf16."""
+        n, out_f, in_f = weight.shape
+        if weight.dtype == torch.bfloat16:
+            if scales is not None:
+                raise ValueError(f"{name} belong to e4m3 and int8 operands")
+        elif scales is None:
+            raise ValueError(f"e4m3 and int8 operands need {name}")
+        elif weight.dtype == torch.int8:
+            self._need(scales, name, torch.float32, (n, out_f))
+        else:
+            self._need(scales, name, torch.float32, (n, (out_f + 127) // 128, in_f // 128))
 
     def _need_rows(self, t, name, rows, cols) -> None:
         self._need(t, name, torch.bfloat16)
@@ -736,9 +754,9 @@ class EpDispatchCombineOp:
         row s of expert first_expert + e.
 
         input: bf16 [>= T*K, in], or float8_e4m3fn with scales fp32 [>= T*K,
-        in/128], as dispatch gives them; weight: [n, out, in] in the same type,
-        e4m3 with weight_scales fp32 [n, ceil(out/128), in/128]; bias: fp32
-        [n, out].  activation: "none", "relu", "gelu", "silu", or "swiglu" /
+        in/128], as dispatch gives them, or int8 with scales fp32 [>= T*K, 1];
+        weight: [n, out, in] in the same type, e4m3 with weight_scales fp32 [n,
+        ceil(out/128), in/128], int8 with [n, out]; bias: fp32 [n, out].  activation: "none", "relu", "gelu", "silu", or "swiglu" /
         "geglu", whose weight holds out/2 gate rows and then out/2 up rows.
         residual: bf16 rows of the result.  preact: bf16 [>= T*K, out], filled
         with the value before the activation for expert_product_backward.
@@ -848,6 +866,182 @@ class EpDispatchCombineOp:
                            device=self.device)
         B.epdc_combine(self._op, self._stream(), grad_output.data_ptr(), 0, 0, grad.data_ptr(), 0)
         return grad
+
+    # ---- the norm before the gate, and rows in 8 bits -----------------------------------------
+    def _norm_args(self, input, weight, residual, eps) -> L.epdc_norm_args:
+        self._need(input, "input", torch.bfloat16)
+        if input.dim() != 2:
+            raise ValueError(f"input must be [rows, features], got {tuple(input.shape)}")
+        if weight.dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError(f"weight must be bfloat16 or float32, got {weight.dtype}")
+        self._need(weight, "weight", None, (input.shape[1],))
+        if residual is not None:
+            self._need(residual, "residual", torch.bfloat16, input.shape)
+        return L.make_norm_args(input.shape[0], input.shape[1],
+                                L.EPDC_DT_BF16 if weight.dtype == torch.bfloat16
+                                else L.EPDC_DT_FP32, eps, input.data_ptr(), _ptr(residual),
+                                weight.data_ptr())
+
+    def _new_codes(self, quant, rows, features):
+        """(dtype, codes, scales) of new rows in 8 bits."""
+        dtype, torch_dtype, unit = CODES[quant]
+        if features % unit:
+            raise ValueError(f"{quant} rows are multiples of {unit} columns, got {features}")
+        codes = torch.empty((rows, features), dtype=torch_dtype, device=self.device)
+        scales = torch.empty((rows, features // 128 if unit == 128 else 1), dtype=torch.float32,
+                             device=self.device)
+        return dtype, codes, scales
+
+    @_on_op_device
+    def add_rms_norm(self, input: torch.Tensor, weight: torch.Tensor,
+                     residual: Optional[torch.Tensor] = None, *, eps: float = 1e-6,
+                     quant: str = "none", output: bool = True,
+                     sum_out: Optional[torch.Tensor] = None):
+        """Root-mean-square norm of input + residual: with s that sum in fp32,
+        y = s * weight / sqrt(mean(s^2) + eps) for every row.
+
+        input, residual: bf16 [rows, features]; weight: bf16 or fp32 [features].
+        quant: "none", or rows in 8 bits of y as dispatch carries and
+        expert_product takes them: "fp8_e4m3_b128" (a scale per 128 columns, as
+        the quantizing dispatch writes) or "int8_row" (one per row).
+
+        Returns (out, sum, codes, scales): out bf16, the rounded y (None unless
+        `output`); sum bf16, the rounded s (None without a residual), in
+        `sum_out` if given, which may be residual itself; codes float8_e4m3fn or
+        int8 with scales fp32 [rows, features/128 or 1], of the unrounded y (None
+        for "none")."""
+        if quant != "none" and quant not in CODES:
+            raise ValueError(f"quant must be one of {['none'] + sorted(CODES)}")
+        if quant == "none" and not output:
+            raise ValueError("neither output nor codes are asked for")
+        args = self._norm_args(input, weight, residual, eps)
+        if residual is None:
+            if sum_out is not None:
+                raise ValueError("sum_out is given without a residual")
+        elif sum_out is None:
+            sum_out = torch.empty_like(input)
+        else:
+            self._need(sum_out, "sum_out", torch.bfloat16, input.shape)
+        out = torch.empty_like(input) if output else None
+        dtype, codes, scales = L.EPDC_DT_BF16, None, None
+        if quant != "none":
+            dtype, codes, scales = self._new_codes(quant, *input.shape)
+        L.epdc_rms_norm(args, self._stream(), _ptr(out), _ptr(sum_out), _ptr(codes),
+                        _ptr(scales), dtype)
+        return out, sum_out, codes, scales
+
+    @_on_op_device
+    def add_rms_norm_backward(self, grad_output: torch.Tensor, input: torch.Tensor,
+                              weight: torch.Tensor, *, eps: float = 1e-6,
+                              grad_sum: Optional[torch.Tensor] = None, need_weight: bool = True):
+        """Gradients of add_rms_norm with respect to out and sum.
+
+        grad_output: bf16 like out; input: the forward's sum (its input where it
+        had no residual); grad_sum: bf16, what flows into sum from elsewhere, or
+        None.  Returns (grad_input bf16, the gradient of input and of residual
+        alike; grad_weight fp32 [features], or None unless `need_weight`)."""
+        args = self._norm_args(input, weight, None, eps)
+        self._need(grad_output, "grad_output", torch.bfloat16, input.shape)
+        if grad_sum is not None:
+            self._need(grad_sum, "grad_sum", torch.bfloat16, input.shape)
+        grad_input = torch.empty_like(input)
+        grad_weight = scratch = None
+        if need_weight:
+            new = lambda n, dtype: torch.empty(n, dtype=dtype, device=self.device)
+            grad_weight = new(input.shape[1], torch.float32)
+            scratch = new(L.epdc_rms_norm_scratch_bytes(input.shape[1]), torch.uint8)
+        L.epdc_rms_norm_backward(args, self._stream(), grad_output.data_ptr(), _ptr(grad_sum),
+                                 grad_input.data_ptr(), _ptr(grad_weight), _ptr(scratch))
+        return grad_input, grad_weight
+
+    @_on_op_device
+    def quantize_rows(self, input: torch.Tensor, quant: str, *, routed: bool = False):
+        """bf16 rows [rows, features] in 8 bits, "fp8_e4m3_b128" or "int8_row" as in
+        add_rms_norm: (codes, scales).  `routed`: input is in the received layout
+        of the last dispatch (expert_product's result); only the rows that hold a
+        pair are read, and the others' codes and scales are left unset."""
+        if quant not in CODES:
+            raise ValueError(f"quant must be one of {sorted(CODES)}")
+        self._need(input, "input", torch.bfloat16)
+        if input.dim() != 2:
+            raise ValueError(f"input must be [rows, features], got {tuple(input.shape)}")
+        rows, off = input.shape[0], 0
+        if routed:
+            rows = self._routed()
+            if input.shape[0] < rows:
+                raise ValueError(f"input needs at least {rows} rows, got {input.shape[0]}")
+            off, _ = B.epdc_get_offsets(self._op)
+        dtype, codes, scales = self._new_codes(quant, rows, input.shape[1])
+        L.epdc_quantize_rows(self._stream(), rows, input.shape[1], dtype, input.data_ptr(), off,
+                             self.config.num_experts, codes.data_ptr(), scales.data_ptr())
+        return codes, scales
+
+    # ---- a layer for few tokens -----------------------------------------------------------------
+    @_on_op_device
+    def few_token_layer(self, input: torch.Tensor, weights: Optional[torch.Tensor],
+                        indices: torch.Tensor, w1: torch.Tensor, w2: torch.Tensor, *,
+                        w1_scales: Optional[torch.Tensor] = None,
+                        w2_scales: Optional[torch.Tensor] = None,
+                        bias1: Optional[torch.Tensor] = None,
+                        bias2: Optional[torch.Tensor] = None, activation: str = "none",
+                        first_expert: int = 0,
+                        out: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """dispatch, both expert products and combine for up to 64 tokens, in two
+        launches: out[t] = sum_k weights[t,k] * (act(input[t] @ w1[e].T + bias1[e])
+        @ w2[e].T + bias2[e]), e = indices[t,k] - first_expert, over the k whose
+        expert is one of these n; a token without one gets 0.
+
+        input: bf16 [T, hidden]; weights fp32 [T, K] (None: 1) and indices int32
+        [T, K] as gate gives them; w1: [n, inner, hidden] (gated: [n, 2 * inner,
+        hidden], gate rows first), w2: [n, hidden, inner], both bf16, float8_e4m3fn
+        or int8 with scales as expert_product's weight_scales; biases fp32 [n, rows].
+        The rows stay bf16 whatever the weights are.
+
+        Returns out, bf16 [T, hidden] (allocated if None; may be input).  The
+        routing of the last dispatch is neither used nor changed."""
+        cfg = self.config
+        if activation not in ACTIVATIONS:
+            raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}")
+        if input.dim() != 2 or input.shape[1] != cfg.hidden:
+            raise ValueError(f"input must be [tokens, {cfg.hidden}], got {tuple(input.shape)}")
+        T = input.shape[0]
+        if T > FEW_TOKENS:
+            raise ValueError(f"at most {FEW_TOKENS} tokens, got {T}")
+        self._need(input, "input", torch.bfloat16)
+        self._need(indices, "indices", torch.int32, (T, cfg.topk))
+        if weights is not None:
+            self._need(weights, "weights", torch.float32, (T, cfg.topk))
+        self._need(w1, "w1")
+        self._need(w2, "w2", w1.dtype)
+        dtype = WEIGHT_DTYPES.get(w1.dtype)
+        if dtype is None:
+            raise ValueError(f"w1 must be bfloat16, float8_e4m3fn or int8, got {w1.dtype}")
+        if w2.dim() != 3 or w2.shape[1] != cfg.hidden:
+            raise ValueError(f"w2 must be [experts, {cfg.hidden}, inner], got {tuple(w2.shape)}")
+        n, _, inner = w2.shape
+        up = 2 * inner if activation in GATED else inner
+        if w1.shape != (n, up, cfg.hidden):
+            raise ValueError(f"w1 must be {(n, up, cfg.hidden)}, got {tuple(w1.shape)}")
+        if n < 1 or first_expert < 0 or first_expert + n > cfg.num_experts:
+            raise ValueError(f"experts [{first_expert}, {first_expert + n}) are not within "
+                             f"[0, {cfg.num_experts})")
+        self._need_weight_scales(w1, w1_scales, "w1_scales")
+        self._need_weight_scales(w2, w2_scales, "w2_scales")
+        if bias1 is not None:
+            self._need(bias1, "bias1", torch.float32, (n, up))
+        if bias2 is not None:
+            self._need(bias2, "bias2", torch.float32, (n, cfg.hidden))
+        if out is None:
+            out = torch.empty_like(input)
+        else:
+            self._need(out, "out", torch.bfloat16, input.shape)
+        h = torch.empty((T * cfg.topk, inner), dtype=torch.bfloat16, device=self.device)
+        args = L.make_few_args(T, cfg.topk, n, cfg.hidden, inner, dtype, ACTIVATIONS[activation],
+                               first_expert, input.data_ptr(), _ptr(weights), indices.data_ptr(),
+                               w1.data_ptr(), w2.data_ptr(), _ptr(w1_scales), _ptr(w2_scales),
+                               _ptr(bias1), _ptr(bias2))
+        L.epdc_few_tokens(args, self._stream(), h.data_ptr(), out.data_ptr())
+        return out
 
     def reset(self) -> None:
         B.epdc_reset(self._op)

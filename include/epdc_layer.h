@@ -9,6 +9,12 @@
  *                     with bias, activation and residual in the epilogue
  *   expert_backward   their gradients: input rows, weights, biases
  *   combine_backward  combine's gradients: expert rows and routing weights
+ *   rms_norm          what stands before the gate: the norm of the residual
+ *                     stream, also as rows in 8 bits for dispatch to carry
+ *   rms_norm_backward its gradients
+ *   quantize_rows     bf16 rows into 8 bits, for a product over them
+ *   few_tokens        dispatch, both products and combine of a layer for few
+ *                     tokens, as two launches
  *
  * (The gradient of dispatch is epdc_combine with weights NULL: the sum of a
  * token's K gradient rows.)
@@ -50,8 +56,19 @@ extern "C" {
 typedef enum epdc_layer_dtype {
     EPDC_DT_BF16 = 0,
     EPDC_DT_FP32 = 1,   /* logits and weight gradients only */
-    EPDC_DT_E4M3 = 2    /* OCP E4M3 with fp32 scales: product operands only */
+    EPDC_DT_E4M3 = 2,   /* OCP E4M3 with fp32 scales: product operands, codes */
+    EPDC_DT_INT8 = 3    /* int8 with fp32 scales: product operands, codes */
 } epdc_layer_dtype;
+
+/*
+ * Rows in 8 bits (codes [rows, features] and scales):
+ *   e4m3  scales [rows, features/128] fp32, per block of 128 columns amax/448: the
+ *         layout and the rounding of dispatch's EPDC_QUANT_FP8_E4M3_B128
+ *   int8  scales [rows] fp32, amax/127 of the row
+ * code = round(x / scale), both divisions fp32 to nearest even; a scale of 0 (all
+ * zeros) gives codes 0.  A block or row that holds a NaN or an infinity gets that
+ * as its scale.
+ */
 
 /* The score a gate takes of its logits. */
 typedef enum epdc_gate_score {
@@ -147,20 +164,25 @@ epdc_status epdc_gate_backward(const epdc_gate_args *args, void *stream, const i
  *         cutting each off (toward zero) at 2^-13 of the largest exponent
  *         among them; everything above that, the blocks' scales included, is
  *         fp32.
+ *   int8: in_features a multiple of 16 below 2^17; scales [rows] fp32, one per
+ *         row, weight_scales [E, out] fp32, one per channel (row of weight); sums
+ *         of products are exact whole numbers, z = sum * (scale * weight_scale) +
+ *         bias in fp32; bias, residual and out as in bf16.
  */
 typedef struct epdc_product_args {
     int32_t rows;            /* [0, 2^30]: rows of input, out, residual, preact */
     int32_t num_experts;     /* [1, 512]: experts of weight, bias, expert_off */
     int32_t in_features;     /* [8, 2^20] */
     int32_t out_features;    /* [8, 2^20]: rows of weight (both halves of a gated one) */
-    int32_t dtype;           /* EPDC_DT_BF16 or EPDC_DT_E4M3 */
+    int32_t dtype;           /* EPDC_DT_BF16, EPDC_DT_E4M3 or EPDC_DT_INT8 */
     int32_t activation;      /* epdc_activation */
     int32_t expected_rows;   /* rows these experts are likely to hold, 0 = all `rows`:
                                 decides which form runs fastest, nothing else */
     const void *input;       /* [rows, in] */
-    const float *scales;     /* e4m3: [rows, in/128], else NULL */
+    const float *scales;     /* e4m3: [rows, in/128], int8: [rows], else NULL */
     const void *weight;      /* [E, out, in] */
-    const float *weight_scales; /* e4m3: [E, ceil(out/128), in/128], else NULL */
+    const float *weight_scales; /* e4m3: [E, ceil(out/128), in/128], int8: [E, out],
+                                   else NULL */
     const float *bias;       /* [E, out] fp32 or NULL */
     const int32_t *expert_off;  /* [E + 1], ascending */
 } epdc_product_args;
@@ -207,6 +229,95 @@ epdc_status epdc_combine_backward(void *stream, int32_t num_tokens, int32_t topk
                                   const int32_t *slot_of, const void *grad_output,
                                   const void *input, const float *weights, void *grad_input,
                                   float *grad_weights);
+
+/*
+ * rms_norm: for every row
+ *   s = input + residual (residual NULL: input), in fp32
+ *   y = s * weight / sqrt(mean(s^2) + eps)
+ *   sum = round(s), out = round(y), codes and scales those of y before its rounding
+ * Rows whose sum of squares is beyond fp32 are right too (eps is nothing beside
+ * it), as long as s * weight is not.
+ */
+typedef struct epdc_norm_args {
+    int32_t rows;            /* [0, 2^30] */
+    int32_t features;        /* multiple of 8, at most 2^15; of 128 for e4m3 codes, 16 for int8 */
+    int32_t weight_dtype;    /* EPDC_DT_BF16 or EPDC_DT_FP32 */
+    float eps;               /* >= 0 */
+    const void *input;       /* [rows, features] bf16 */
+    const void *residual;    /* [rows, features] bf16 or NULL */
+    const void *weight;      /* [features], 16-byte aligned */
+} epdc_norm_args;
+
+/* out [rows, features] bf16, NULL if only codes are wanted; sum [rows, features] bf16
+ * or NULL; codes_dtype EPDC_DT_E4M3 or EPDC_DT_INT8 with codes and scales, or
+ * EPDC_DT_BF16 with both NULL.  Outputs may overlap neither each other nor what the
+ * call reads, except that sum may be residual or input itself. */
+epdc_status epdc_rms_norm(const epdc_norm_args *args, void *stream, void *out, void *sum,
+                          void *codes, float *scales, int32_t codes_dtype);
+
+/* Bytes of scratch a weight gradient needs (host only).  Its contents mean nothing
+ * between calls; calls that share one must be ordered. */
+epdc_status epdc_rms_norm_scratch_bytes(int32_t features, size_t *bytes);
+
+/*
+ * Gradient of rms_norm.  args->input is the sum the forward wrote (its input where
+ * there was no residual), args->residual NULL.  With q = 1/sqrt(mean(s^2) + eps),
+ * n = s q, g = grad_out * weight:
+ *   grad_input  = round(q (g - n mean(g n)) + grad_sum)   [rows, features] bf16
+ *   grad_weight = sum over rows of grad_out * n           [features] fp32 or NULL
+ * grad_sum (bf16 or NULL) is what flows into sum from elsewhere; grad_input is the
+ * gradient of input and of residual alike, and may be grad_out or grad_sum itself.
+ * grad_weight and scratch (16-byte aligned, epdc_rms_norm_scratch_bytes) go together.
+ * No rows: grad_weight 0.
+ */
+epdc_status epdc_rms_norm_backward(const epdc_norm_args *args, void *stream, const void *grad_out,
+                                   const void *grad_sum, void *grad_input, float *grad_weight,
+                                   void *scratch);
+
+/*
+ * quantize_rows: bf16 rows into codes and scales.  features: a multiple of 128 (e4m3)
+ * or 16 (int8), at most 2^17.  With expert_off (of num_experts experts) only rows
+ * [expert_off[0], expert_off[num_experts]) are read and written; NULL: all rows.
+ * codes (16-byte aligned) and scales may overlap neither each other nor the input.
+ */
+epdc_status epdc_quantize_rows(void *stream, int32_t rows, int32_t features, int32_t codes_dtype,
+                               const void *input, const int32_t *expert_off, int32_t num_experts,
+                               void *codes, float *scales);
+
+/*
+ * few_tokens: for every token t
+ *   out[t] = round(sum_k weights[t,k] * (h[t,k] . w2[e]^T + bias2[e]))
+ *   h[t,k] = round(act(input[t] . w1[e]^T + bias1[e])),  e = indices[t,k] - first_expert
+ * over the k whose e is in [0, num_experts); a token without one gets 0.  Equal to
+ * dispatch, both products and combine over the same weights up to the rounding of
+ * the rows between them; the routing of an op is neither used nor changed.  Two
+ * launches.
+ *   e4m3 weights: hidden and inner multiples of 128, scales per block of 128 x 128;
+ *   int8 weights: multiples of 16, scales per channel; both as in expert_product.
+ *   The rows stay bf16: the weights are widened, which is exact.
+ */
+typedef struct epdc_few_args {
+    int32_t num_tokens;      /* [0, 64] */
+    int32_t topk;            /* [1, 16] */
+    int32_t num_experts;     /* [1, 512]: experts of w1, w2, biases */
+    int32_t first_expert;    /* [0, 512]: the index that stands for the first of them */
+    int32_t hidden;          /* multiple of 8, at most 2^20 */
+    int32_t inner;           /* columns of h; multiple of 8, at most 2^20 */
+    int32_t dtype;           /* of w1 and w2: EPDC_DT_BF16, EPDC_DT_E4M3 or EPDC_DT_INT8 */
+    int32_t activation;      /* epdc_activation */
+    const void *input;       /* [T, hidden] bf16 */
+    const float *weights;    /* [T, topk] or NULL (1) */
+    const int32_t *indices;  /* [T, topk] */
+    const void *w1;          /* [E, inner, hidden]; gated: [E, 2 inner, hidden] */
+    const void *w2;          /* [E, hidden, inner] */
+    const float *w1_scales, *w2_scales;   /* as expert_product's weight_scales, or NULL */
+    const float *bias1, *bias2;           /* [E, rows of w1 or w2] or NULL */
+} epdc_few_args;
+
+/* h: workspace [T, topk, inner] bf16, 16-byte aligned, under 2 GiB; out [T, hidden]
+ * bf16.  They may overlap neither each other nor what the call reads, except that out may
+ * be input itself. */
+epdc_status epdc_few_tokens(const epdc_few_args *args, void *stream, void *h, void *out);
 
 /* Thread-local message for the last non-SUCCESS status ("" if none). */
 const char *epdc_layer_last_error(void);

@@ -1,0 +1,286 @@
+"""A layer for few tokens in two launches, against 64 bits.
+
+Bounds, from the operands on: a sum of K products in fp32 is off by K * 2^-23 of the
+absolute values' sum (one rounding or truncation per addition; blocks' scales
+and biases count as one more each), activations are Lipschitz with constant 1.13 and
+evaluated to 2^-19, h is rounded to bf16 (2^-8), and so is the result.  With small whole
+numbers all of it is exact and bits must be equal.
+"""
+import numpy as np
+import pytest
+import torch
+
+from combine_routing_histogram_amd.op import EpDispatchCombineConfig, EpDispatchCombineOp
+from layer_common import DEV, draw_indices, ints, normal
+
+pytestmark = pytest.mark.gpu
+U, LIP, BF = 2.0 ** -8, 1.13, torch.bfloat16
+STEP = {"bf16": 8, "fp8": 128, "int8": 16}
+
+
+def _act(z, name):
+    F = torch.nn.functional
+    if name in ("swiglu", "geglu"):
+        g, u = z.chunk(2, dim=1)
+        return (F.silu if name == "swiglu" else F.gelu)(g) * u
+    return {"none": lambda v: v, "relu": F.relu, "gelu": F.gelu, "silu": F.silu}[name](z)
+
+
+def _weight(rng, shape, kind):
+    """(weight, scales, its values in 64 bits)"""
+    n, o, i = shape
+    if kind == "bf16":
+        w = normal(rng, shape, i ** -0.5)
+        return w, None, w.double()
+    if kind == "int8":
+        w = torch.from_numpy(rng.integers(-128, 128, shape).astype(np.int8)).to(DEV)
+        s = torch.from_numpy(rng.uniform(0.5, 2, (n, o)).astype(np.float32)).to(DEV)
+        s *= i ** -0.5 / 64
+        return w, s, w.double() * s.double()[..., None]
+    w = normal(rng, shape).to(torch.float8_e4m3fn)
+    blocks = ((o + 127) // 128, i // 128)
+    s = torch.from_numpy(rng.uniform(0.5, 2, (n,) + blocks).astype(np.float32)).to(DEV)
+    s *= i ** -0.5
+    full = s.double().repeat_interleave(128, 1)[:, :o].repeat_interleave(128, 2)
+    return w, s, w.double() * full
+
+
+class Few:
+    """A layer's tensors and its op."""
+
+    def __init__(self, T, K, E, H, I, kind="bf16", act="swiglu", bias=False, seed=0, idx=None):
+        rng = np.random.default_rng(seed)
+        self.act, self.K, self.E = act, K, E
+        up = 2 * I if act in ("swiglu", "geglu") else I
+        self.op = EpDispatchCombineOp(EpDispatchCombineConfig(max(T, 1), H, K, E, 1), DEV)
+        self.idx = draw_indices(rng, T, K, E) if idx is None else np.asarray(idx, np.int32)
+        self.indices = torch.from_numpy(self.idx).to(DEV)
+        self.x = normal(rng, (T, H))
+        self.w = torch.softmax(normal(rng, (T, K), dtype=torch.float32), 1)
+        self.w1, self.s1, self.d1 = _weight(rng, (E, up, H), kind)
+        self.w2, self.s2, self.d2 = _weight(rng, (E, H, I), kind)
+        self.b1 = normal(rng, (E, up), dtype=torch.float32) if bias else None
+        self.b2 = normal(rng, (E, H), dtype=torch.float32) if bias else None
+
+    def run(self, **kw):
+        args = dict(w1_scales=self.s1, w2_scales=self.s2, bias1=self.b1, bias2=self.b2,
+                    activation=self.act)
+        return self.op.few_token_layer(self.x, self.w, self.indices, self.w1, self.w2,
+                                       **dict(args, **kw))
+
+    def reference(self, first=0, weighted=True):
+        x = self.x.double()
+        H, K1, K2 = x.shape[1], self.d1.shape[2], self.d2.shape[2]
+        y = torch.zeros_like(x)
+        tol, size = torch.zeros_like(x), torch.zeros_like(x)
+        for t in range(x.shape[0]):
+            for k in range(self.K):
+                e = int(self.idx[t, k]) - first
+                if not 0 <= e < self.d1.shape[0]:
+                    continue
+                w1, w2 = self.d1[e].t().contiguous(), self.d2[e].t().contiguous()
+                z = torch.mm(x[t:t + 1], w1)
+                dz = (K1 + 2) * 2.0 ** -23 * torch.mm(x[t:t + 1].abs(), w1.abs())
+                if self.b1 is not None:
+                    z = z + self.b1[e].double()
+                    dz = dz + 2.0 ** -23 * z.abs()
+                h = _act(z, self.act)
+                if self.act in ("swiglu", "geglu"):
+                    g, u = z.chunk(2, dim=1)
+                    dg, du = dz.chunk(2, dim=1)
+                    dh = LIP * dg * (u.abs() + du) + (LIP * g.abs() + dg) * du
+                    dh = dh + 2.0 ** -19 * h.abs()
+                else:
+                    dh = LIP * dz + (2.0 ** -19 * (h.abs() + z.abs()) if self.act != "none" else 0)
+                dh = dh + U * (h.abs() + dh)
+                o = torch.mm(h, w2)
+                do = torch.mm(dh, w2.abs()) + (K2 + 2) * 2.0 ** -23 * torch.mm(h.abs() + dh,
+                                                                             w2.abs())
+                if self.b2 is not None:
+                    o = o + self.b2[e].double()
+                w = float(self.w[t, k]) if weighted else 1.0
+                y[t] += w * o[0]
+                tol[t] += abs(w) * do[0]
+                size[t] += abs(w) * o[0].abs()
+        tol = tol + (2 * self.K + 8) * 2.0 ** -23 * size
+        return y, tol + U * (y.abs() + tol) + 1e-30
+
+
+def _within(got, ref, tol, what=""):
+    err = (got.double() - ref).abs()
+    assert bool((err <= tol).all()), \
+        f"{what}: off by {float((err - tol).max())} beyond the bound, worst {float(err.max())}"
+
+
+# (T, K, E, hidden / step, inner / step): one token, one expert, row tiles that end at 16, 17
+# and 32, more than 32 tokens of one expert, columns and contractions that end inside a tile
+SHAPES = [(1, 1, 1, 1, 1), (1, 8, 64, 9, 5), (2, 2, 3, 3, 2), (16, 1, 1, 5, 3), (16, 4, 8, 17, 4),
+          (17, 2, 4, 4, 9), (33, 1, 1, 3, 3), (64, 3, 4, 5, 2), (64, 16, 40, 2, 1)]
+
+
+@pytest.mark.parametrize("kind", sorted(STEP))
+@pytest.mark.parametrize("T,K,E,h,i", SHAPES)
+def test_layer(T, K, E, h, i, kind):
+    H, I = h * STEP[kind], i * STEP[kind]
+    print(f"few {kind} T={T} K={K} E={E} H={H} I={I}", flush=True)
+    for act, bias in (("swiglu", False), ("gelu", True)):
+        m = Few(T, K, E, H, I, kind, act, bias, seed=T + h)
+        y, tol = m.reference()
+        got = m.run()
+        _within(got, y, tol, act)
+        assert torch.equal(m.run(), got)
+
+
+@pytest.mark.parametrize("act", ["none", "relu", "silu", "geglu"])
+@pytest.mark.parametrize("kind", sorted(STEP))
+def test_activations(kind, act):
+    m = Few(9, 3, 6, 384, 256, kind, act, True, seed=5)
+    y, tol = m.reference()
+    _within(m.run(), y, tol, act)
+
+
+@pytest.mark.parametrize("kind", sorted(STEP))
+@pytest.mark.parametrize("T,H,I", [(5, 256, 128), (40, 1408, 640)])
+def test_whole_numbers(T, H, I, kind):
+    """Weights of -1, 0 and 1, few of them not 0: every sum is a whole number below 257."""
+    rng = np.random.default_rng(H)
+    E, K = 4, 2
+    m = Few(T, K, E, H, I, "bf16", "none", seed=1)
+    sparse = lambda shape: ints(rng, shape) * (torch.from_numpy(rng.random(shape)).to(DEV) < 0.03)
+    m.x, m.w1, m.w2 = ints(rng, (T, H)), sparse((E, I, H)).to(BF), sparse((E, H, I)).to(BF)
+    m.w = torch.full((T, K), 2.0, device=DEV)
+    m.d1, m.d2 = m.w1.double(), m.w2.double()
+    if kind != "bf16":
+        t = torch.int8 if kind == "int8" else torch.float8_e4m3fn
+        shapes = [(E, I), (E, H)] if kind == "int8" else [(E, -(-I // 128), H // 128),
+                                                          (E, H // 128, -(-I // 128))]
+        m.w1, m.w2 = m.w1.to(t), m.w2.to(t)
+        m.s1, m.s2 = (torch.ones(s, device=DEV) for s in shapes)
+    y, _ = m.reference()
+    assert float(y.abs().max()) <= 256
+    got = m.run()
+    assert torch.equal(got.double(), y)
+    m.w = None
+    y, _ = m.reference(weighted=False)
+    assert torch.equal(m.run().double(), y)
+
+
+@pytest.mark.parametrize("kind", sorted(STEP))
+def test_dropped_repeated_and_foreign_experts(kind):
+    """Pairs without an expert, an expert twice, tokens without any, and weights full of NaN
+    in experts that only other tokens ask for, or none."""
+    T, K, E = 20, 4, 6
+    rng = np.random.default_rng(8)
+    idx = draw_indices(rng, T, K, E - 1)
+    idx[:, 3] = idx[:, 0]
+    idx[::3, 1] = -1
+    idx[4] = -1
+    idx[7] = [-1, E, 2 ** 31 - 1, -2 ** 31]
+    m = Few(T, K, E, 256, 128, kind, "swiglu", True, seed=2, idx=idx)
+    y, tol = m.reference()
+    clean = m.run()
+    _within(clean, y, tol)
+    assert not clean[4].any() and not clean[7].any()
+    # nobody's expert, then one that only token 0 asks for
+    bad = float("nan")
+    for t in (m.b1, m.b2) + ((m.w1, m.w2) if kind == "bf16" else (m.s1, m.s2)):
+        t[E - 1] = bad
+    assert torch.equal(m.run(), clean)
+    idx = m.idx.copy()
+    idx[0, 2] = E - 1
+    m.indices = torch.from_numpy(idx).to(DEV)
+    got = m.run()
+    assert bool(got[0].isnan().all())
+    ok = torch.arange(T, device=DEV) != 0
+    _within(got[ok], y[ok], tol[ok])
+
+
+def test_some_of_the_experts_and_buffers():
+    """The experts of one rank: the parts of all ranks add up to the layer; a given buffer,
+    and the input's own, hold the same."""
+    m = Few(24, 4, 8, 264, 72, seed=3)
+    y, tol = m.reference()
+    whole = m.run()
+    total, bound = torch.zeros_like(y), tol.clone()
+    for first in (0, 3):
+        n = 3 if first == 0 else 5
+        part = m.op.few_token_layer(m.x, m.w, m.indices, m.w1[first:first + n].contiguous(),
+                                    m.w2[first:first + n].contiguous(), activation="swiglu",
+                                    first_expert=first)
+        total += part.double()
+        bound += U * part.double().abs() + tol
+    _within(total, y, bound)
+    out = torch.full((24, 264), 7.0, dtype=BF, device=DEV)
+    assert m.run(out=out) is out and torch.equal(out, whole)
+    m.run(out=m.x)
+    assert torch.equal(m.x, whole)
+
+
+def test_no_tokens():
+    m = Few(0, 2, 4, 64, 32)
+    assert m.run().shape == (0, 64)
+
+
+def test_nothing_is_written_past_the_result():
+    m = Few(5, 2, 4, 72, 40, seed=4)
+    buf = torch.full((7, 72), 3.0, dtype=BF, device=DEV)
+    m.run(out=buf[1:6])
+    assert bool((buf[0] == 3).all()) and bool((buf[6] == 3).all())
+
+
+def test_many_experts():
+    """512 experts, of which 1024 pairs ask for most."""
+    m = Few(64, 16, 512, 64, 32, "int8", seed=6)
+    y, tol = m.reference()
+    _within(m.run(), y, tol)
+
+
+def test_equals_the_separate_steps():
+    """What dispatch, both products and combine give, up to the rounding of the rows between
+    them: both are within the bound of 64 bits, dispatch's way with one more rounding."""
+    m = Few(32, 4, 8, 512, 256, "bf16", "swiglu", True, seed=7)
+    y, tol = m.reference()
+    few = m.run()
+    rows, row_w, _, _, _ = m.op.dispatch(m.x, m.w, None, m.indices)
+    h = m.op.expert_product(rows, m.w1, bias=m.b1, activation="swiglu")
+    o = m.op.expert_product(h, m.w2, bias=m.b2)
+    steps, _ = m.op.combine(o, row_w)
+    size = torch.zeros_like(y)
+    slot = m.op.get_routing()[2].reshape(-1, 4).long()
+    for k in range(4):
+        size += (o[slot[:, k]].double() * m.w[:, k:k + 1].double()).abs()
+    _within(few, steps.double(), 2 * tol + 2 * U * size)
+    # and leaves the recorded routing alone
+    again, _ = m.op.combine(o, row_w)
+    assert torch.equal(again, steps)
+
+
+def test_captured_and_on_another_stream():
+    """Gate and layer in one graph, replayed on new inputs with eager steps between."""
+    T, K, E, H, I = 8, 2, 16, 128, 64
+    m = Few(T, K, E, H, I, "int8", seed=9)
+    logits = normal(np.random.default_rng(0), (T, E), dtype=torch.float32)
+
+    def step():
+        w, i = m.op.gate(logits)
+        return m.op.few_token_layer(m.x, w, i, m.w1, m.w2, w1_scales=m.s1, w2_scales=m.s2,
+                                    activation="swiglu")
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = step()
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(got, step())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = step()
+    for k in range(4):
+        rng = np.random.default_rng(k + 10)
+        m.x.copy_(normal(rng, (T, H)))
+        logits.copy_(normal(rng, (T, E), dtype=torch.float32))
+        want = step().clone()
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want), k
