@@ -455,27 +455,100 @@ void launch_int8(hipStream_t st, const QuantArgs &a)
 
 // ---- a layer for few tokens -----------------------------------------------------------
 
-template <int kType, int kMI>
+epdc_status check_few(const epdc_few_args *args, int *of_type)
+{
+    if (!args)
+        return fail(EPDC_ERR_INVALID_ARGS, "args is NULL");
+    const epdc_few_args &p = *args;
+    if (p.num_tokens < 0 || p.num_tokens > kFewTokens)
+        return fail(EPDC_ERR_INVALID_ARGS, "num_tokens must be in [0, %d]", kFewTokens);
+    if (p.topk < 1 || p.topk > kMaxTopk)
+        return fail(EPDC_ERR_INVALID_ARGS, "topk must be in [1, %d]", kMaxTopk);
+    if (p.num_experts < 1 || p.num_experts > kMaxExperts || p.first_expert < 0 ||
+        p.first_expert > kMaxExperts)
+        return fail(EPDC_ERR_INVALID_ARGS,
+                    "num_experts must be in [1, %d] and first_expert in [0, %d]", kMaxExperts,
+                    kMaxExperts);
+    if (p.activation < EPDC_ACT_NONE || p.activation > EPDC_ACT_GEGLU)
+        return fail(EPDC_ERR_INVALID_ARGS, "unknown activation %d", p.activation);
+    int type;
+    if (!product_type(p.dtype, &type))
+        return fail(EPDC_ERR_INVALID_ARGS, "weights must be bf16, e4m3 or int8");
+    const int unit = unit_features(type);
+    if (p.hidden < unit || p.hidden > kMaxFeatures || p.hidden % unit || p.inner < unit ||
+        p.inner > kMaxFeatures || p.inner % unit)
+        return fail(EPDC_ERR_INVALID_ARGS, "hidden and inner must be multiples of %d, at most %d",
+                    unit, kMaxFeatures);
+    const bool gated = act_gated(p.activation);
+    const int64_t H = p.hidden, I = p.inner, up = gated ? 2 * I : I;
+    if (up * H * element_bytes(type) > kMaxExpertBytes ||
+        (int64_t)p.num_tokens * p.topk * I * 2 > kMaxExpertBytes)
+        return fail(EPDC_ERR_INVALID_ARGS,
+                    "one expert's weight, and the rows of h, must be smaller than 2 GiB");
+    *of_type = type;
+    return EPDC_SUCCESS;
+}
+
+template <int kType, int kRows>
 epdc_status launch_few(hipStream_t st, const FewArgs &a)
 {
-    const int pairs = a.tokens * a.topk, most = pairs < a.experts ? pairs : a.experts;
-    const int up = most * ((a.inner + 15) / 16), down = (a.hidden + 15) / 16;
+    const int64_t tiles =
+        row_tile_bound(a.tokens * a.topk, a.experts, kRows) * ((a.inner + 15) / 16);
+    const int up = (int)(tiles < kFewUpBlocks ? tiles : kFewUpBlocks);
+    const int down = (a.hidden + 15) / 16 * a.splits;
     epdc_status s = launch("k_few_up", [&] {
         if (act_gated(a.act))
-            k_few_up<kType, kMI, true><<<up, kFewUpWaves * kWave, 0, st>>>(a);
+            k_few_up<kType, kRows, true><<<up, kFewUpWaves * kWave, 0, st>>>(a);
         else
-            k_few_up<kType, kMI, false><<<up, kFewUpWaves * kWave, 0, st>>>(a);
+            k_few_up<kType, kRows, false><<<up, kFewUpWaves * kWave, 0, st>>>(a);
     });
     if (s == EPDC_SUCCESS)
         s = launch("k_few_down",
-                   [&] { k_few_down<kType, kMI><<<down, kFewDownWaves * kWave, 0, st>>>(a); });
+                   [&] { k_few_down<kType, kRows><<<down, kFewDownWaves * kWave, 0, st>>>(a); });
+    return s;
+}
+
+// Blocks that share a column tile of the down product: as many as give every CU two, but
+// no wave fewer than four steps, which take about as long as joining the blocks' sums.
+int few_splits(int type, int64_t pairs, int experts, int hidden, int inner)
+{
+    const int tiles = (hidden + 15) / 16, step = kStepBytes / element_bytes(type);
+    const int64_t active = pairs < experts ? pairs : experts;
+    const int64_t steps = active * ((inner + step - 1) / step);
+    int64_t n = 512 / tiles;
+    n = n < steps / (4 * kFewDownWaves) ? n : steps / (4 * kFewDownWaves);
+    return (int)(n < 1 ? 1 : n < kFewMostSplits ? n : kFewMostSplits);
+}
+
+// Scratch: h, then the tickets and the sums of the down product's blocks.
+struct FewScratch {
+    int splits;
+    int64_t h, ticket, partial;   // bytes of each, multiples of 256
+    int64_t bytes() const { return h + ticket + partial; }
+};
+
+FewScratch few_scratch(const epdc_few_args &p, int type)
+{
+    const auto whole = [](int64_t n) { return (n + 255) / 256 * 256; };
+    const int64_t pairs = (int64_t)p.num_tokens * p.topk, tiles = (p.hidden + 15) / 16;
+    FewScratch s;
+    s.splits = few_splits(type, pairs, p.num_experts, p.hidden, p.inner);
+    s.h = whole(pairs * p.inner * 2);
+    s.ticket = s.splits > 1 ? whole(tiles * 4) : 0;
+    s.partial = s.splits > 1 ? whole(tiles * s.splits * p.num_tokens * 16 * 4) : 0;
     return s;
 }
 
 template <int kType>
 epdc_status launch_few_rows(hipStream_t st, const FewArgs &a)
 {
-    return a.tokens <= 16 ? launch_few<kType, 1>(st, a) : launch_few<kType, 2>(st, a);
+    constexpr int kLine = few_line_rows(kType);
+    const int mean = a.tokens * a.topk / a.experts;
+    if (a.tokens <= kLine || mean <= kLine / 2)
+        return launch_few<kType, kLine>(st, a);
+    if (a.tokens <= 16 || mean <= 10)
+        return launch_few<kType, 16>(st, a);
+    return launch_few<kType, 32>(st, a);
 }
 
 }  // namespace
@@ -1022,58 +1095,51 @@ epdc_status epdc_quantize_rows(void *stream, int32_t rows, int32_t features, int
     return s == EPDC_SUCCESS ? ok() : s;
 }
 
-epdc_status epdc_few_tokens(const epdc_few_args *args, void *stream, void *h, void *out)
+epdc_status epdc_few_tokens_scratch_bytes(const epdc_few_args *args, size_t *bytes)
 {
-    if (!args)
-        return fail(EPDC_ERR_INVALID_ARGS, "args is NULL");
-    const epdc_few_args &p = *args;
-    if (p.num_tokens < 0 || p.num_tokens > kFewTokens)
-        return fail(EPDC_ERR_INVALID_ARGS, "num_tokens must be in [0, %d]", kFewTokens);
-    if (p.topk < 1 || p.topk > kMaxTopk)
-        return fail(EPDC_ERR_INVALID_ARGS, "topk must be in [1, %d]", kMaxTopk);
-    if (p.num_experts < 1 || p.num_experts > kMaxExperts || p.first_expert < 0 ||
-        p.first_expert > kMaxExperts)
-        return fail(EPDC_ERR_INVALID_ARGS,
-                    "num_experts must be in [1, %d] and first_expert in [0, %d]", kMaxExperts,
-                    kMaxExperts);
-    if (p.activation < EPDC_ACT_NONE || p.activation > EPDC_ACT_GEGLU)
-        return fail(EPDC_ERR_INVALID_ARGS, "unknown activation %d", p.activation);
     int type;
-    if (!product_type(p.dtype, &type))
-        return fail(EPDC_ERR_INVALID_ARGS, "weights must be bf16, e4m3 or int8");
-    const int unit = unit_features(type);
-    if (p.hidden < unit || p.hidden > kMaxFeatures || p.hidden % unit || p.inner < unit ||
-        p.inner > kMaxFeatures || p.inner % unit)
-        return fail(EPDC_ERR_INVALID_ARGS, "hidden and inner must be multiples of %d, at most %d",
-                    unit, kMaxFeatures);
+    const epdc_status s = check_few(args, &type);
+    if (s != EPDC_SUCCESS)
+        return s;
+    if (!bytes)
+        return fail(EPDC_ERR_INVALID_ARGS, "bytes is required");
+    *bytes = (size_t)few_scratch(*args, type).bytes();
+    return ok();
+}
+
+epdc_status epdc_few_tokens(const epdc_few_args *args, void *stream, void *scratch, void *out)
+{
+    int type;
+    epdc_status s = check_few(args, &type);
+    if (s != EPDC_SUCCESS)
+        return s;
+    const epdc_few_args &p = *args;
     const bool gated = act_gated(p.activation);
     const int64_t T = p.num_tokens, pairs = T * p.topk, E = p.num_experts, H = p.hidden,
                   I = p.inner, up = gated ? 2 * I : I, elem = element_bytes(type);
-    if (up * H * elem > kMaxExpertBytes || pairs * I * 2 > kMaxExpertBytes)
-        return fail(EPDC_ERR_INVALID_ARGS,
-                    "one expert's weight, and the rows of h, must be smaller than 2 GiB");
     const bool scaled = type != kTypeBf16;
     if (scaled != (p.w1_scales != nullptr) || scaled != (p.w2_scales != nullptr))
         return fail(EPDC_ERR_INVALID_ARGS,
                     "w1_scales and w2_scales belong to e4m3 and int8 weights, both of them");
-    if (T > 0 && (!p.input || !p.indices || !p.w1 || !p.w2 || !h || !out))
-        return fail(EPDC_ERR_INVALID_ARGS, "input, indices, w1, w2, h and out are required");
-    if (!aligned(p.input, 16) || !aligned(p.w1, 16) || !aligned(p.w2, 16) || !aligned(h, 16) ||
-        !aligned(out, 16) || !aligned(p.weights, 4) || !aligned(p.indices, 4) ||
+    if (T > 0 && (!p.input || !p.indices || !p.w1 || !p.w2 || !scratch || !out))
+        return fail(EPDC_ERR_INVALID_ARGS, "input, indices, w1, w2, scratch and out are required");
+    if (!aligned(p.input, 16) || !aligned(p.w1, 16) || !aligned(p.w2, 16) ||
+        !aligned(scratch, 256) || !aligned(out, 16) || !aligned(p.weights, 4) || !aligned(p.indices, 4) ||
         !aligned(p.w1_scales, 4) || !aligned(p.w2_scales, 4) || !aligned(p.bias1, 4) ||
         !aligned(p.bias2, 4))
-        return fail(EPDC_ERR_INVALID_ARGS, "input, w1, w2, h and out must be 16-byte aligned, the "
-                                           "other arrays 4-byte aligned");
+        return fail(EPDC_ERR_INVALID_ARGS, "input, w1, w2 and out must be 16-byte aligned, scratch "
+                                           "256-byte aligned, the other arrays 4-byte aligned");
     if (T == 0)
         return ok();
+    const FewScratch parts = few_scratch(p, type);
     const Array x = {"input", p.input, T * H * 2}, rw = {"weights", p.weights, pairs * 4},
                 ids = {"indices", p.indices, pairs * 4}, w1 = {"w1", p.w1, E * up * H * elem},
                 w2 = {"w2", p.w2, E * H * I * elem},
                 s1 = {"w1_scales", p.w1_scales, weight_scales(type, E, up, H) * 4},
                 s2 = {"w2_scales", p.w2_scales, weight_scales(type, E, H, I) * 4},
                 b1 = {"bias1", p.bias1, E * up * 4}, b2 = {"bias2", p.bias2, E * H * 4};
-    const Array mid = {"h", h, pairs * I * 2}, to = {"out", out, T * H * 2};
-    epdc_status s = check_apart(mid, {x, rw, ids, w1, w2, s1, s2, b1, b2, to});
+    const Array mid = {"scratch", scratch, parts.bytes()}, to = {"out", out, T * H * 2};
+    s = check_apart(mid, {x, rw, ids, w1, w2, s1, s2, b1, b2, to});
     // the input is not read any more when out is written
     if (s == EPDC_SUCCESS)
         s = check_apart(to, {out == p.input ? Array{} : x, rw, ids, w1, w2, s1, s2, b1, b2});
@@ -1087,6 +1153,7 @@ epdc_status epdc_few_tokens(const epdc_few_args *args, void *stream, void *h, vo
     a.hidden = p.hidden;
     a.inner = p.inner;
     a.act = p.activation;
+    a.per_token = few_per_token(p.topk);
     a.x = static_cast<const uint8_t *>(p.input);
     a.weights = p.weights;
     a.indices = p.indices;
@@ -1096,8 +1163,11 @@ epdc_status epdc_few_tokens(const epdc_few_args *args, void *stream, void *h, vo
     a.s2 = p.w2_scales;
     a.b1 = p.bias1;
     a.b2 = p.bias2;
-    a.h = static_cast<uint8_t *>(h);
+    a.h = static_cast<uint8_t *>(scratch);
     a.out = static_cast<uint8_t *>(out);
+    a.splits = parts.splits;
+    a.ticket = reinterpret_cast<uint32_t *>(a.h + parts.h);
+    a.partial = reinterpret_cast<float *>(a.h + parts.h + parts.ticket);
     hipStream_t st = static_cast<hipStream_t>(stream);
     s = type == kTypeE4m3   ? launch_few_rows<kTypeE4m3>(st, a)
         : type == kTypeInt8 ? launch_few_rows<kTypeInt8>(st, a)

@@ -3,81 +3,171 @@
 //   k_few_up:    h[t, k]  = act(x[t] W1[e]^T + b1[e]),      e = indices[t, k]
 //   k_few_down:  y[t]     = sum_k w[t, k] (h[t, k] W2[e]^T + b2[e])
 //
-// The weights of the experts that are asked for are the traffic, read once as in
-// k_product_stream (whole 128-byte lines past the caches, turned through LDS into
-// fragments); nothing is routed in memory.  Every block finds the experts'
-// tokens from the indices itself: at most 1024, a token set per expert in one
-// 64-bit word.  8-bit weights are widened to bf16, which holds them exactly, so
-// the activations stay bf16.
+// The weights of the experts that are asked for are the traffic, read once in whole
+// 128-byte lines past the caches and turned through LDS into fragments, as in
+// k_product_stream; nothing is routed in memory.  Every block finds the experts' rows
+// from the indices itself: at most 1024, a token set per expert in one 64-bit
+// word.  8-bit weights are widened to bf16, which holds them exactly, so the
+// activations stay bf16.
 #pragma once
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "layer_gate.hpp"
 #include "layer_product.hpp"
 
 namespace epdc_layer {
 
 constexpr int kFewTokens = 64, kFewPairs = 1024;
+// Registers for loads in flight, of the 128 that a wave has where a SIMD holds four.
+constexpr int kFewSlotRegs = 62;
 
 struct FewArgs {
     int32_t tokens, topk, experts, first_expert;
     int32_t hidden, inner, act;
+    uint32_t per_token;   // 2^16 / topk, rounded up past it: p * per_token >> 16 = p / topk
     const uint8_t *x;
     const float *weights;
     const int32_t *indices;
     const uint8_t *w1, *w2;
     const float *s1, *s2, *b1, *b2;
-    uint8_t *h;    // [tokens * topk, inner] bf16
+    uint8_t *h;    // [tokens * topk, inner] bf16: written at the first of a token's pairs
+                   // with an expert
     uint8_t *out;  // [tokens, hidden] bf16
+    // blocks that share the steps of a column tile of y, the sums they leave
+    // [tiles][splits][tokens][16] and their tickets [tiles] (more than one of them)
+    int32_t splits;
+    float *partial;
+    uint32_t *ticket;
 };
 
-// Who asks for which expert, in LDS.
-struct FewRouting {
-    uint64_t tokens[kMaxExperts];   // of an expert of this call
-    int16_t id[kFewPairs];          // expert of a pair, -1 for none of this call's
-    int16_t active[kMaxExperts];    // experts with tokens, ascending
-};
-
-// Fills the routing and ends with a barrier; returns the number of active experts.
-template <int kThreads>
-__device__ inline int few_routing(const FewArgs &a, FewRouting &r)
+__host__ __device__ inline uint32_t few_per_token(int topk) { return 65536u / topk + 1; }
+__device__ inline int few_token(const FewArgs &a, int pair)
 {
-    const int tid = threadIdx.x, lane = tid & 63;
-    for (int e = tid; e < a.experts; e += kThreads)
-        r.tokens[e] = 0;
-    __syncthreads();
-    const int pairs = a.tokens * a.topk;
-    for (int p = tid; p < pairs; p += kThreads) {
-        const uint32_t e = (uint32_t)a.indices[p] - (uint32_t)a.first_expert;
-        const bool in = e < (uint32_t)a.experts;
-        r.id[p] = (int16_t)(in ? e : -1);
-        if (in)
-            atomicOr(reinterpret_cast<unsigned long long *>(&r.tokens[e]),
-                     1ull << (p / a.topk));
-    }
-    __syncthreads();
-    int count = 0;
-    for (int e0 = 0; e0 < a.experts; e0 += 64) {
-        const int e = e0 + lane;
-        const bool some = e < a.experts && r.tokens[e] != 0;
-        const uint64_t set = __ballot(some);
-        if (some && tid < 64)
-            r.active[count + __popcll(set & ((1ull << lane) - 1))] = (int16_t)e;
-        count += __popcll(set);
-    }
-    __syncthreads();
-    return uniform(count);
+    return (int)((uint32_t)pair * a.per_token >> 16);   // exact for pairs below 1024
 }
 
-// The tokens of a set in ascending order, one per lane of the wave, in `list`.
-__device__ inline int few_rows(uint64_t set, int lane, uint8_t *list)
+// The rows of the experts (one per token and expert, experts and tokens ascending), in
+// LDS, and the units of work they make: up to 4, 8, 16 or 32 rows of an expert.
+struct FewRouting {
+    uint64_t tokens[kMaxExperts];   // that ask for an expert
+    uint16_t start[kMaxExperts];    // first row of an expert
+    uint16_t row[kFewPairs];        // the token, above the first of its pairs (10 bits)
+    uint32_t unit[kMaxExperts + kFewPairs / 4];   // expert, first row, rows
+    int units, rows, pairs;
+};
+
+struct FewUnit {
+    int expert, first, rows;
+};
+
+__device__ inline FewUnit few_unit(const FewRouting &r, int n)
 {
-    if (set >> lane & 1)
-        list[__popcll(set & ((1ull << lane) - 1))] = (uint8_t)lane;
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    return __popcll(set);
+    const uint32_t u = (uint32_t)uniform((int)r.unit[n]);
+    return {(int)(u & 0x3ff), (int)(u >> 10 & 0x7ff), (int)(u >> 21)};
+}
+
+// Sum over the lanes up to this one; eight adds without LDS.
+__device__ inline int sum_upto(int v)
+{
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, true);   // row_shr 1, 2, 4, 8
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);  // row 0 to 1, 2 to 3
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);  // rows 0, 1 to 2, 3
+    return v;
+}
+
+// Fills the routing, and `weight` of a row unless it is NULL, and ends with a barrier;
+// returns the number of units.
+template <int kThreads, int kUnitRows>
+__device__ inline int few_routing(const FewArgs &a, FewRouting &r, float *weight)
+{
+    constexpr int kEach = kFewPairs / kThreads;
+    const int tid = threadIdx.x, lane = tid & 63, pairs = a.tokens * a.topk;
+    uint32_t expert[kEach];
+    float w[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        const int p = i * kThreads + tid;
+        expert[i] = ~0u;
+        w[i] = 1.0f;
+        if (p < pairs) {
+            expert[i] = (uint32_t)a.indices[p] - (uint32_t)a.first_expert;
+            if (weight && a.weights)
+                w[i] = a.weights[p];
+        }
+    }
+    for (int e = tid; e < a.experts; e += kThreads)
+        r.tokens[e] = 0;
+    if (tid == 0)
+        r.pairs = 0;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        if (i * kThreads >= pairs)
+            break;
+        const int p = i * kThreads + tid;
+        const bool in = expert[i] < (uint32_t)a.experts;
+        if (in)
+            atomicOr(reinterpret_cast<unsigned long long *>(&r.tokens[expert[i]]),
+                     1ull << few_token(a, p));
+        const int have = __popcll(__ballot(in));
+        if (lane == 0 && have)
+            atomicAdd(&r.pairs, have);
+    }
+    __syncthreads();
+    if (tid < 64) {
+        int rows = 0, units = 0;
+        for (int e0 = 0; e0 < a.experts; e0 += 64) {
+            const int e = e0 + lane, n = e < a.experts ? __popcll(r.tokens[e]) : 0;
+            const int u = (n + kUnitRows - 1) / kUnitRows;
+            const int upto = sum_upto(n | u << 16);   // both at once: at most 1024 of each
+            const int first = rows + (upto & 0xffff) - n, at = units + (upto >> 16) - u;
+            if (e < a.experts)
+                r.start[e] = (uint16_t)first;
+            for (int i = 0; i < u; ++i) {
+                const int left = n - i * kUnitRows;
+                r.unit[at + i] = (uint32_t)e | (uint32_t)(first + i * kUnitRows) << 10 |
+                                 (uint32_t)(left < kUnitRows ? left : kUnitRows) << 21;
+            }
+            const int all = __builtin_amdgcn_readlane(upto, 63);
+            rows += all & 0xffff;
+            units += all >> 16;
+        }
+        if (lane == 0) {
+            r.units = units;
+            r.rows = rows;
+        }
+    }
+    __syncthreads();
+    const bool repeats = r.rows != r.pairs;   // a token that lists an expert twice
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        const int p = i * kThreads + tid, e = (int)expert[i];
+        if (expert[i] >= (uint32_t)a.experts)
+            continue;
+        const int t = few_token(a, p);
+        bool first = true;
+        if (repeats)
+            for (int k = 0; k < a.topk; ++k) {
+                const int q = t * a.topk + k;
+                if (q == p || a.indices[q] != e + a.first_expert)
+                    continue;
+                first &= q > p;
+                w[i] += a.weights ? a.weights[q] : 1.0f;
+            }
+        if (first) {
+            const int row = r.start[e] + __popcll(r.tokens[e] & ((1ull << t) - 1));
+            r.row[row] = (uint16_t)(t << 10 | p);
+            if (weight)
+                weight[row] = w[i];
+        }
+    }
+    __syncthreads();
+    return uniform(r.units);
 }
 
 // 16 bytes of weight as fragments of 8 bf16: as they are, or widened.
@@ -113,224 +203,342 @@ struct FewWeight {
     }
 };
 
-// A wave's part of rows x columns: kMI * 16 rows of bf16 (x or h) by 16 columns of kQ
-// weights, over the steps [s0, s1) of 128 weight bytes, `stride` steps apart.
-template <int kType, int kMI, int kQ>
+// Rows of a unit whose part of a step one load of a wave holds.
+constexpr int few_line_rows(int type) { return type == kTypeBf16 ? 8 : 4; }
+
+// Registers of a step's loads, and the waves of a SIMD: four where two steps' loads fit
+// into theirs, else two.
+constexpr int few_slot_regs(int type, int rows, int q)
+{
+    return q * 8 + (rows < 16 ? 4 : (rows + 15) / 16 * 16 / element_bytes(type)) +
+           (type != kTypeBf16 ? 1 : 0);
+}
+constexpr int few_waves(int type, int rows, int q)
+{
+    return 2 * few_slot_regs(type, rows, q) <= kFewSlotRegs + 4 ? 4 : 2;
+}
+
+// A wave's share of rows x columns: kRows rows of bf16 (x or h) by 16 columns of kQ
+// weights, a step of 128 weight bytes at a time.  The loads of kDepth steps are in
+// flight: a step's slot is loaded again as soon as it has been multiplied.  Loads past
+// the end of a contraction, or of a wave's steps, give zeros without traffic, so that
+// every step runs the same instructions and waits for its own loads only.
+//
+// Units of few rows take theirs as the weights, a step's part of all of them by one
+// load, and turn them through LDS; 16 or 32 rows come as fragments.  A load instruction
+// of 16 bytes a lane keeps a CU's address unit for 16 cycles whether its lanes are
+// active or not: with fragments for 32 rows beside every 2 KiB of 8-bit weights (ten
+// instructions) 32 tokens through 4 of 64 int8 experts of 2048 x 4096 streamed them at
+// 4.2 TB/s, however many waves or loads in flight.
+template <int kType, int kRows, int kQ>
 struct FewProduct {
     typedef FewWeight<kType> Weight;
     static constexpr int kFrags = Weight::kFrags;
     static constexpr int kStep = kStepBytes / element_bytes(kType);  // elements
-    static constexpr int kTurnBytes = 2 * kQ * 16 * kStepBytes;      // LDS of a wave
-    // steps whose loads are in flight
-    static constexpr int kBatch = kType == kTypeBf16 ? 4 / kMI : 2 / kMI;
+    static constexpr int kMI = (kRows + 15) / 16;
+    static constexpr bool kLine = kRows < 16;
+    static_assert(!kLine || kRows == few_line_rows(kType), "one load holds the rows");
+    static constexpr int kXLoads = kLine ? 1 : kMI * 2 * kFrags;
+    static constexpr int kTurnBytes = 16 * kStepBytes + (kLine ? 1024 : 0);  // LDS of a wave
+    static constexpr bool kBeside = kType != kTypeBf16;
+    static constexpr int kSlotRegs = few_slot_regs(kType, kRows, kQ);
+    static constexpr int kFit = 4 / few_waves(kType, kRows, kQ) * kFewSlotRegs / kSlotRegs;
+    static constexpr int kDepth = kFit < 2 ? 2 : kFit < 4 ? kFit : 4;
+    static_assert(kSlotRegs == kQ * 8 + kXLoads * 4 + (kBeside ? 1 : 0), "registers of a slot");
 
-    int contract, lane, rows;   // rows: that hold a token
+    struct Slot {
+        i32x4 w[kQ][2], x[kXLoads];
+        int beside;   // scales and biases (below)
+    };
+
+    int contract, steps, lane;
     uint8_t *turn;
-    const uint8_t *qp[kQ][2];
-    const float *scale[kQ];     // e4m3: of the columns' block
-    __amdgpu_buffer_rsrc_t p;
-    uint32_t off[kMI];          // of this lane's row and contraction part in p, or kNowhere
+    __amdgpu_buffer_rsrc_t q, p;
+    // 8-bit weights: what belongs to the 16 columns of each part comes with every step, a
+    // word a lane, as a load at a unit's end would wait for all loads in flight.  Lanes 0
+    // to 15 and 16 to 31: int8 the channels' scales of part 0 and 1, e4m3 the scale of
+    // the step's block, 32 to 47 and 48 to 63: the biases.
+    const float *beside_at;
+    int beside;          // of the last step
+    uint32_t qoff[kQ][2];
+    uint32_t off[kMI];   // of this lane's row and contraction part in p, or kNowhere
     f32x4 acc[kMI][kQ];
 
+    const float *nowhere;
+
+    __device__ inline void init(int contraction, int l, uint8_t *t, const uint8_t *rows,
+                                uint32_t bytes, const void *some_word)
+    {
+        nowhere = static_cast<const float *>(some_word);
+        contract = contraction;
+        steps = (contraction + kStep - 1) / kStep;
+        lane = l;
+        turn = t;
+        p = buffer_at(rows, bytes);
+        clear();
+    }
     __device__ inline void clear()
     {
 #pragma unroll
         for (int i = 0; i < kMI; ++i)
 #pragma unroll
-            for (int q = 0; q < kQ; ++q)
-                acc[i][q] = f32x4{0, 0, 0, 0};
+            for (int j = 0; j < kQ; ++j)
+                acc[i][j] = f32x4{0, 0, 0, 0};
     }
-    // from column c0 of each q of expert e's weight, cols columns each (rows in memory)
-    __device__ inline void weights(const uint8_t *w, const float *s, int e, int c0, int cols)
+    // loads from here on are of columns c0 ... c0 + 15 of each of the kQ parts of expert e's
+    // weight, `cols` columns (rows in memory) a part; row(i): the row of p that is row i of
+    // the unit, or -1
+    template <typename F>
+    __device__ inline void expert(const uint8_t *w, const float *s, const float *bias, int e,
+                                  int c0, int cols, F &&row)
     {
-        const size_t bytes = (size_t)contract * element_bytes(kType);
-        w += (size_t)e * kQ * cols * bytes;
+        const uint32_t bytes = (uint32_t)kQ * cols * contract * element_bytes(kType);
+        q = buffer_at(w + (size_t)e * bytes, bytes);
 #pragma unroll
-        for (int q = 0; q < kQ; ++q) {
+        for (int j = 0; j < kQ; ++j)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 int c = c0 + h * 8 + (lane >> 3);
-                c = (c < cols ? c : cols - 1) + q * cols;
-                qp[q][h] = w + c * bytes + (lane & 7) * 16;
+                c = (c < cols ? c : cols - 1) + j * cols;
+                qoff[j][h] = (uint32_t)c * contract * element_bytes(kType) + (lane & 7) * 16;
             }
-            if constexpr (kType == kTypeE4m3) {
-                const int of_expert = (kQ * cols + 127) / 128;
-                scale[q] = s + ((size_t)e * of_expert + (q * cols + c0) / 128) * (contract / 128);
-            }
+#pragma unroll
+        for (int i = 0; i < kMI; ++i) {
+            const int r = row(kLine ? lane / (64 / kRows) : i * 16 + (lane & 15));
+            const int part = kLine ? lane % (64 / kRows) * 16 : (lane >> 4) * (kFrags * 16);
+            off[i] = r < 0 ? kNowhere : (uint32_t)r * contract * 2 + part;
+        }
+        if constexpr (!kBeside)
+            return;
+        // where there is nothing to load, a word of the indices stands in
+        const int part = lane >> 4 & 1 & (kQ - 1), c = c0 + (lane & 15);
+        const size_t col = (size_t)e * kQ * cols + part * cols + (c < cols ? c : cols - 1);
+        beside_at = nowhere;
+        if (lane >= 32) {
+            if (bias)
+                beside_at = bias + col;
+        } else if constexpr (kType == kTypeInt8) {
+            beside_at = s + col;
+        } else if constexpr (kType == kTypeE4m3) {
+            beside_at = s + ((size_t)e * ((kQ * cols + 127) / 128) + (part * cols + c0) / 128) *
+                                (contract / 128);
         }
     }
-    template <bool kTail>
-    __device__ inline void load(int s, i32x4 (&w)[kQ][2], i32x4 (&x)[kMI][2][kFrags])
+    __device__ inline void load(Slot &to, int s)
     {
-        const bool in = !kTail || s * kStep + (lane & 7) * (16 / element_bytes(kType)) < contract;
+        const int left = contract - s * kStep;   // none: past the wave's steps
+        const uint32_t at = (uint32_t)s * kStepBytes, xat = (uint32_t)s * (kStep * 2);
+        const bool in = (lane & 7) * (16 / element_bytes(kType)) < left;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int q = 0; q < kQ; ++q) {
-                const i32x4 *at = reinterpret_cast<const i32x4 *>(qp[q][h] + (size_t)s * kStepBytes);
-                w[q][h] = in ? __builtin_nontemporal_load(at) : i32x4{0, 0, 0, 0};
-            }
+            for (int j = 0; j < kQ; ++j)
+                to.w[j][h] = __builtin_bit_cast(
+                    i32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                               q, in ? qoff[j][h] + at : kNowhere, 0, 2 /* nt */));
 #pragma unroll
-            for (int i = 0; i < kMI; ++i) {
-                if (i * 16 >= rows)
-                    continue;
-#pragma unroll
-                for (int f = 0; f < kFrags; ++f) {
-                    const int el = s * kStep + h * (kStep / 2) + (lane >> 4) * (8 * kFrags) + f * 8;
-                    const uint32_t o = kTail && el >= contract
-                                           ? kNowhere
-                                           : off[i] + (s * kStep + h * (kStep / 2) + f * 8) * 2;
-                    x[i][h][f] = __builtin_bit_cast(
-                        i32x4, __builtin_amdgcn_raw_buffer_load_b128(p, o, 0, 0));
-                }
-            }
+        for (int n = 0; n < kXLoads; ++n) {
+            // fragment f of half h of row tile i
+            const int i = n / (2 * kFrags), h = n / kFrags % 2, f = n % kFrags;
+            const int el = kLine ? 0 : h * (kStep / 2) + f * 8;
+            const int lane_el = kLine ? lane % (64 / kRows) * 8 : (lane >> 4) * (8 * kFrags);
+            to.x[n] = __builtin_bit_cast(
+                i32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                           p, el + lane_el < left ? off[i] + xat + el * 2 : kNowhere, 0, 0));
         }
+        if constexpr (kBeside) {
+            int word = 0;
+            if constexpr (kType == kTypeE4m3)
+                word = lane < 32 ? (s < steps ? s : steps - 1) : 0;
+            to.beside = __float_as_int(beside_at[word]);
+        }
+    }
+    // this lane's four columns of group g of the lanes
+    __device__ inline f32x4 columns(int g) const
+    {
+        f32x4 v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            v[i] = __int_as_float(__shfl(beside, g * 16 + (lane >> 4) * 4 + i, 64));
+        return v;
+    }
+    // and of part j's biases, of expert e's columns from c0 on
+    __device__ inline f32x4 biases(const float *bias, int e, int j, int c0, int cols) const
+    {
+        if constexpr (kBeside)
+            return columns(2 + j);
+        f32x4 v;
+        const float *at = bias + (size_t)e * kQ * cols + j * cols;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int c = c0 + (lane >> 4) * 4 + i;
+            v[i] = at[c < cols ? c : cols - 1];
+        }
+        return v;
     }
     // lines of 8 + 8 columns to fragments of 16; lanes read what others wrote, in
     // the order in which the wave's LDS accesses run
-    __device__ inline void turned(i32x4 (&w)[kQ][2], int buf)
+    __device__ inline void turned(i32x4 (&w)[2])
     {
         typedef StraightTile<16, 1, false> Turn;
-        uint8_t *to = turn + buf * (kQ * 16 * kStepBytes);
 #pragma unroll
-        for (int q = 0; q < kQ; ++q)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int r = h * 8 + (lane >> 3);
-                *reinterpret_cast<i32x4 *>(to + (q * 16 + r) * kStepBytes +
-                                           ((lane & 7) ^ (r & 7)) * 16) = w[q][h];
-            }
+        for (int h = 0; h < 2; ++h) {
+            const int r = h * 8 + (lane >> 3);
+            *reinterpret_cast<i32x4 *>(turn + r * kStepBytes + ((lane & 7) ^ (r & 7)) * 16) = w[h];
+        }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
 #pragma unroll
-        for (int q = 0; q < kQ; ++q)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                w[q][h] = Turn::frag(to + q * 16 * kStepBytes, 0, h, lane);
+        for (int h = 0; h < 2; ++h)
+            w[h] = Turn::frag(turn, 0, h, lane);
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
     }
-    __device__ inline void multiply(int s, const i32x4 (&w)[kQ][2],
-                                    const i32x4 (&x)[kMI][2][kFrags])
+    // rows taken as a line to fragments of 16, of which kRows are its own
+    __device__ inline void turned_rows(i32x4 line, i32x4 (&x)[2][kFrags])
     {
+        constexpr int kChunks = 64 / kRows;   // of 16 bytes, in a row's part of a step
+        uint8_t *at = turn + 16 * kStepBytes;
+        const int to = lane / kChunks, r = lane & (kRows - 1);
+        *reinterpret_cast<i32x4 *>(at + to * (kChunks * 16) +
+                                   ((lane % kChunks) ^ (to & 7)) * 16) = line;
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
 #pragma unroll
-        for (int q = 0; q < kQ; ++q) {
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int f = 0; f < kFrags; ++f) {
+                const int c = h * (kChunks / 2) + (lane >> 4) * kFrags + f;
+                x[h][f] = *reinterpret_cast<const i32x4 *>(at + r * (kChunks * 16) +
+                                                           (c ^ (r & 7)) * 16);
+            }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+    }
+    __device__ inline void multiply(Slot &of)
+    {
+        i32x4 x[kMI][2][kFrags];
+        if constexpr (kLine) {
+            turned_rows(of.x[0], x[0]);
+        } else {
+#pragma unroll
+            for (int n = 0; n < kXLoads; ++n)
+                x[n / (2 * kFrags)][n / kFrags % 2][n % kFrags] = of.x[n];
+        }
+#pragma unroll
+        for (int j = 0; j < kQ; ++j)
+            turned(of.w[j]);
+#pragma unroll
+        for (int j = 0; j < kQ; ++j) {
+            const float scale = kBeside ? __int_as_float(__builtin_amdgcn_readlane(of.beside, j * 16))
+                                        : 1.0f;
             i32x4 f[2][kFrags];
-            Weight::widen(w[q][0], f[0]);
-            Weight::widen(w[q][1], f[1]);
+            Weight::widen(of.w[j][0], f[0]);
+            Weight::widen(of.w[j][1], f[1]);
 #pragma unroll
             for (int i = 0; i < kMI; ++i) {
-                if (i * 16 >= rows)
-                    continue;
-                f32x4 d = kType == kTypeE4m3 ? f32x4{0, 0, 0, 0} : acc[i][q];
+                f32x4 d = kType == kTypeE4m3 ? f32x4{0, 0, 0, 0} : acc[i][j];
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int k = 0; k < kFrags; ++k)
                         d = mfma_bf16(f[h][k], x[i][h][k], d);
                 if constexpr (kType == kTypeE4m3) {
-                    const float by = scale[q][s];
 #pragma unroll
                     for (int v = 0; v < 4; ++v)
-                        acc[i][q][v] = __builtin_fmaf(d[v], by, acc[i][q][v]);
+                        acc[i][j][v] = __builtin_fmaf(d[v], scale, acc[i][j][v]);
                 } else {
-                    acc[i][q] = d;
+                    acc[i][j] = d;
                 }
             }
         }
-    }
-    __device__ inline void run(int s0, int s1, int stride)
-    {
-        const int whole = contract / kStep;
-        int s = s0;
-        for (; s + (kBatch - 1) * stride < (s1 < whole ? s1 : whole); s += kBatch * stride) {
-            i32x4 w[kBatch][kQ][2], x[kBatch][kMI][2][kFrags];
-#pragma unroll
-            for (int b = 0; b < kBatch; ++b)
-                load<false>(s + b * stride, w[b], x[b]);
-#pragma unroll
-            for (int b = 0; b < kBatch; ++b) {
-                turned(w[b], b & 1);
-                multiply(s + b * stride, w[b], x[b]);
-            }
+        // What the slot gives is taken before it is loaded again: else parts of it go to
+        // other registers, whose copies at the end of the loop wait for every load.
+        if constexpr (kBeside) {
+            beside = of.beside;
+            asm volatile("" : "+v"(beside));
         }
-        for (; s < s1; s += stride) {
-            i32x4 w[kQ][2], x[kMI][2][kFrags];
-            load<true>(s, w, x);
-            turned(w, 0);
-            multiply(s, w, x);
+        if constexpr (kType == kTypeE4m3) {
+#pragma unroll
+            for (int i = 0; i < kMI; ++i)
+#pragma unroll
+                for (int j = 0; j < kQ; ++j)
+                    asm volatile("" : "+v"(acc[i][j]));
         }
     }
 };
 
 constexpr int kFewUpWaves = 4, kFewDownWaves = 8;
+constexpr int kFewShort = 4;        // steps of a wave
+constexpr int kFewMostSplits = 8;
+constexpr int kFewUpBlocks = 1024;  // four to a CU
 
-// A block: 16 columns of h (gated: 16 gate and 16 up) of one active expert; its waves
-// take the contraction's steps in turn.
-template <int kType, int kMI, bool kGated>
-__global__ __launch_bounds__(kFewUpWaves *kWave) void k_few_up(const FewArgs a)
+// A tile: 16 columns of h (gated: 16 gate and 16 up) for one unit of rows; a block's
+// waves take the contraction's steps in turn and add up through LDS.  Blocks stay for
+// tile after tile, the next one's loads in flight while a tile ends.
+template <int kType, int kRows, bool kGated>
+__global__ __launch_bounds__(kFewUpWaves *kWave, few_waves(kType, kRows, kGated ? 2 : 1)) void k_few_up(const FewArgs a)
 {
     constexpr int kQ = kGated ? 2 : 1;
-    typedef FewProduct<kType, kMI, kQ> Product;
+    typedef FewProduct<kType, kRows, kQ> Product;
+    constexpr int kMI = Product::kMI;
     __shared__ FewRouting routing;
-    __shared__ __align__(16) f32x4 part[kFewUpWaves][kMI * kQ][kWave];
+    __shared__ __align__(16) f32x4 parts[kFewUpWaves][kMI * kQ][kWave];
     __shared__ __align__(16) uint8_t turn[kFewUpWaves][Product::kTurnBytes];
-    __shared__ uint8_t lists[kFewUpWaves][kFewTokens];
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x / kWave);
-    const int count = few_routing<kFewUpWaves * kWave>(a, routing);
-    const int col_tiles = (a.inner + 15) / 16, n = blockIdx.x / col_tiles;
-    if (n >= count)
+    const int units = few_routing<kFewUpWaves * kWave, kRows>(a, routing, nullptr);
+    const int col_tiles = (a.inner + 15) / 16, tiles = units * col_tiles;
+    int tile = blockIdx.x;
+    if (tile == 0 && a.splits > 1)   // for the launch behind this one
+        for (int i = threadIdx.x; i < (a.hidden + 15) / 16; i += kFewUpWaves * kWave)
+            a.ticket[i] = 0;
+    if (tile >= tiles)
         return;
-    const int e = uniform(routing.active[n]), c0 = (blockIdx.x - n * col_tiles) * 16;
-    const int rows = uniform(few_rows(routing.tokens[e], lane, lists[wave]));
     Product m;
-    m.contract = a.hidden;
-    m.lane = lane;
-    m.turn = turn[wave];
-    m.p = buffer_at(a.x, (uint32_t)a.tokens * a.hidden * 2);
-    const int cols = a.inner * kQ;
-    m.weights(a.w1, a.s1, e, c0, a.inner);
-    const int steps = (a.hidden + Product::kStep - 1) / Product::kStep;
-    for (int r0 = 0; r0 < rows; r0 += kMI * 16) {
-        m.rows = rows - r0;
-#pragma unroll
-        for (int i = 0; i < kMI; ++i) {
-            const int r = r0 + i * 16 + (lane & 15);
-            m.off[i] = r < rows ? (uint32_t)lists[wave][r] * a.hidden * 2 +
-                                      (lane >> 4) * (Product::kFrags * 16)
-                                : kNowhere;
+    m.init(a.hidden, lane, turn[wave], a.x, (uint32_t)a.tokens * a.hidden * 2, a.indices);
+    // every wave runs as many steps of a tile; some of them may lie past the end
+    const int per = (m.steps + kFewUpWaves - 1) / kFewUpWaves;
+    const int count = (tiles - tile + (int)gridDim.x - 1) / (int)gridDim.x * per;
+    int load_tile = tile, load_step = 0, loaded = 0;
+    const auto enter = [&] {
+        const int n = load_tile / col_tiles, c0 = (load_tile - n * col_tiles) * 16;
+        const FewUnit u = few_unit(routing, n);
+        m.expert(a.w1, a.s1, a.b1, u.expert, c0, a.inner, [&](int r) {
+            return r < u.rows ? routing.row[u.first + r] >> 10 : -1;
+        });
+    };
+    const auto next_load = [&](typename Product::Slot &to) {
+        m.load(to, loaded < count ? load_step * kFewUpWaves + wave : m.steps);
+        ++loaded;
+        if (++load_step == per && loaded < count) {
+            load_step = 0;
+            load_tile += gridDim.x;
+            enter();
         }
-        m.clear();
-        m.run(wave, steps, kFewUpWaves);
-        if (r0 > 0)
-            __syncthreads();   // the parts of the rows before have been read
+    };
+    const auto leave = [&] {
+        const int n = tile / col_tiles, c0 = (tile - n * col_tiles) * 16;
+        const FewUnit u = few_unit(routing, n);
+        __syncthreads();   // the last tile's parts have been read
 #pragma unroll
         for (int i = 0; i < kMI; ++i)
 #pragma unroll
             for (int q = 0; q < kQ; ++q)
-                part[wave][i * kQ + q][lane] = m.acc[i][q];
+                parts[wave][i * kQ + q][lane] = m.acc[i][q];
+        m.clear();
         __syncthreads();
         // wave i finishes row block i, adding the waves' parts in order
-        for (int i = wave; i < kMI; i += kFewUpWaves) {
+        if (wave < kMI) {
             f32x4 z[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}};
 #pragma unroll
-            for (int q = 0; q < kQ; ++q)
+            for (int q = 0; q < kQ; ++q) {
 #pragma unroll
                 for (int w = 0; w < kFewUpWaves; ++w)
-                    z[q] += part[w][i * kQ + q][lane];
-            const int r = r0 + i * 16 + (lane & 15), c = c0 + (lane >> 4) * 4;
-            if (r >= rows || c >= a.inner)
-                continue;
-#pragma unroll
-            for (int q = 0; q < kQ; ++q) {
-                const size_t at = (size_t)e * cols + q * a.inner + c;
-#pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    if constexpr (kType == kTypeInt8)
-                        z[q][v] *= a.s1[at + v];
-                    if (a.b1)
-                        z[q][v] += a.b1[at + v];
-                }
+                    z[q] += parts[w][wave * kQ + q][lane];
+                if constexpr (kType == kTypeInt8)
+                    z[q] *= m.columns(q);
+                if (a.b1)
+                    z[q] += m.biases(a.b1, u.expert, q, c0, a.inner);
             }
             f32x4 y;
 #pragma unroll
@@ -339,102 +547,190 @@ __global__ __launch_bounds__(kFewUpWaves *kWave) void k_few_up(const FewArgs a)
                 if (kGated)
                     y[v] *= z[1][v];
             }
-            const int t = lists[wave][r];
-            for (int k = 0; k < a.topk; ++k)
-                if (routing.id[t * a.topk + k] == e)
-                    *reinterpret_cast<bf16x4 *>(
-                        a.h + ((size_t)(t * a.topk + k) * a.inner + c) * 2) = to_bf16(y);
+            const int r = wave * 16 + (lane & 15), c = c0 + (lane >> 4) * 4;
+            if (r < u.rows && c < a.inner)
+                *reinterpret_cast<bf16x4 *>(
+                    a.h + ((size_t)(routing.row[u.first + r] & 0x3ff) * a.inner + c) * 2) =
+                    to_bf16(y);
         }
-    }
+        tile += gridDim.x;
+    };
+    // a short list with few loads in flight: those past its end are not for nothing
+    // (8 pairs of 256 x 128: 6.9 us with eight steps, 6.0 with two)
+    const auto pipeline = [&](auto depth) {
+        constexpr int kDepth = decltype(depth)::value;
+        typename Product::Slot slot[kDepth];
+#pragma unroll
+        for (int b = 0; b < kDepth; ++b)
+            next_load(slot[b]);
+        int step = 0;
+        for (int i = 0; i < count; i += kDepth)
+#pragma unroll
+            for (int b = 0; b < kDepth; ++b) {
+                m.multiply(slot[b]);
+                next_load(slot[b]);
+                if (++step == per && i + b < count) {
+                    leave();
+                    step = 0;
+                }
+            }
+    };
+    enter();
+    if (count <= kFewShort)
+        pipeline(Count<2>());
+    else
+        pipeline(Count<Product::kDepth>());
 }
 
-// A block: 16 columns of y over every active expert.  The experts' contractions end to
-// end are one list of steps, of which each wave takes an equal run; where a run
-// leaves an expert, its sums go, weighted, to the wave's totals of the tokens in
-// LDS, and the waves' totals are added in order.  (Rows of tokens that do not ask
-// for an expert never meet its weights, whatever these hold.)
-template <int kType, int kMI>
-__global__ __launch_bounds__(kFewDownWaves *kWave) void k_few_down(const FewArgs a)
+// A block: 16 columns of y over every unit, or one of a.splits parts of that.  The units'
+// contractions end to end are one list of steps, of which each wave takes an equal run;
+// where a run leaves a unit, its sums go, weighted, to the wave's totals of the tokens in
+// LDS, and the waves' totals are added in order.  (Rows of tokens that do not ask for an
+// expert never meet its weights, whatever these hold.)  Where y has few columns the
+// blocks of a tile share its list; the last to finish adds their sums in order.
+template <int kType, int kRows>
+__global__ __launch_bounds__(kFewDownWaves *kWave, few_waves(kType, kRows, 1)) void k_few_down(const FewArgs a)
 {
-    typedef FewProduct<kType, kMI, 1> Product;
+    typedef FewProduct<kType, kRows, 1> Product;
+    constexpr int kMI = Product::kMI;
     __shared__ FewRouting routing;
+    __shared__ float weight[kFewPairs];
     __shared__ __align__(16) f32x4 total[kFewDownWaves][kFewTokens][4];
     __shared__ __align__(16) uint8_t turn[kFewDownWaves][Product::kTurnBytes];
-    __shared__ uint8_t lists[kFewDownWaves][kFewTokens];
+    __shared__ int last;
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x / kWave);
-    const int count = few_routing<kFewDownWaves * kWave>(a, routing);
-    const int c0 = blockIdx.x * 16;
+    const int units = few_routing<kFewDownWaves * kWave, kRows>(a, routing, weight);
+    const int col_tiles = (a.hidden + 15) / 16, split = blockIdx.x / col_tiles;
+    const int tile = blockIdx.x - split * col_tiles, c0 = tile * 16;
     for (int i = lane; i < a.tokens * 4; i += kWave)
         total[wave][i / 4][i % 4] = f32x4{0, 0, 0, 0};
     Product m;
-    m.contract = a.inner;
-    m.lane = lane;
-    m.turn = turn[wave];
-    m.p = buffer_at(a.h, (uint32_t)a.tokens * a.topk * a.inner * 2);
-    const int steps = (a.inner + Product::kStep - 1) / Product::kStep;
-    const int all = count * steps;
-    int at = (int)((int64_t)all * wave / kFewDownWaves);
-    const int end = (int)((int64_t)all * (wave + 1) / kFewDownWaves);
-    while (at < end) {
-        const int n = at / steps, s0 = at - n * steps;
-        const int left = end - at, s1 = s0 + left < steps ? s0 + left : steps;
-        at += s1 - s0;
-        const int e = uniform(routing.active[n]);
-        const int rows = uniform(few_rows(routing.tokens[e], lane, lists[wave]));
-        m.weights(a.w2, a.s2, e, c0, a.hidden);
-        for (int r0 = 0; r0 < rows; r0 += kMI * 16) {
-            m.rows = rows - r0;
-            int token[kMI];
-            float by[kMI];   // the token's weight for this expert
-#pragma unroll
-            for (int i = 0; i < kMI; ++i) {
-                const int r = r0 + i * 16 + (lane & 15);
-                token[i] = -1;
-                by[i] = 0.0f;
-                m.off[i] = kNowhere;
-                if (r < rows) {
-                    token[i] = lists[wave][r];
-                    for (int k = a.topk - 1; k >= 0; --k) {
-                        const int p = token[i] * a.topk + k;
-                        if (routing.id[p] == e) {
-                            by[i] += a.weights ? a.weights[p] : 1.0f;
-                            m.off[i] = (uint32_t)p * a.inner * 2 +
-                                       (lane >> 4) * (Product::kFrags * 16);
-                        }
-                    }
-                }
-            }
-            m.clear();
-            m.run(s0, s1, 1);
-            const int c = c0 + (lane >> 4) * 4;
-#pragma unroll
-            for (int i = 0; i < kMI; ++i) {
-                if (token[i] < 0 || c >= a.hidden)
-                    continue;
-                f32x4 &sum = total[wave][token[i]][lane >> 4];
-                f32x4 o = m.acc[i][0];
-                const size_t col = (size_t)e * a.hidden + c;
-#pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    if constexpr (kType == kTypeInt8)
-                        o[v] *= a.s2[col + v];
-                    if (a.b2 && s0 == 0)
-                        o[v] += a.b2[col + v];
-                    sum[v] = __builtin_fmaf(by[i], o[v], sum[v]);
-                }
-            }
+    m.init(a.inner, lane, turn[wave], a.h, (uint32_t)a.tokens * a.topk * a.inner * 2, a.indices);
+    const int all = units * m.steps, runs = kFewDownWaves * a.splits;
+    const int run = split * kFewDownWaves + wave;
+    const int begin = (int)((int64_t)all * run / runs);
+    const int count = (int)((int64_t)all * (run + 1) / runs) - begin;
+    // where loads and multiplications are in the list
+    int load_unit = begin / m.steps, load_step = begin - load_unit * m.steps, loaded = 0;
+    int unit = load_unit, step = load_step;
+    bool first = step == 0;
+    const auto enter = [&] {
+        const FewUnit u = few_unit(routing, load_unit);
+        m.expert(a.w2, a.s2, a.b2, u.expert, c0, a.hidden, [&](int r) {
+            return r < u.rows ? routing.row[u.first + r] & 0x3ff : -1;
+        });
+    };
+    const auto next_load = [&](typename Product::Slot &to) {
+        m.load(to, loaded < count ? load_step : m.steps);
+        ++loaded;
+        if (++load_step == m.steps && loaded < count) {
+            load_step = 0;
+            ++load_unit;
+            enter();
         }
+    };
+    // the unit's sums into the totals; its bias with its first step
+    const auto leave = [&] {
+        const FewUnit u = few_unit(routing, unit);
+        const int quad = lane >> 4;
+        f32x4 by = {1, 1, 1, 1}, plus = {0, 0, 0, 0};
+        if constexpr (kType == kTypeInt8)
+            by = m.columns(0);
+        if (a.b2 && first)
+            plus = m.biases(a.b2, u.expert, 0, c0, a.hidden);
+#pragma unroll
+        for (int i = 0; i < kMI; ++i) {
+            const int r = i * 16 + (lane & 15);
+            if (r >= u.rows)
+                continue;
+            const float w = weight[u.first + r];
+            f32x4 &sum = total[wave][routing.row[u.first + r] >> 10][quad];
+            f32x4 t = sum;
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+                t[v] = __builtin_fmaf(w, m.acc[i][0][v] * by[v] + plus[v], t[v]);
+            sum = t;
+        }
+        m.clear();
+    };
+    const auto pipeline = [&](auto depth) {
+        constexpr int kDepth = decltype(depth)::value;
+        typename Product::Slot slot[kDepth];
+#pragma unroll
+        for (int b = 0; b < kDepth; ++b)
+            next_load(slot[b]);
+        for (int i = 0; i < count; i += kDepth)
+#pragma unroll
+            for (int b = 0; b < kDepth; ++b) {
+                m.multiply(slot[b]);
+                next_load(slot[b]);
+                if (i + b == count - 1 || (i + b < count && step == m.steps - 1))
+                    leave();
+                if (++step == m.steps) {
+                    step = 0;
+                    ++unit;
+                    first = true;
+                }
+            }
+    };
+    if (count > 0) {
+        enter();
+        if (count <= kFewShort)
+            pipeline(Count<2>());
+        else
+            pipeline(Count<Product::kDepth>());
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < a.tokens * 4; i += kFewDownWaves * kWave) {
-        const int c = c0 + i % 4 * 4;
-        if (c >= a.hidden)
-            continue;
+    const auto sum_of = [&](int i) {
         f32x4 y = total[0][i / 4][i % 4];
 #pragma unroll
         for (int w = 1; w < kFewDownWaves; ++w)
             y += total[w][i / 4][i % 4];
-        *reinterpret_cast<bf16x4 *>(a.out + ((size_t)(i / 4) * a.hidden + c) * 2) = to_bf16(y);
+        return y;
+    };
+    const auto store = [&](int i, f32x4 y) {
+        const int c = c0 + i % 4 * 4;
+        if (c < a.hidden)
+            *reinterpret_cast<bf16x4 *>(a.out + ((size_t)(i / 4) * a.hidden + c) * 2) = to_bf16(y);
+    };
+    if (a.splits == 1) {
+        for (int i = threadIdx.x; i < a.tokens * 4; i += kFewDownWaves * kWave)
+            store(i, sum_of(i));
+        return;
+    }
+    // The blocks' sums go through the memory that all XCDs share, and so do the tickets:
+    // relaxed accesses of the agent's scope, ordered by each wave's wait for its own stores
+    // before the block takes a ticket (as in k_gate).
+    const int words = a.tokens * 16;
+    float *tops = a.partial + (size_t)tile * a.splits * words;
+    for (int i = threadIdx.x; i < a.tokens * 4; i += kFewDownWaves * kWave) {
+        const f32x4 y = sum_of(i);
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+            store_agent(tops + (size_t)split * words + i * 4 + v, y[v]);
+    }
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+    if (threadIdx.x == 0)
+        last = __hip_atomic_fetch_add(a.ticket + tile, 1u, __ATOMIC_RELAXED,
+                                      __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)a.splits - 1;
+    __syncthreads();
+    if (!last)
+        return;
+    for (int i = threadIdx.x; i < a.tokens * 4; i += kFewDownWaves * kWave) {
+        f32x4 y = {0, 0, 0, 0}, part[kFewMostSplits];
+#pragma unroll
+        for (int z = 0; z < kFewMostSplits; ++z)
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+                part[z][v] = z < a.splits
+                                 ? __hip_atomic_load(tops + (size_t)z * words + i * 4 + v,
+                                                     __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)
+                                 : 0.0f;
+#pragma unroll
+        for (int z = 0; z < kFewMostSplits; ++z)
+            y += part[z];
+        store(i, y);
     }
 }
 

@@ -78,6 +78,7 @@ _SIGNATURES = {
     "epdc_rms_norm_scratch_bytes": (I32, [I32, ctypes.POINTER(SZ)]),
     "epdc_rms_norm_backward": (I32, [PNORM, P, P, P, P, P, P]),
     "epdc_quantize_rows": (I32, [P, I32, I32, I32, P, P, I32, P, P]),
+    "epdc_few_tokens_scratch_bytes": (I32, [PFEW, ctypes.POINTER(SZ)]),
     "epdc_few_tokens": (I32, [PFEW, P, P, P]),
     "epdc_layer_last_error": (ctypes.c_char_p, []),
 }
@@ -217,8 +218,15 @@ def epdc_quantize_rows(stream: int, rows: int, features: int, codes_dtype: int, 
                                     scales or None))
 
 
-def epdc_few_tokens(args: epdc_few_args, stream: int, h: int, out: int) -> None:
-    _check(lib().epdc_few_tokens(ctypes.byref(args), stream or None, h or None, out or None))
+def epdc_few_tokens_scratch_bytes(args: epdc_few_args) -> int:
+    n = SZ(0)
+    _check(lib().epdc_few_tokens_scratch_bytes(ctypes.byref(args), ctypes.byref(n)))
+    return n.value
+
+
+def epdc_few_tokens(args: epdc_few_args, stream: int, scratch: int, out: int) -> None:
+    _check(lib().epdc_few_tokens(ctypes.byref(args), stream or None, scratch or None,
+                                 out or None))
 
 
 def epdc_layer_last_error() -> str:

@@ -1035,12 +1035,13 @@ class EpDispatchCombineOp:
             out = torch.empty_like(input)
         else:
             self._need(out, "out", torch.bfloat16, input.shape)
-        h = torch.empty((T * cfg.topk, inner), dtype=torch.bfloat16, device=self.device)
         args = L.make_few_args(T, cfg.topk, n, cfg.hidden, inner, dtype, ACTIVATIONS[activation],
                                first_expert, input.data_ptr(), _ptr(weights), indices.data_ptr(),
                                w1.data_ptr(), w2.data_ptr(), _ptr(w1_scales), _ptr(w2_scales),
                                _ptr(bias1), _ptr(bias2))
-        L.epdc_few_tokens(args, self._stream(), h.data_ptr(), out.data_ptr())
+        scratch = torch.empty(L.epdc_few_tokens_scratch_bytes(args), dtype=torch.uint8,
+                              device=self.device)
+        L.epdc_few_tokens(args, self._stream(), scratch.data_ptr(), out.data_ptr())
         return out
 
     def reset(self) -> None:

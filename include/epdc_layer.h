@@ -302,7 +302,8 @@ typedef struct epdc_few_args {
     int32_t num_experts;     /* [1, 512]: experts of w1, w2, biases */
     int32_t first_expert;    /* [0, 512]: the index that stands for the first of them */
     int32_t hidden;          /* multiple of 8, at most 2^20 */
-    int32_t inner;           /* columns of h; multiple of 8, at most 2^20 */
+    int32_t inner;           /* columns of h; multiple of 8, at most 2^20, T * topk rows of
+                                them under 2 GiB */
     int32_t dtype;           /* of w1 and w2: EPDC_DT_BF16, EPDC_DT_E4M3 or EPDC_DT_INT8 */
     int32_t activation;      /* epdc_activation */
     const void *input;       /* [T, hidden] bf16 */
@@ -314,10 +315,13 @@ typedef struct epdc_few_args {
     const float *bias1, *bias2;           /* [E, rows of w1 or w2] or NULL */
 } epdc_few_args;
 
-/* h: workspace [T, topk, inner] bf16, 16-byte aligned, under 2 GiB; out [T, hidden]
- * bf16.  They may overlap neither each other nor what the call reads, except that out may
- * be input itself. */
-epdc_status epdc_few_tokens(const epdc_few_args *args, void *stream, void *h, void *out);
+/* Bytes of scratch a call needs (host only; pointers of args are not looked at).  Its
+ * contents mean nothing between calls; calls that share one must be ordered. */
+epdc_status epdc_few_tokens_scratch_bytes(const epdc_few_args *args, size_t *bytes);
+
+/* scratch: 256-byte aligned; out [T, hidden] bf16.  They may overlap neither each other nor
+ * what the call reads, except that out may be input itself. */
+epdc_status epdc_few_tokens(const epdc_few_args *args, void *stream, void *scratch, void *out);
 
 /* Thread-local message for the last non-SUCCESS status ("" if none). */
 const char *epdc_layer_last_error(void);

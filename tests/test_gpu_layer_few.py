@@ -131,6 +131,28 @@ def test_layer(T, K, E, h, i, kind):
         assert torch.equal(m.run(), got)
 
 
+@pytest.mark.parametrize("kind", sorted(STEP))
+@pytest.mark.parametrize("T,K,E,H,I", [(1, 8, 16, 256, 1024), (20, 4, 8, 384, 2048),
+                                       (64, 2, 4, 1152, 4096), (3, 2, 2, 128, 16384)])
+def test_few_columns(T, K, E, H, I, kind):
+    """Results of few columns, whose blocks share the contractions: also while another stream
+    runs the same, each with a scratch of its own."""
+    print(f"few columns {kind} T={T} K={K} E={E} H={H} I={I}", flush=True)
+    m = Few(T, K, E, H, I, kind, "silu", True, seed=T)
+    y, tol = m.reference()
+    got = m.run()
+    _within(got, y, tol)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    outs = []
+    for _ in range(4):
+        with torch.cuda.stream(side):
+            outs.append(m.run())
+        outs.append(m.run())
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, got) for o in outs)
+
+
 @pytest.mark.parametrize("act", ["none", "relu", "silu", "geglu"])
 @pytest.mark.parametrize("kind", sorted(STEP))
 def test_activations(kind, act):

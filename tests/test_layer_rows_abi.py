@@ -176,18 +176,32 @@ def test_few_token_refusals(kw, msg):
     _refused(lambda: L.epdc_few_tokens(_few(**kw), 0, A["h"], A["out"]), msg)
 
 
+def test_few_token_scratch(lib):
+    f = L.epdc_few_tokens_scratch_bytes
+    assert f(L.make_few_args(0, 2, 4, 256, 128)) == 0
+    assert f(_few()) >= 8 * 2 * 128 * 2
+    # blocks that share a tile leave their sums: more than h alone
+    assert f(_few(hidden=1024, inner=8192, num_tokens=64)) > 64 * 2 * 8192 * 2
+    _refused(lambda: f(_few(topk=0)), "topk")
+    assert lib.epdc_few_tokens_scratch_bytes(_few(), None) == B.EPDC_ERR_INVALID_ARGS
+
+
 def test_few_token_buffers(lib):
     f = lambda h, out, **kw: L.epdc_few_tokens(_few(bias1=A["bias1"], bias2=A["bias2"], **kw), 0,
                                                h, out)
     _refused(lambda: f(0, A["out"]), "required")
     _refused(lambda: f(A["h"], 0), "required")
-    _refused(lambda: f(A["h"] + 8, A["out"]), "aligned")
+    _refused(lambda: f(A["h"] + 128, A["out"]), "aligned")
     _refused(lambda: f(A["h"], A["out"] + 8), "aligned")
     for over in ("input", "weights", "indices", "w1", "w2", "bias1", "bias2"):
         _refused(lambda: f(A[over], A["out"]), "overlap")
         _refused(lambda: f(A["h"], A[over] + 16), "overlap")
     _refused(lambda: f(A["h"], A["h"] + 16), "overlap")
     _refused(lambda: f(A["h"], A["input"] - 16), "overlap")
+    # the sums behind h are part of the scratch
+    kw = dict(hidden=1024, inner=8192, num_tokens=64)
+    end = L.epdc_few_tokens_scratch_bytes(_few(**kw))
+    _refused(lambda: f(A["h"], A["h"] + end - 16, **kw), "overlap")
     L.epdc_few_tokens(_few(num_tokens=0, input=0, indices=0, w1=0, w2=0), 0, 0, 0)
     assert lib.epdc_few_tokens(None, None, None, None) == B.EPDC_ERR_INVALID_ARGS
 
