@@ -318,7 +318,7 @@ epdc_status launch_stream(hipStream_t st, ProductArgs &a)
 template <int kType>
 epdc_status launch_forward(hipStream_t st, ProductArgs &a, int64_t mean)
 {
-    constexpr bool kE4m3 = kType == kTypeE4m3;
+    constexpr bool kE4m3 = kType == kTypeE4m3, kInt8 = kType == kTypeInt8;
     // By mean rows per expert, all that is known here of the experts' counts.  The
     // streamed form reads the weights fastest but once per 16 (32) rows of an
     // expert, the tiles once per 64 (256) at 85% of that rate.  Measured over 64
@@ -327,14 +327,16 @@ epdc_status launch_forward(hipStream_t st, ProductArgs &a, int64_t mean)
     // e4m3: 12: 195, 239, 238; 16: 261, 253, 236 (with 32 rows its registers
     // leave too few waves).  64- against 256-row tiles, bf16: 40 rows 399, 410; 64:
     // 429, 441; 80: 462, 449; 128: 520, 475.  e4m3: 40: 242, 243; 64: 250, 249; 80:
-    // 280, 254; 128: 328, 270.
-    if (mean <= (kE4m3 ? 12 : 10))
+    // 280, 254; 128: 328, 270.  int8, all four: 12: 194, 197, 221, 236; 16: 256, 204, 225,
+    // 241; 20: -, 218, 227, 241; 24: 356, 246, 230, 245; 96: 64- and 256-row tiles 261,
+    // 264; 128: 287, 273; 160: 334, 289.
+    if (mean <= (kType == kTypeBf16 ? 10 : 12))
         return launch_stream<kType, 1>(st, a);
     if constexpr (!kE4m3) {
-        if (mean <= 24)
+        if (mean <= (kInt8 ? 20 : 24))
             return launch_stream<kType, 2>(st, a);
     }
-    if (mean <= 64)
+    if (mean <= (kInt8 ? 96 : 64))
         return launch_tile<kType, 1>(st, a);
     return launch_tile<kType, 4>(st, a);
 }
@@ -368,8 +370,9 @@ int team_blocks(int64_t rows)
     return row_blocks(rows, kThreads, kThreads / (kWaves * kWave));
 }
 
-// f(waves of a team, vectors of a lane): the fewest lanes that hold a row of `vecs`
-// vectors, four of them at most.
+// f(waves of a team, vectors of a lane) for rows of `vecs` vectors.  Eight waves of two
+// where four of four would do: 4096 x 7168 into bf16 and e4m3 50 us where it took 55, the
+// gradient of 8192 x 7168 110 where it took 115.
 template <typename F>
 void row_form(int vecs, F &&f)
 {
@@ -380,7 +383,7 @@ void row_form(int vecs, F &&f)
     else if (vecs <= 512)
         f(Count<4>(), Count<2>());
     else if (vecs <= 1024)
-        f(Count<4>(), Count<4>());
+        f(Count<8>(), Count<2>());
     else if (vecs <= 2048)
         f(Count<16>(), Count<2>());
     else

@@ -2,7 +2,7 @@
 // the residual's addition and rows in 8 bits, its gradient, and bf16 rows into
 // 8 bits.
 //
-// A team of 1, 4 or 16 waves owns a row and keeps it in registers from its one
+// A team of 1, 4, 8 or 16 waves owns a row and keeps it in registers from its one
 // read to its one write; the row's sums go through LDS once.
 #pragma once
 
@@ -170,7 +170,9 @@ __device__ inline float inverse_rms(const NormArgs &a, const RowSums &s)
 }
 
 // s = x + r, y = s w / rms(s), each rounded once from fp32; codes from the unrounded y.
-// Bytes are the bound.  y is (s w) times the inverse, in that order: the rounded
+// Bytes are the bound.  The sum leaves past the caches, as nothing reads it before the
+// layer's weights have gone through them, out does not: with the router's product behind it
+// 4096 x 7168 took 68.8 us, sum past the caches 67.7, both 75.9.  y is (s w) times the inverse, in that order: the rounded
 // product keeps the order of s w, so that the largest |y| is known from the largest
 // |s w| and int8 rows need no second reduction.
 template <int kWaves, int kV, int kCodes>
@@ -213,7 +215,7 @@ __global__ __launch_bounds__(team_threads(kWaves)) void k_rms_norm(const NormArg
             if (v >= a.vecs)
                 continue;
             if (a.sum)
-                *reinterpret_cast<bf16x8 *>(a.sum + (at + v) * 16) = o;
+                __builtin_nontemporal_store(o, reinterpret_cast<bf16x8 *>(a.sum + (at + v) * 16));
             float w[8];
             weight_at(a, v, w);
 #pragma unroll
@@ -285,21 +287,40 @@ __global__ __launch_bounds__(team_threads(kWaves)) void k_rms_norm_grad(const No
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             dw[k][i] = 0.0f;
-    int turn = 0;
-    const int64_t first = (int64_t)blockIdx.x * kTeams + team;
-    for (int64_t row = first; row < a.rows; row += (int64_t)gridDim.x * kTeams, turn ^= 1) {
+    // a row's loads are in flight while the row before it is worked on, where registers
+    // allow
+    constexpr bool kAhead = kWaves < 16;
+    bf16x8 s[kV], dy[kV], ds[kV], next_s[kV], next_dy[kV], next_ds[kV];
+    const auto load = [&](int64_t row, bf16x8(&to_s)[kV], bf16x8(&to_dy)[kV], bf16x8(&to_ds)[kV]) {
         const size_t at = (size_t)row * a.vecs;
-        bf16x8 s[kV], dy[kV], ds[kV];
 #pragma unroll
         for (int k = 0; k < kV; ++k) {
             const int v = k * kLanes + tid;
-            s[k] = dy[k] = ds[k] = bf16x8{};
-            if (v < a.vecs) {
-                s[k] = *reinterpret_cast<const bf16x8 *>(a.input + (at + v) * 16);
-                dy[k] = *reinterpret_cast<const bf16x8 *>(a.grad_out + (at + v) * 16);
+            to_s[k] = to_dy[k] = to_ds[k] = bf16x8{};
+            if (row < a.rows && v < a.vecs) {
+                to_s[k] = *reinterpret_cast<const bf16x8 *>(a.input + (at + v) * 16);
+                to_dy[k] = *reinterpret_cast<const bf16x8 *>(a.grad_out + (at + v) * 16);
                 if (a.grad_sum)
-                    ds[k] = *reinterpret_cast<const bf16x8 *>(a.grad_sum + (at + v) * 16);
+                    to_ds[k] = *reinterpret_cast<const bf16x8 *>(a.grad_sum + (at + v) * 16);
             }
+        }
+    };
+    int turn = 0;
+    const int64_t first = (int64_t)blockIdx.x * kTeams + team, stride = (int64_t)gridDim.x * kTeams;
+    if (kAhead)
+        load(first, next_s, next_dy, next_ds);
+    for (int64_t row = first; row < a.rows; row += stride, turn ^= 1) {
+        const size_t at = (size_t)row * a.vecs;
+        if constexpr (kAhead) {
+#pragma unroll
+            for (int k = 0; k < kV; ++k) {
+                s[k] = next_s[k];
+                dy[k] = next_dy[k];
+                ds[k] = next_ds[k];
+            }
+            load(row + stride, next_s, next_dy, next_ds);
+        } else {
+            load(row, s, dy, ds);
         }
         RowSums sums = {0.0f, 0.0f, 0.0f, 0};
 #pragma unroll

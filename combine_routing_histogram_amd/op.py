@@ -106,6 +106,17 @@ if not hasattr(torch._C, "_cuda_getCurrentRawStream"):  # older torch
         return torch.cuda.current_stream(device_index).cuda_stream
 
 
+# Sizes that the library gives for a shape, asked once each (host cost of small calls).
+@functools.lru_cache(maxsize=256)
+def _norm_scratch_bytes(features: int) -> int:
+    return L.epdc_rms_norm_scratch_bytes(features)
+
+
+@functools.lru_cache(maxsize=256)
+def _few_scratch_bytes(*shape) -> int:
+    return L.epdc_few_tokens_scratch_bytes(L.make_few_args(*shape))
+
+
 def _on_op_device(method):
     """Run a method with the op's device current, whatever the caller's is: its
     kernels and its new tensors belong there."""
@@ -949,7 +960,7 @@ class EpDispatchCombineOp:
         if need_weight:
             new = lambda n, dtype: torch.empty(n, dtype=dtype, device=self.device)
             grad_weight = new(input.shape[1], torch.float32)
-            scratch = new(L.epdc_rms_norm_scratch_bytes(input.shape[1]), torch.uint8)
+            scratch = new(_norm_scratch_bytes(input.shape[1]), torch.uint8)
         L.epdc_rms_norm_backward(args, self._stream(), grad_output.data_ptr(), _ptr(grad_sum),
                                  grad_input.data_ptr(), _ptr(grad_weight), _ptr(scratch))
         return grad_input, grad_weight
@@ -1039,8 +1050,9 @@ class EpDispatchCombineOp:
                                first_expert, input.data_ptr(), _ptr(weights), indices.data_ptr(),
                                w1.data_ptr(), w2.data_ptr(), _ptr(w1_scales), _ptr(w2_scales),
                                _ptr(bias1), _ptr(bias2))
-        scratch = torch.empty(L.epdc_few_tokens_scratch_bytes(args), dtype=torch.uint8,
-                              device=self.device)
+        scratch = torch.empty(_few_scratch_bytes(T, cfg.topk, n, cfg.hidden, inner, dtype,
+                                                 ACTIVATIONS[activation]),
+                              dtype=torch.uint8, device=self.device)
         L.epdc_few_tokens(args, self._stream(), scratch.data_ptr(), out.data_ptr())
         return out
 

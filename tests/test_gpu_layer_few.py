@@ -243,6 +243,33 @@ def test_no_tokens():
     assert m.run().shape == (0, 64)
 
 
+@pytest.mark.parametrize("kind", sorted(STEP))
+@pytest.mark.parametrize("H,I", [(512, 128), (128, 16384)])
+def test_no_experts(H, I, kind):
+    """Tokens none of whose experts is here, also where blocks share a result's columns."""
+    m = Few(5, 2, 4, H, I, kind, "silu", True, idx=np.full((5, 2), -1))
+    out = torch.full((5, H), 3.0, dtype=BF, device=DEV)
+    assert not m.run(out=out).any()
+    m.indices.fill_(4)
+    assert not m.run().any()
+
+
+def test_values_that_are_no_numbers_stay_with_their_token():
+    """A NaN and an infinity in two tokens' inputs and in one's weight reach no other."""
+    for T, kind in ((12, "bf16"), (40, "int8")):
+        m = Few(T, 3, 4, 256, 128, kind, "swiglu", seed=11)
+        clean = m.run()
+        m.x[2, 7] = float("nan")
+        m.x[5, 9] = float("inf")
+        m.w[8, 1] = float("nan")
+        got = m.run()
+        ok = torch.ones(T, dtype=torch.bool, device=DEV)
+        ok[[2, 5, 8]] = False
+        assert torch.equal(got[ok], clean[ok])
+        assert bool(got[2].isnan().all()) and bool(got[8].isnan().all())
+        assert not bool(got[5].isfinite().all())
+
+
 def test_nothing_is_written_past_the_result():
     m = Few(5, 2, 4, 72, 40, seed=4)
     buf = torch.full((7, 72), 3.0, dtype=BF, device=DEV)

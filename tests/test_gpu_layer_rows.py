@@ -15,6 +15,7 @@ import numpy as np
 import pytest
 import torch
 
+from combine_routing_histogram_amd import layer as L
 from combine_routing_histogram_amd.op import EpDispatchCombineConfig, EpDispatchCombineOp
 from layer_common import DEV, draw_indices, layout, normal, routed_op
 from oracle import oracle
@@ -113,6 +114,51 @@ def test_norm_in_place_and_empty(op):
     gx, gw = op.add_rms_norm_backward(none, none, w)
     assert gx.shape == (0, 4112) and not gw.any()
     assert op.quantize_rows(none, "int8_row")[1].shape == (0, 1)
+
+
+def test_in_place_of_what_flows_in(op):
+    """The sum over its input, the gradient over grad_out or grad_sum, as the header allows."""
+    rng = np.random.default_rng(3)
+    T, H = 700, 1288
+    x, r, dy, ds = (normal(rng, (T, H)) for _ in range(4))
+    w = normal(rng, (H,))
+    out, total, _, _ = op.add_rms_norm(x, w, r)
+    keep = x.clone()
+    out2, _, _, _ = op.add_rms_norm(keep, w, r, sum_out=keep)
+    assert torch.equal(out2, out) and torch.equal(keep, total)
+    want, dw = op.add_rms_norm_backward(dy, total, w, grad_sum=ds)
+    args = L.make_norm_args(T, H, L.EPDC_DT_BF16, 1e-6, total.data_ptr(), 0, w.data_ptr())
+    for over in (0, 1):
+        g, s = dy.clone(), ds.clone()
+        gw = torch.empty(H, device=DEV)
+        scratch = torch.empty(L.epdc_rms_norm_scratch_bytes(H), dtype=torch.uint8, device=DEV)
+        L.epdc_rms_norm_backward(args, torch.cuda.current_stream().cuda_stream, g.data_ptr(),
+                                 s.data_ptr(), (s if over else g).data_ptr(), gw.data_ptr(),
+                                 scratch.data_ptr())
+        assert torch.equal(s if over else g, want) and torch.equal(gw, dw)
+
+
+def test_rows_past_four_gigabytes(op):
+    """Arrays whose last rows lie beyond 2^32 bytes."""
+    T, H = 66000, 32768
+    x = torch.zeros(T, H, dtype=BF, device=DEV)
+    tail = normal(np.random.default_rng(5), (3, H))
+    x[-3:] = tail
+    w = normal(np.random.default_rng(6), (H,))
+    small = op.add_rms_norm(tail, w, tail, quant="int8_row")
+    big = op.add_rms_norm(x, w, x, quant="int8_row")
+    for a, b in zip(small, big):
+        assert torch.equal(a, b[-3:])
+    assert not big[0][:-3].any() and not big[3][:-3].any()
+    del big
+    small, _ = op.add_rms_norm_backward(tail, tail, w)
+    big, _ = op.add_rms_norm_backward(x, x, w)
+    assert torch.equal(small, big[-3:])
+    del big
+    for quant in sorted(FORMATS):
+        small, big = op.quantize_rows(tail, quant), op.quantize_rows(x, quant)
+        for a, b in zip(small, big):
+            assert torch.equal(a.view(torch.uint8), b[-3:].view(torch.uint8))
 
 
 def test_norm_of_extreme_rows(op):
@@ -273,7 +319,6 @@ def test_quantize_received_rows(quant):
     op = routed_op(idx, 8)
     x = normal(rng, (245, 256))
     x[off[-1]:] = float("nan")
-    import combine_routing_histogram_amd.layer as L
     codes, scales = op.quantize_rows(x, quant, routed=True)
     want, wscales = op.quantize_rows(x[:off[-1]].contiguous(), quant)
     assert codes.shape == (240, 256)
