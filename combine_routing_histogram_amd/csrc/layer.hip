@@ -513,6 +513,9 @@ epdc_status launch_few(hipStream_t st, const FewArgs &a)
 
 // Blocks that share a column tile of the down product: as many as give every CU two, but
 // no wave fewer than four steps, which take about as long as joining the blocks' sums.
+// With one block a tile and with these, us: 64 tiles, 8 bf16 experts of 2048 columns 23.4,
+// 11.3; 40 tiles, 20 e4m3 of 1280 34.4, 13.3; 128 tiles, 32 int8 of 1024 28.6, 21.7;
+// 129 tiles, 32 int8 of 1040 40.4, 33.0 (two blocks a tile: 43.4).
 int few_splits(int type, int64_t pairs, int experts, int hidden, int inner)
 {
     const int tiles = (hidden + 15) / 16, step = kStepBytes / element_bytes(type);

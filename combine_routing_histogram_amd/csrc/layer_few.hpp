@@ -262,9 +262,8 @@ struct FewProduct {
     int beside;          // of the last step
     uint32_t qoff[kQ][2];
     uint32_t off[kMI];   // of this lane's row and contraction part in p, or kNowhere
-    f32x4 acc[kMI][kQ];
-
     const float *nowhere;
+    f32x4 acc[kMI][kQ];
 
     __device__ inline void init(int contraction, int l, uint8_t *t, const uint8_t *rows,
                                 uint32_t bytes, const void *some_word)
@@ -475,9 +474,13 @@ constexpr int kFewUpBlocks = 1024;  // four to a CU
 
 // A tile: 16 columns of h (gated: 16 gate and 16 up) for one unit of rows; a block's
 // waves take the contraction's steps in turn and add up through LDS.  Blocks stay for
-// tile after tile, the next one's loads in flight while a tile ends.
+// tile after tile, the next one's loads in flight while a tile ends.  (One token through
+// 8 of 64 bf16 experts of 7168 x 2 x 2048, 470 MB: 70 us, 6.7 TB/s; 16 tokens through 82 of
+// 128 e4m3 experts of 4096 x 2 x 2048, 1.38 GB: 221 us, 6.2 TB/s; 8 pairs of 256 x 2 x 128:
+// 5.0 us, of which the routing takes 1.2 and a launch without it 1.7.)
 template <int kType, int kRows, bool kGated>
-__global__ __launch_bounds__(kFewUpWaves *kWave, few_waves(kType, kRows, kGated ? 2 : 1)) void k_few_up(const FewArgs a)
+__global__ __launch_bounds__(kFewUpWaves *kWave, few_waves(kType, kRows, kGated ? 2 : 1)) void
+k_few_up(const FewArgs a)
 {
     constexpr int kQ = kGated ? 2 : 1;
     typedef FewProduct<kType, kRows, kQ> Product;
@@ -587,9 +590,12 @@ __global__ __launch_bounds__(kFewUpWaves *kWave, few_waves(kType, kRows, kGated 
 // where a run leaves a unit, its sums go, weighted, to the wave's totals of the tokens in
 // LDS, and the waves' totals are added in order.  (Rows of tokens that do not ask for an
 // expert never meet its weights, whatever these hold.)  Where y has few columns the
-// blocks of a tile share its list; the last to finish adds their sums in order.
+// blocks of a tile share its list; the last to finish adds their sums in order.  (The same
+// layers' second products, 235 MB: 43 us, 5.5 TB/s, and 0.69 GB: 108 us, 6.4 TB/s.  With
+// four waves taking neighbouring steps in turn, longer runs of a row at a time, as fast.)
 template <int kType, int kRows>
-__global__ __launch_bounds__(kFewDownWaves *kWave, few_waves(kType, kRows, 1)) void k_few_down(const FewArgs a)
+__global__ __launch_bounds__(kFewDownWaves *kWave, few_waves(kType, kRows, 1)) void k_few_down(
+    const FewArgs a)
 {
     typedef FewProduct<kType, kRows, 1> Product;
     constexpr int kMI = Product::kMI;

@@ -632,6 +632,10 @@ __device__ inline void finish_forward8(const ProductArgs &a, int row, int col, f
 // 1.35 PFLOP/s of the 1.43 of a library product; e4m3 950 to 980 us.  Skewed over
 // 64 experts 1.80 to 1.91 ms, e4m3 1.17 to 1.21: the last tiles and row groups that
 // are not full.
+//
+// int8 runs as bf16 does, a step's 128 bytes being 128 features instead of 64, with exact
+// sums; a row's and a column's scales meet them as the accumulators leave: 800 to 820 us,
+// 2.4 POP/s where a library product of 8192 x 8192 x 8192 reaches 2.0, skewed 0.97 to 1.02 ms.
 
 constexpr int kTileWaves = 8, kTileWavesM = 2, kTileWavesN = 4, kTileCols = 256;
 

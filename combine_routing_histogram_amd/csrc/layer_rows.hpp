@@ -172,7 +172,8 @@ __device__ inline float inverse_rms(const NormArgs &a, const RowSums &s)
 // s = x + r, y = s w / rms(s), each rounded once from fp32; codes from the unrounded y.
 // Bytes are the bound.  The sum leaves past the caches, as nothing reads it before the
 // layer's weights have gone through them, out does not: with the router's product behind it
-// 4096 x 7168 took 68.8 us, sum past the caches 67.7, both 75.9.  y is (s w) times the inverse, in that order: the rounded
+// 4096 x 7168 took 68.8 us, sum past the caches 67.7, both 75.9.  (4096 x 7168 with the
+// residual into bf16 and e4m3, 265 MB: 47.7 us, 5.6 TB/s; one row 3.6.)  y is (s w) times the inverse, in that order: the rounded
 // product keeps the order of s w, so that the largest |y| is known from the largest
 // |s w| and int8 rows need no second reduction.
 template <int kWaves, int kV, int kCodes>
@@ -274,7 +275,8 @@ __global__ __launch_bounds__(team_threads(kWaves)) void k_rms_norm(const NormArg
 // With q = 1 / rms(s), n = s q and g = dy w:  dx = q (g - n mean(g n)) + dsum, and the
 // team's share of dw = sum dy n over its rows.  Rows are dealt to the teams in
 // turn, and the teams' shares are added in order (k_norm_weight_grad), so nothing
-// varies.
+// varies.  (8192 x 7168 with dsum, 470 MB: 110 us, 4.3 TB/s, and 5 for the shares; with
+// 1024 teams 105 and 7, 256 119 and 5.)
 template <int kWaves, int kV>
 __global__ __launch_bounds__(team_threads(kWaves)) void k_rms_norm_grad(const NormArgs a)
 {
@@ -459,7 +461,8 @@ struct Sixteen {
 
 constexpr int kQuantThreads = 256;
 
-// e4m3: eight lanes hold a block of 128 columns, whatever row it is of.
+// e4m3: eight lanes hold a block of 128 columns, whatever row it is of.  (32768 x 2048,
+// 203 MB: 33 us, 6.2 TB/s.)
 __global__ __launch_bounds__(kQuantThreads) void k_quantize_e4m3(const QuantArgs a)
 {
     int64_t r0, r1;
@@ -484,7 +487,7 @@ __global__ __launch_bounds__(kQuantThreads) void k_quantize_e4m3(const QuantArgs
     }
 }
 
-// int8: a team per row.
+// int8: a team per row.  (1000 x 2048: 5.3 us.)
 template <int kWaves, int kV>
 __global__ __launch_bounds__(team_threads(kWaves)) void k_quantize_int8(const QuantArgs a)
 {
