@@ -434,14 +434,22 @@ void launch_norm(hipStream_t st, const NormArgs &a)
     });
 }
 
-// Teams that share the rows of a gradient: each leaves a row of fp32 sums, so no
-// more of them than keep the chip full.
-constexpr int kNormGradTeams = 512;
-
-int norm_grad_blocks(int64_t rows, int teams)
+// Blocks that share the rows of a gradient: each of their teams leaves a row of fp32
+// sums, so no more of them than the chip holds at once.  (8192 x 7168, eight waves: 256
+// blocks 97 and 4.8 us, 512 102 and 5.4.)
+constexpr int norm_grad_blocks(int waves) { return waves < 8 ? 512 : 256; }
+constexpr int norm_grad_teams(int waves)
 {
-    const int64_t most = kNormGradTeams / teams, b = (rows + teams - 1) / teams;
-    return (int)(b < most ? b : most);
+    return norm_grad_blocks(waves) * (team_threads(waves) / (waves * kWave));
+}
+
+int64_t norm_scratch(int features)
+{
+    int teams = 0;
+    row_form(features / 8, [&](auto waves, auto) {
+        teams = norm_grad_teams(decltype(waves)::value);
+    });
+    return (int64_t)teams * features * (int64_t)sizeof(float);
 }
 
 // Columns of a scale of a format of codes; 0 for none of them.
@@ -961,7 +969,7 @@ epdc_status epdc_rms_norm_scratch_bytes(int32_t features, size_t *bytes)
         return fail(EPDC_ERR_INVALID_ARGS,
                     "features, a multiple of 8 and at most %d, and bytes are required",
                     kMaxNormFeatures);
-    *bytes = sizeof(float) * (size_t)kNormGradTeams * (size_t)features;
+    *bytes = (size_t)norm_scratch(features);
     return ok();
 }
 
@@ -990,7 +998,7 @@ epdc_status epdc_rms_norm_backward(const epdc_norm_args *args, void *stream, con
                 ds = {"grad_sum", rows ? grad_sum : nullptr, n * 2};
     const Array dx = {"grad_input", rows ? grad_input : nullptr, n * 2},
                 dw = {"grad_weight", grad_weight, (int64_t)args->features * 4},
-                part = {"scratch", scratch, (int64_t)kNormGradTeams * args->features * 4};
+                part = {"scratch", scratch, norm_scratch(args->features)};
     // a row's gradient may take the place of what flows in: the thread that writes an
     // element has read it
     s = check_apart(dx, {x, w, grad_input == grad_out ? Array{} : dy,
@@ -1013,7 +1021,8 @@ epdc_status epdc_rms_norm_backward(const epdc_norm_args *args, void *stream, con
             row_form(a.vecs, [&](auto waves, auto vecs) {
                 constexpr int kWaves = decltype(waves)::value, kThreads = team_threads(kWaves);
                 constexpr int kTeams = kThreads / (kWaves * kWave);
-                const int grid = norm_grad_blocks(a.rows, kTeams);
+                const int most = norm_grad_blocks(kWaves), need = (a.rows + kTeams - 1) / kTeams;
+                const int grid = need < most ? need : most;
                 teams = grid * kTeams;
                 k_rms_norm_grad<kWaves, decltype(vecs)::value><<<grid, kThreads, 0, st>>>(a);
             });

@@ -429,8 +429,9 @@ struct FewProduct {
             turned(of.w[j]);
 #pragma unroll
         for (int j = 0; j < kQ; ++j) {
-            const float scale = kBeside ? __int_as_float(__builtin_amdgcn_readlane(of.beside, j * 16))
-                                        : 1.0f;
+            float scale = 1.0f;
+            if constexpr (kType == kTypeE4m3)
+                scale = __int_as_float(__builtin_amdgcn_readlane(of.beside, j * 16));
             i32x4 f[2][kFrags];
             Weight::widen(of.w[j][0], f[0]);
             Weight::widen(of.w[j][1], f[1]);

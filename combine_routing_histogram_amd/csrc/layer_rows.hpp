@@ -83,8 +83,8 @@ __device__ inline RowSums team_reduce(RowSums s, RowSums (&parts)[kWaves])
 // x / s to nearest, for the codes of a row or block: from the correctly rounded
 // reciprocal r of s, two corrections of the quotient by its exact remainder, of
 // which the second gives the rounding of the true quotient.  Five instructions
-// where the division itself takes about fourteen slots.  `plain`: s is so small or large that a remainder might not be
-// exact, or no number.
+// where the division itself takes about fourteen slots.  `plain`: s is so small or
+// large that a remainder might not be exact, or no number.
 __device__ inline float quotient(float x, float s, float r, bool plain)
 {
     if (plain)
@@ -173,9 +173,9 @@ __device__ inline float inverse_rms(const NormArgs &a, const RowSums &s)
 // Bytes are the bound.  The sum leaves past the caches, as nothing reads it before the
 // layer's weights have gone through them, out does not: with the router's product behind it
 // 4096 x 7168 took 68.8 us, sum past the caches 67.7, both 75.9.  (4096 x 7168 with the
-// residual into bf16 and e4m3, 265 MB: 47.7 us, 5.6 TB/s; one row 3.6.)  y is (s w) times the inverse, in that order: the rounded
-// product keeps the order of s w, so that the largest |y| is known from the largest
-// |s w| and int8 rows need no second reduction.
+// residual into bf16 and e4m3, 265 MB: 47.7 us, 5.6 TB/s; one row 3.6.)  y is (s w) times
+// the inverse, in that order: the rounded product keeps the order of s w, so that the
+// largest |y| is known from the largest |s w| and int8 rows need no second reduction.
 template <int kWaves, int kV, int kCodes>
 __global__ __launch_bounds__(team_threads(kWaves)) void k_rms_norm(const NormArgs a)
 {
@@ -275,23 +275,33 @@ __global__ __launch_bounds__(team_threads(kWaves)) void k_rms_norm(const NormArg
 // With q = 1 / rms(s), n = s q and g = dy w:  dx = q (g - n mean(g n)) + dsum, and the
 // team's share of dw = sum dy n over its rows.  Rows are dealt to the teams in
 // turn, and the teams' shares are added in order (k_norm_weight_grad), so nothing
-// varies.  (8192 x 7168 with dsum, 470 MB: 110 us, 4.3 TB/s, and 5 for the shares; with
-// 1024 teams 105 and 7, 256 119 and 5.)
+// varies.  (8192 x 7168 with dsum, 470 MB: 98 us, 4.8 TB/s, and 5 for the shares; with the
+// weight loaded for every row, and so every row's loads waited for, 112.)
 template <int kWaves, int kV>
 __global__ __launch_bounds__(team_threads(kWaves)) void k_rms_norm_grad(const NormArgs a)
 {
     constexpr int kTeams = team_threads(kWaves) / (kWaves * 64), kLanes = kWaves * 64;
     __shared__ RowSums parts[2][kWaves];
     const int tid = threadIdx.x & (kLanes - 1), team = threadIdx.x / kLanes;
-    float dw[kV][8];
-#pragma unroll
-    for (int k = 0; k < kV; ++k)
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            dw[k][i] = 0.0f;
-    // a row's loads are in flight while the row before it is worked on, where registers
-    // allow
+    // Where registers allow, a row's loads are in flight while the row before it is worked
+    // on, and the weight stays in registers: its loads would wait for theirs.
     constexpr bool kAhead = kWaves < 16;
+    float held[kAhead ? kV : 1][8] = {}, dw[kV][8] = {};
+    if constexpr (kAhead) {
+#pragma unroll
+        for (int k = 0; k < kV; ++k)
+            if (k * kLanes + tid < a.vecs)
+                weight_at(a, k * kLanes + tid, held[k]);
+    }
+    const auto weight = [&](int k, float(&w)[8]) {
+        if constexpr (kAhead) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                w[i] = held[k][i];
+        } else {
+            weight_at(a, k * kLanes + tid, w);
+        }
+    };
     bf16x8 s[kV], dy[kV], ds[kV], next_s[kV], next_dy[kV], next_ds[kV];
     const auto load = [&](int64_t row, bf16x8(&to_s)[kV], bf16x8(&to_dy)[kV], bf16x8(&to_ds)[kV]) {
         const size_t at = (size_t)row * a.vecs;
@@ -331,7 +341,7 @@ __global__ __launch_bounds__(team_threads(kWaves)) void k_rms_norm_grad(const No
             if (v >= a.vecs)
                 continue;
             float w[8];
-            weight_at(a, v, w);
+            weight(k, w);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const float x = (float)s[k][i], far = x * 0x1p-80f;
@@ -349,7 +359,7 @@ __global__ __launch_bounds__(team_threads(kWaves)) void k_rms_norm_grad(const No
             if (v >= a.vecs)
                 continue;
             float w[8];
-            weight_at(a, v, w);
+            weight(k, w);
             bf16x8 o;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {

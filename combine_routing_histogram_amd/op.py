@@ -767,9 +767,10 @@ class EpDispatchCombineOp:
         input: bf16 [>= T*K, in], or float8_e4m3fn with scales fp32 [>= T*K,
         in/128], as dispatch gives them, or int8 with scales fp32 [>= T*K, 1];
         weight: [n, out, in] in the same type, e4m3 with weight_scales fp32 [n,
-        ceil(out/128), in/128], int8 with [n, out]; bias: fp32 [n, out].  activation: "none", "relu", "gelu", "silu", or "swiglu" /
-        "geglu", whose weight holds out/2 gate rows and then out/2 up rows.
-        residual: bf16 rows of the result.  preact: bf16 [>= T*K, out], filled
+        ceil(out/128), in/128], int8 with [n, out]; bias: fp32 [n, out].
+        activation: "none", "relu", "gelu", "silu", or "swiglu" / "geglu", whose
+        weight holds out/2 gate rows and then out/2 up rows.  residual: bf16 rows
+        of the result.  preact: bf16 [>= T*K, out], filled
         with the value before the activation for expert_product_backward.
 
         Returns out, bf16 [>= T*K, out or out/2] (allocated with T*K rows if
