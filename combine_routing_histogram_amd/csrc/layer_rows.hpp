@@ -187,7 +187,7 @@ __global__ __launch_bounds__(team_threads(kWaves)) void k_rms_norm(const NormArg
          row += (int64_t)gridDim.x * kTeams, turn ^= 1) {
         const size_t at = (size_t)row * a.vecs;
         bf16x8 x[kV], res[kV];
-        float t[kV][8];
+        float t[kV][8], w[kV][8];
 #pragma unroll
         for (int k = 0; k < kV; ++k) {
             const int v = k * kLanes + tid;
@@ -196,6 +196,7 @@ __global__ __launch_bounds__(team_threads(kWaves)) void k_rms_norm(const NormArg
                 x[k] = *reinterpret_cast<const bf16x8 *>(a.input + (at + v) * 16);
                 if (a.residual)
                     res[k] = *reinterpret_cast<const bf16x8 *>(a.residual + (at + v) * 16);
+                weight_at(a, v, w[k]);
             }
         }
         RowSums s = {0.0f, 0.0f, 0.0f, 0};
@@ -217,11 +218,9 @@ __global__ __launch_bounds__(team_threads(kWaves)) void k_rms_norm(const NormArg
                 continue;
             if (a.sum)
                 __builtin_nontemporal_store(o, reinterpret_cast<bf16x8 *>(a.sum + (at + v) * 16));
-            float w[8];
-            weight_at(a, v, w);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                t[k][i] *= w[i];
+                t[k][i] *= w[k][i];
                 if (kCodes == kCodesInt8) {
                     const int b = abs_bits(t[k][i]);
                     s.top = s.top > b ? s.top : b;
