@@ -556,11 +556,17 @@ FewScratch few_scratch(const epdc_few_args &p, int type)
 template <int kType>
 epdc_status launch_few_rows(hipStream_t st, const FewArgs &a)
 {
-    constexpr int kLine = few_line_rows(kType);
+    // By the mean rows of an expert: an expert of more rows than a unit's is read once per
+    // unit.  64 tokens, experts of 4096 x 1024, us of both launches with units of 4, 16, 32
+    // rows, int8: 1: 100, 107, 138; 2: 139, 144, 175; 4: 194, 167, 202; 10: 354, 196, 220;
+    // 16 (32 experts): 265, 139, 136; 32 (16 experts): 239, 124, 118.  bf16, 16 and 32: 1:
+    // 168, 176; 10: 314, 320; 16: 220, 179; 32: 183, 142.
     const int mean = a.tokens * a.topk / a.experts;
-    if (a.tokens <= kLine || mean <= kLine / 2)
-        return launch_few<kType, kLine>(st, a);
-    if (a.tokens <= 16 || mean <= 10)
+    if constexpr (kType != kTypeBf16) {
+        if (a.tokens <= kFewLineRows || mean <= 2)
+            return launch_few<kType, kFewLineRows>(st, a);
+    }
+    if (a.tokens <= 16 || mean <= 12)
         return launch_few<kType, 16>(st, a);
     return launch_few<kType, 32>(st, a);
 }

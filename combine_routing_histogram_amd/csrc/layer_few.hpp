@@ -49,7 +49,7 @@ __device__ inline int few_token(const FewArgs &a, int pair)
 }
 
 // The rows of the experts (one per token and expert, experts and tokens ascending), in
-// LDS, and the units of work they make: up to 4, 8, 16 or 32 rows of an expert.
+// LDS, and the units of work they make: up to 4, 16 or 32 rows of an expert.
 struct FewRouting {
     uint64_t tokens[kMaxExperts];   // that ask for an expert
     uint16_t start[kMaxExperts];    // first row of an expert
@@ -203,8 +203,8 @@ struct FewWeight {
     }
 };
 
-// Rows of a unit whose part of a step one load of a wave holds.
-constexpr int few_line_rows(int type) { return type == kTypeBf16 ? 8 : 4; }
+// Rows of a unit beside 8-bit weights whose part of a step one load of a wave holds.
+constexpr int kFewLineRows = 4;
 
 // Registers of a step's loads, and the waves of a SIMD: four where two steps' loads fit
 // into theirs, else two.
@@ -224,12 +224,13 @@ constexpr int few_waves(int type, int rows, int q)
 // the end of a contraction, or of a wave's steps, give zeros without traffic, so that
 // every step runs the same instructions and waits for its own loads only.
 //
-// Units of few rows take theirs as the weights, a step's part of all of them by one
+// Units of four rows take theirs as the weights, a step's part of all of them by one
 // load, and turn them through LDS; 16 or 32 rows come as fragments.  A load instruction
 // of 16 bytes a lane keeps a CU's address unit for 16 cycles whether its lanes are
 // active or not: with fragments for 32 rows beside every 2 KiB of 8-bit weights (ten
 // instructions) 32 tokens through 4 of 64 int8 experts of 2048 x 4096 streamed them at
-// 4.2 TB/s, however many waves or loads in flight.
+// 4.2 TB/s, however many waves or loads in flight.  (Beside bf16, 64 features a step,
+// eight rows in a load gained nothing on fragments of 16.)
 template <int kType, int kRows, int kQ>
 struct FewProduct {
     typedef FewWeight<kType> Weight;
@@ -237,7 +238,7 @@ struct FewProduct {
     static constexpr int kStep = kStepBytes / element_bytes(kType);  // elements
     static constexpr int kMI = (kRows + 15) / 16;
     static constexpr bool kLine = kRows < 16;
-    static_assert(!kLine || kRows == few_line_rows(kType), "one load holds the rows");
+    static_assert(!kLine || (kRows == kFewLineRows && kType != kTypeBf16), "in one load");
     static constexpr int kXLoads = kLine ? 1 : kMI * 2 * kFrags;
     static constexpr int kTurnBytes = 16 * kStepBytes + (kLine ? 1024 : 0);  // LDS of a wave
     static constexpr bool kBeside = kType != kTypeBf16;
