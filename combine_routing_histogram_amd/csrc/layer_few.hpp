@@ -474,6 +474,8 @@ constexpr int kFewShort = 4;        // steps of a wave
 constexpr int kFewMostSplits = 8;
 constexpr int kFewUpBlocks = 1024;  // four to a CU
 
+// h is rounded to bf16, the type in which the matrix cores take it and in which
+// expert_product leaves it; that costs the result as much again as its own rounding.
 // A tile: 16 columns of h (gated: 16 gate and 16 up) for one unit of rows; a block's
 // waves take the contraction's steps in turn and add up through LDS.  Blocks stay for
 // tile after tile, the next one's loads in flight while a tile ends.  (One token through
