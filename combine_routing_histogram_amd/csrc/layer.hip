@@ -507,31 +507,59 @@ epdc_status launch_few(hipStream_t st, const FewArgs &a)
         row_tile_bound(a.tokens * a.topk, a.experts, kRows) * ((a.inner + 15) / 16);
     const int up = (int)(tiles < kFewUpBlocks ? tiles : kFewUpBlocks);
     const int down = (a.hidden + 15) / 16 * a.splits;
+    // Whether rows are whole lines; e4m3's are but where w is not at one's start.
+    const auto form = [](const uint8_t *w, int64_t contract, auto &&f) {
+        if constexpr (kType == kTypeE4m3) {
+            f(Count<1>());
+        } else {
+            if (((uintptr_t)w | (uintptr_t)(contract * element_bytes(kType))) % kStepBytes == 0)
+                f(Count<1>());
+            else
+                f(Count<0>());
+        }
+    };
     epdc_status s = launch("k_few_up", [&] {
-        if (act_gated(a.act))
-            k_few_up<kType, kRows, true><<<up, kFewUpWaves * kWave, 0, st>>>(a);
-        else
-            k_few_up<kType, kRows, false><<<up, kFewUpWaves * kWave, 0, st>>>(a);
+        form(a.w1, a.hidden, [&](auto whole) {
+            constexpr bool kWhole = decltype(whole)::value;
+            if (act_gated(a.act))
+                k_few_up<kType, kRows, true, kWhole><<<up, kFewUpWaves * kWave, 0, st>>>(a);
+            else
+                k_few_up<kType, kRows, false, kWhole><<<up, kFewUpWaves * kWave, 0, st>>>(a);
+        });
     });
     if (s == EPDC_SUCCESS)
-        s = launch("k_few_down",
-                   [&] { k_few_down<kType, kRows><<<down, kFewDownWaves * kWave, 0, st>>>(a); });
+        s = launch("k_few_down", [&] {
+            form(a.w2, a.inner, [&](auto whole) {
+                k_few_down<kType, kRows, decltype(whole)::value>
+                    <<<down, kFewDownWaves * kWave, 0, st>>>(a);
+            });
+        });
     return s;
 }
 
-// Blocks that share a column tile of the down product: as many as give every CU two, but
-// no wave fewer than four steps, which take about as long as joining the blocks' sums.
-// With one block a tile and with these, us: 64 tiles, 8 bf16 experts of 2048 columns 23.4,
-// 11.3; 40 tiles, 20 e4m3 of 1280 34.4, 13.3; 128 tiles, 32 int8 of 1024 28.6, 21.7;
-// 129 tiles, 32 int8 of 1040 40.4, 33.0 (two blocks a tile: 43.4).
+// Blocks that share a column tile of the down product: as many as take the least time, in
+// rounds of 512 blocks (two to a CU), each as long as a wave's steps and four more, which the
+// routing and joining the blocks' sums come to; but no wave fewer than four steps (40 tiles,
+// 20 e4m3 experts of 1280 columns: 11.9 us with 6 blocks a tile, 15.8 with 8).  With one block
+// a tile and with these, us: 64 tiles, 8 bf16 of 2048 23.4, 11.3; the 40 tiles 34.4, 11.9; 128
+// tiles, 32 int8 of 1024 28.6, 21.7; 129 tiles, 32 int8 of 1040 40.4, 33.0; 257 tiles, 82
+// int8 of 2064 199, 148.
 int few_splits(int type, int64_t pairs, int experts, int hidden, int inner)
 {
     const int tiles = (hidden + 15) / 16, step = kStepBytes / element_bytes(type);
     const int64_t active = pairs < experts ? pairs : experts;
     const int64_t steps = active * ((inner + step - 1) / step);
-    int64_t n = 512 / tiles;
-    n = n < steps / (4 * kFewDownWaves) ? n : steps / (4 * kFewDownWaves);
-    return (int)(n < 1 ? 1 : n < kFewMostSplits ? n : kFewMostSplits);
+    int best = 1;
+    double least = 0.0;
+    for (int n = 1; n <= kFewMostSplits && (n == 1 || n * 4 * kFewDownWaves <= steps); ++n) {
+        const int64_t rounds = ((int64_t)tiles * n + 511) / 512;
+        const double time = (double)rounds * ((double)steps / (n * kFewDownWaves) + 4.0);
+        if (n == 1 || time < least) {
+            best = n;
+            least = time;
+        }
+    }
+    return best;
 }
 
 // Scratch: h, then the tickets and the sums of the down product's blocks.

@@ -231,7 +231,17 @@ constexpr int few_waves(int type, int rows, int q)
 // instructions) 32 tokens through 4 of 64 int8 experts of 2048 x 4096 streamed them at
 // 4.2 TB/s, however many waves or loads in flight.  (Beside bf16, 64 features a step,
 // eight rows in a load gained nothing on fragments of 16.)
-template <int kType, int kRows, int kQ>
+//
+// kWhole: every row of the weight begins with a line.  Rows that do not are read in whole
+// lines all the same, each once, and a step's window of the contraction lags so far behind its
+// line that every row has it: window s is the row's 16-byte chunks 8 s - 7 ... 8 s, of
+// which line s holds those that a wave's LDS did not have from line s - 1.  A row's place in
+// its first line is the same eight rows on, as chunks are eight to a line.  The lines go
+// through the caches, since two rows share one.  (us of both launches, loaded as 128
+// bytes of every row that lie in two lines, and so: one token, 8 bf16 experts of 7176 x
+// 2056 162, 135; 60 tokens, 64 of 4104 x 1416 686, 536; 37 tokens, 32 int8 of 2064 x 1040 60,
+// 53.  Past the caches the last takes 59.)
+template <int kType, int kRows, int kQ, bool kWhole>
 struct FewProduct {
     typedef FewWeight<kType> Weight;
     static constexpr int kFrags = Weight::kFrags;
@@ -240,7 +250,10 @@ struct FewProduct {
     static constexpr bool kLine = kRows < 16;
     static_assert(!kLine || (kRows == kFewLineRows && kType != kTypeBf16), "in one load");
     static constexpr int kXLoads = kLine ? 1 : kMI * 2 * kFrags;
-    static constexpr int kTurnBytes = 16 * kStepBytes + (kLine ? 1024 : 0);  // LDS of a wave
+    static constexpr int kLag = kWhole ? 0 : 7;            // chunks
+    static constexpr int kChunk = 16 / element_bytes(kType);  // elements
+    static constexpr int kTurns = kWhole ? 1 : kQ;
+    static constexpr int kTurnBytes = kTurns * 16 * kStepBytes + (kLine ? 1024 : 0);  // of a wave
     static constexpr bool kBeside = kType != kTypeBf16;
     static constexpr int kSlotRegs = few_slot_regs(kType, kRows, kQ);
     static constexpr int kFit = 4 / few_waves(kType, kRows, kQ) * kFewSlotRegs / kSlotRegs;
@@ -253,6 +266,7 @@ struct FewProduct {
     };
 
     int contract, steps, lane;
+    int chunk;   // of the row that this lane loads in step 0
     uint8_t *turn;
     __amdgpu_buffer_rsrc_t q, p;
     // 8-bit weights: what belongs to the 16 columns of each part comes with every step, a
@@ -266,14 +280,22 @@ struct FewProduct {
     const float *nowhere;
     f32x4 acc[kMI][kQ];
 
-    __device__ inline void init(int contraction, int l, uint8_t *t, const uint8_t *rows,
-                                uint32_t bytes, const void *some_word)
+    __device__ inline void init(const uint8_t *weight, int contraction, int l, uint8_t *t,
+                                const uint8_t *rows, uint32_t bytes, const void *some_word)
     {
         nowhere = static_cast<const float *>(some_word);
         contract = contraction;
-        steps = (contraction + kStep - 1) / kStep;
+        steps = (contraction + kLag * kChunk + kStep - 1) / kStep;
         lane = l;
         turn = t;
+        chunk = lane & 7;
+        if constexpr (!kWhole) {
+            chunk -= ((uint32_t)(uintptr_t)weight / 16 + (lane >> 3) * (contract / kChunk)) & 7;
+            // chunks before a row's first meet rows of zeros, and so may not be just anything
+#pragma unroll
+            for (int i = 0; i < kTurns * 2; ++i)
+                reinterpret_cast<i32x4 *>(turn)[i * kWave + lane] = i32x4{0, 0, 0, 0};
+        }
         p = buffer_at(rows, bytes);
         clear();
     }
@@ -299,8 +321,8 @@ struct FewProduct {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 int c = c0 + h * 8 + (lane >> 3);
-                c = (c < cols ? c : cols - 1) + j * cols;
-                qoff[j][h] = (uint32_t)c * contract * element_bytes(kType) + (lane & 7) * 16;
+                c = (c < cols ? c : c - 8) + j * cols;
+                qoff[j][h] = (uint32_t)c * contract * element_bytes(kType) + chunk * 16;
             }
 #pragma unroll
         for (int i = 0; i < kMI; ++i) {
@@ -326,16 +348,16 @@ struct FewProduct {
     }
     __device__ inline void load(Slot &to, int s)
     {
-        const int left = contract - s * kStep;   // none: past the wave's steps
-        const uint32_t at = (uint32_t)s * kStepBytes, xat = (uint32_t)s * (kStep * 2);
-        const bool in = (lane & 7) * (16 / element_bytes(kType)) < left;
+        const int begin = s * kStep - kLag * kChunk, left = contract - begin;
+        const uint32_t at = (uint32_t)s * kStepBytes, xat = (uint32_t)begin * 2;
+        const bool in = (uint32_t)(s * 8 + chunk) < (uint32_t)contract / kChunk;
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int j = 0; j < kQ; ++j)
                 to.w[j][h] = __builtin_bit_cast(
                     i32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                               q, in ? qoff[j][h] + at : kNowhere, 0, 2 /* nt */));
+                               q, in ? qoff[j][h] + at : kNowhere, 0, kWhole ? 2 /* nt */ : 0));
 #pragma unroll
         for (int n = 0; n < kXLoads; ++n) {
             // fragment f of half h of row tile i
@@ -344,7 +366,11 @@ struct FewProduct {
             const int lane_el = kLine ? lane % (64 / kRows) * 8 : (lane >> 4) * (8 * kFrags);
             to.x[n] = __builtin_bit_cast(
                 i32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                           p, el + lane_el < left ? off[i] + xat + el * 2 : kNowhere, 0, 0));
+                           p,
+                           el + lane_el < left && (kWhole || el + lane_el + begin >= 0)
+                               ? off[i] + xat + el * 2
+                               : kNowhere,
+                           0, 0));
         }
         if constexpr (kBeside) {
             int word = 0;
@@ -378,27 +404,40 @@ struct FewProduct {
     }
     // lines of 8 + 8 columns to fragments of 16; lanes read what others wrote, in
     // the order in which the wave's LDS accesses run
-    __device__ inline void turned(i32x4 (&w)[2])
+    __device__ inline void turned(i32x4 (&w)[2], int part)
     {
         typedef StraightTile<16, 1, false> Turn;
+        uint8_t *const at = turn + (kWhole ? 0 : part) * 16 * kStepBytes;
+        const i32x4 line[2] = {w[0], w[1]};
+        const auto write = [&] {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int r = h * 8 + (lane >> 3);
-            *reinterpret_cast<i32x4 *>(turn + r * kStepBytes + ((lane & 7) ^ (r & 7)) * 16) = w[h];
-        }
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
+            for (int h = 0; h < 2; ++h) {
+                const int r = h * 8 + (lane >> 3);
+                *reinterpret_cast<i32x4 *>(at + r * kStepBytes +
+                                           (((chunk + kLag) & 7) ^ (r & 7)) * 16) = line[h];
+            }
+        };
+        const auto sync = [] {
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+        };
+        if (kWhole || chunk <= 0)
+            write();
+        sync();
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-            w[h] = Turn::frag(turn, 0, h, lane);
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
+            w[h] = Turn::frag(at, 0, h, lane);
+        sync();
+        if constexpr (!kWhole) {   // the next window's
+            if (chunk > 0)
+                write();
+        }
     }
     // rows taken as a line to fragments of 16, of which kRows are its own
     __device__ inline void turned_rows(i32x4 line, i32x4 (&x)[2][kFrags])
     {
         constexpr int kChunks = 64 / kRows;   // of 16 bytes, in a row's part of a step
-        uint8_t *at = turn + 16 * kStepBytes;
+        uint8_t *at = turn + kTurns * 16 * kStepBytes;
         const int to = lane / kChunks, r = lane & (kRows - 1);
         *reinterpret_cast<i32x4 *>(at + to * (kChunks * 16) +
                                    ((lane % kChunks) ^ (to & 7)) * 16) = line;
@@ -427,7 +466,7 @@ struct FewProduct {
         }
 #pragma unroll
         for (int j = 0; j < kQ; ++j)
-            turned(of.w[j]);
+            turned(of.w[j], j);
 #pragma unroll
         for (int j = 0; j < kQ; ++j) {
             float scale = 1.0f;
@@ -477,17 +516,18 @@ constexpr int kFewUpBlocks = 1024;  // four to a CU
 // h is rounded to bf16, the type in which the matrix cores take it and in which
 // expert_product leaves it; that costs the result as much again as its own rounding.
 // A tile: 16 columns of h (gated: 16 gate and 16 up) for one unit of rows; a block's
-// waves take the contraction's steps in turn and add up through LDS.  Blocks stay for
+// waves take the contraction's steps in turn (in runs, each behind the line before its
+// first, where rows are not whole lines) and add up through LDS.  Blocks stay for
 // tile after tile, the next one's loads in flight while a tile ends.  (One token through
 // 8 of 64 bf16 experts of 7168 x 2 x 2048, 470 MB: 70 us, 6.7 TB/s; 16 tokens through 82 of
 // 128 e4m3 experts of 4096 x 2 x 2048, 1.38 GB: 221 us, 6.2 TB/s; 8 pairs of 256 x 2 x 128:
 // 5.0 us, of which the routing takes 1.2 and a launch without it 1.7.)
-template <int kType, int kRows, bool kGated>
+template <int kType, int kRows, bool kGated, bool kWhole>
 __global__ __launch_bounds__(kFewUpWaves *kWave, few_waves(kType, kRows, kGated ? 2 : 1)) void
 k_few_up(const FewArgs a)
 {
     constexpr int kQ = kGated ? 2 : 1;
-    typedef FewProduct<kType, kRows, kQ> Product;
+    typedef FewProduct<kType, kRows, kQ, kWhole> Product;
     constexpr int kMI = Product::kMI;
     __shared__ FewRouting routing;
     __shared__ __align__(16) f32x4 parts[kFewUpWaves][kMI * kQ][kWave];
@@ -502,9 +542,9 @@ k_few_up(const FewArgs a)
     if (tile >= tiles)
         return;
     Product m;
-    m.init(a.hidden, lane, turn[wave], a.x, (uint32_t)a.tokens * a.hidden * 2, a.indices);
+    m.init(a.w1, a.hidden, lane, turn[wave], a.x, (uint32_t)a.tokens * a.hidden * 2, a.indices);
     // every wave runs as many steps of a tile; some of them may lie past the end
-    const int per = (m.steps + kFewUpWaves - 1) / kFewUpWaves;
+    const int share = (m.steps + kFewUpWaves - 1) / kFewUpWaves, per = share + !kWhole;
     const int count = (tiles - tile + (int)gridDim.x - 1) / (int)gridDim.x * per;
     int load_tile = tile, load_step = 0, loaded = 0;
     const auto enter = [&] {
@@ -515,7 +555,8 @@ k_few_up(const FewArgs a)
         });
     };
     const auto next_load = [&](typename Product::Slot &to) {
-        m.load(to, loaded < count ? load_step * kFewUpWaves + wave : m.steps);
+        const int s = kWhole ? load_step * kFewUpWaves + wave : wave * share - 1 + load_step;
+        m.load(to, loaded < count ? s : m.steps);
         ++loaded;
         if (++load_step == per && loaded < count) {
             load_step = 0;
@@ -575,6 +616,8 @@ k_few_up(const FewArgs a)
 #pragma unroll
             for (int b = 0; b < kDepth; ++b) {
                 m.multiply(slot[b]);
+                if (!kWhole && step == 0)
+                    m.clear();
                 next_load(slot[b]);
                 if (++step == per && i + b < count) {
                     leave();
@@ -597,11 +640,11 @@ k_few_up(const FewArgs a)
 // blocks of a tile share its list; the last to finish adds their sums in order.  (The same
 // layers' second products, 235 MB: 43 us, 5.5 TB/s, and 0.69 GB: 108 us, 6.4 TB/s.  With
 // four waves taking neighbouring steps in turn, longer runs of a row at a time, as fast.)
-template <int kType, int kRows>
+template <int kType, int kRows, bool kWhole>
 __global__ __launch_bounds__(kFewDownWaves *kWave, few_waves(kType, kRows, 1)) void k_few_down(
     const FewArgs a)
 {
-    typedef FewProduct<kType, kRows, 1> Product;
+    typedef FewProduct<kType, kRows, 1, kWhole> Product;
     constexpr int kMI = Product::kMI;
     __shared__ FewRouting routing;
     __shared__ float weight[kFewPairs];
@@ -615,15 +658,19 @@ __global__ __launch_bounds__(kFewDownWaves *kWave, few_waves(kType, kRows, 1)) v
     for (int i = lane; i < a.tokens * 4; i += kWave)
         total[wave][i / 4][i % 4] = f32x4{0, 0, 0, 0};
     Product m;
-    m.init(a.inner, lane, turn[wave], a.h, (uint32_t)a.tokens * a.topk * a.inner * 2, a.indices);
+    m.init(a.w2, a.inner, lane, turn[wave], a.h, (uint32_t)a.tokens * a.topk * a.inner * 2,
+           a.indices);
     const int all = units * m.steps, runs = kFewDownWaves * a.splits;
     const int run = split * kFewDownWaves + wave;
     const int begin = (int)((int64_t)all * run / runs);
-    const int count = (int)((int64_t)all * (run + 1) / runs) - begin;
+    int count = (int)((int64_t)all * (run + 1) / runs) - begin;
     // where loads and multiplications are in the list
     int load_unit = begin / m.steps, load_step = begin - load_unit * m.steps, loaded = 0;
+    bool first = load_step == 0;
+    const bool behind = !kWhole && !first && count > 0;   // the line before the run's first
+    load_step -= behind;
+    count += behind;
     int unit = load_unit, step = load_step;
-    bool first = step == 0;
     const auto enter = [&] {
         const FewUnit u = few_unit(routing, load_unit);
         m.expert(a.w2, a.s2, a.b2, u.expert, c0, a.hidden, [&](int r) {
@@ -673,6 +720,8 @@ __global__ __launch_bounds__(kFewDownWaves *kWave, few_waves(kType, kRows, 1)) v
 #pragma unroll
             for (int b = 0; b < kDepth; ++b) {
                 m.multiply(slot[b]);
+                if (behind && i + b == 0)
+                    m.clear();
                 next_load(slot[b]);
                 if (i + b == count - 1 || (i + b < count && step == m.steps - 1))
                     leave();

@@ -333,3 +333,34 @@ def test_captured_and_on_another_stream():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want), k
+
+
+def _at(w, chunks, fill):
+    """The same weight, its first byte `chunks` * 16 past a line's, `fill` around it."""
+    n = w.numel() * w.element_size()
+    raw = torch.full((n + 512,), fill, dtype=torch.uint8, device=DEV)
+    assert raw.data_ptr() % 128 == 0
+    part = raw[chunks * 16:chunks * 16 + n]
+    part.copy_(w.view(torch.uint8).flatten())
+    return part.view(w.dtype).view(w.shape)
+
+
+@pytest.mark.parametrize("T,act", [(5, "silu"), (40, "geglu")])
+@pytest.mark.parametrize("kind,H,I", [("bf16", 280, 4104), ("bf16", 1032, 72), ("int8", 528, 4112),
+                                      ("int8", 1040, 80), ("fp8", 384, 2048)])
+def test_rows_that_begin_inside_a_line(kind, H, I, T, act):
+    """Weights at every place in a line, with rows that are no whole lines: what lies before and
+    behind, and the experts between those that are asked for, hold NaN (int8: other
+    numbers, of which the scales are NaN)."""
+    rng = np.random.default_rng(H + T)
+    idx = draw_indices(rng, T, 2, 3) * 2
+    m = Few(T, 2, 6, H, I, kind, act, True, seed=T, idx=idx)
+    y, tol = m.reference()
+    for t in (m.w1, m.w2):
+        t.view(torch.uint8)[1::2] = 0xff
+    if kind == "int8":
+        m.s1[1::2] = m.s2[1::2] = float("nan")
+    w1, w2 = m.w1, m.w2
+    for c in range(8):
+        m.w1, m.w2 = _at(w1, c, 0xff), _at(w2, (3 * c + 1) % 8, 0xff)
+        _within(m.run(), y, tol, f"at {c}")
