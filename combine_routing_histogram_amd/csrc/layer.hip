@@ -298,6 +298,20 @@ epdc_status launch_tile(hipStream_t st, ProductArgs &a)
     });
 }
 
+// f(whether rows of weight are whole lines); e4m3's are but where w is not at one's start.
+template <int kType, typename F>
+void line_form(const void *w, int64_t row_bytes, F &&f)
+{
+    if constexpr (kType == kTypeE4m3) {
+        f(Count<1>());
+    } else {
+        if (((uintptr_t)w | (uintptr_t)row_bytes) % kStepBytes == 0)
+            f(Count<1>());
+        else
+            f(Count<0>());
+    }
+}
+
 template <int kType, int kMI>
 epdc_status launch_stream(hipStream_t st, ProductArgs &a)
 {
@@ -308,10 +322,15 @@ epdc_status launch_stream(hipStream_t st, ProductArgs &a)
     if (s != EPDC_SUCCESS)
         return s;
     return launch("k_product_stream", [&] {
-        if (act_gated(a.act))
-            k_product_stream<kType, kMI, true><<<grid, kStreamWaves * kWave, 0, st>>>(a);
-        else
-            k_product_stream<kType, kMI, false><<<grid, kStreamWaves * kWave, 0, st>>>(a);
+        line_form<kType>(a.q, a.q_bytes, [&](auto whole) {
+            constexpr bool kWhole = decltype(whole)::value;
+            if (act_gated(a.act))
+                k_product_stream<kType, kMI, true, kWhole>
+                    <<<grid, kStreamWaves * kWave, 0, st>>>(a);
+            else
+                k_product_stream<kType, kMI, false, kWhole>
+                    <<<grid, kStreamWaves * kWave, 0, st>>>(a);
+        });
     });
 }
 
@@ -507,19 +526,8 @@ epdc_status launch_few(hipStream_t st, const FewArgs &a)
         row_tile_bound(a.tokens * a.topk, a.experts, kRows) * ((a.inner + 15) / 16);
     const int up = (int)(tiles < kFewUpBlocks ? tiles : kFewUpBlocks);
     const int down = (a.hidden + 15) / 16 * a.splits;
-    // Whether rows are whole lines; e4m3's are but where w is not at one's start.
-    const auto form = [](const uint8_t *w, int64_t contract, auto &&f) {
-        if constexpr (kType == kTypeE4m3) {
-            f(Count<1>());
-        } else {
-            if (((uintptr_t)w | (uintptr_t)(contract * element_bytes(kType))) % kStepBytes == 0)
-                f(Count<1>());
-            else
-                f(Count<0>());
-        }
-    };
     epdc_status s = launch("k_few_up", [&] {
-        form(a.w1, a.hidden, [&](auto whole) {
+        line_form<kType>(a.w1, (int64_t)a.hidden * element_bytes(kType), [&](auto whole) {
             constexpr bool kWhole = decltype(whole)::value;
             if (act_gated(a.act))
                 k_few_up<kType, kRows, true, kWhole><<<up, kFewUpWaves * kWave, 0, st>>>(a);
@@ -529,7 +537,7 @@ epdc_status launch_few(hipStream_t st, const FewArgs &a)
     });
     if (s == EPDC_SUCCESS)
         s = launch("k_few_down", [&] {
-            form(a.w2, a.inner, [&](auto whole) {
+            line_form<kType>(a.w2, (int64_t)a.inner * element_bytes(kType), [&](auto whole) {
                 k_few_down<kType, kRows, decltype(whole)::value>
                     <<<down, kFewDownWaves * kWave, 0, st>>>(a);
             });

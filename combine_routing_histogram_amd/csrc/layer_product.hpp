@@ -1147,11 +1147,14 @@ __global__ __launch_bounds__(kTileWaves *kWave) void k_product_tile(const Produc
 // caches, and a wave turns them through 2 KiB of LDS of its own into fragments
 // of 16 rows.  (Loaded as fragments, 64 bytes of 16 rows, one token's eight
 // experts of 7168 x 4096 took 89 us, 5.3 TB/s; as lines 83, and past the caches
-// 72, 6.6 TB/s; with the loads' depth chosen below 68 to 70.)
+// 72, 6.6 TB/s; with the loads' depth chosen below 68 to 70.)  Rows that are not whole
+// lines (kWhole false) go through the caches, as half of each line is another step's: past
+// them 64 int8 experts of 2 x 2048 x 4112 with 12 rows each took 150 us, so 130; 8 rows, bf16
+// and 4104 columns 235 and 202.
 
 constexpr int kStreamWaves = 4;
 
-template <int kType, int kMI, bool kGated>
+template <int kType, int kMI, bool kGated, bool kWhole>
 __global__ __launch_bounds__(kStreamWaves *kWave) void k_product_stream(const ProductArgs a)
 {
     constexpr int kQ = kGated ? 2 : 1;
@@ -1256,9 +1259,10 @@ __global__ __launch_bounds__(kStreamWaves *kWave) void k_product_stream(const Pr
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
 #pragma unroll
-                for (int q = 0; q < kQ; ++q)
-                    w[b][q][h] = __builtin_nontemporal_load(
-                        reinterpret_cast<const i32x4 *>(qp[q][h] + o));
+                for (int q = 0; q < kQ; ++q) {
+                    const i32x4 *from = reinterpret_cast<const i32x4 *>(qp[q][h] + o);
+                    w[b][q][h] = kWhole ? __builtin_nontemporal_load(from) : *from;
+                }
 #pragma unroll
                 for (int i = 0; i < kMI; ++i)
                     x[b][i][h] = *reinterpret_cast<const i32x4 *>(pp[i] + o + h * 64);
