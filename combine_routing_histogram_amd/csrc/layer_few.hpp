@@ -234,13 +234,13 @@ constexpr int few_waves(int type, int rows, int q)
 //
 // kWhole: every row of the weight begins with a line.  Rows that do not are read in whole
 // lines all the same, each once, and a step's window of the contraction lags so far behind its
-// line that every row has it: window s is the row's 16-byte chunks 8 s - 7 ... 8 s, of
-// which line s holds those that a wave's LDS did not have from line s - 1.  A row's place in
-// its first line is the same eight rows on, as chunks are eight to a line.  The lines go
-// through the caches, since two rows share one.  (us of both launches, loaded as 128
+// line that every row has it: with a lag of 7, window s is the row's 16-byte chunks 8 s - 7
+// ... 8 s, of which line s holds those that a wave's LDS did not have from line s - 1.  A row's
+// place in its first line is the same eight rows on, as chunks are eight to a line.  The lines
+// go through the caches, since two rows share one.  (us of both launches, loaded as 128
 // bytes of every row that lie in two lines, and so: one token, 8 bf16 experts of 7176 x
-// 2056 162, 135; 60 tokens, 64 of 4104 x 1416 686, 536; 37 tokens, 32 int8 of 2064 x 1040 60,
-// 53.  Past the caches the last takes 59.)
+// 2056 162, 135; 60 tokens, 64 of 4104 x 1416 686, 501; 37 tokens, 32 int8 of 2064 x 1040 60,
+// 52.  Past the caches the last takes 59.)
 template <int kType, int kRows, int kQ, bool kWhole>
 struct FewProduct {
     typedef FewWeight<kType> Weight;
@@ -250,7 +250,6 @@ struct FewProduct {
     static constexpr bool kLine = kRows < 16;
     static_assert(!kLine || (kRows == kFewLineRows && kType != kTypeBf16), "in one load");
     static constexpr int kXLoads = kLine ? 1 : kMI * 2 * kFrags;
-    static constexpr int kLag = kWhole ? 0 : 7;            // chunks
     static constexpr int kChunk = 16 / element_bytes(kType);  // elements
     static constexpr int kTurns = kWhole ? 1 : kQ;
     static constexpr int kTurnBytes = kTurns * 16 * kStepBytes + (kLine ? 1024 : 0);  // of a wave
@@ -267,6 +266,7 @@ struct FewProduct {
 
     int contract, steps, lane;
     int chunk;   // of the row that this lane loads in step 0
+    int lag;     // of windows behind their lines, in chunks: the last place of a row in a line
     uint8_t *turn;
     __amdgpu_buffer_rsrc_t q, p;
     // 8-bit weights: what belongs to the 16 columns of each part comes with every step, a
@@ -285,17 +285,20 @@ struct FewProduct {
     {
         nowhere = static_cast<const float *>(some_word);
         contract = contraction;
-        steps = (contraction + kLag * kChunk + kStep - 1) / kStep;
         lane = l;
         turn = t;
         chunk = lane & 7;
+        lag = 0;
         if constexpr (!kWhole) {
-            chunk -= ((uint32_t)(uintptr_t)weight / 16 + (lane >> 3) * (contract / kChunk)) & 7;
+            const int at = (uint32_t)(uintptr_t)weight / 16 & 7, row = contract / kChunk;
+            chunk -= (at + (lane >> 3) * row) & 7;
+            lag = at || row & 1 ? 7 : row & 2 ? 6 : 4;
             // chunks before a row's first meet rows of zeros, and so may not be just anything
 #pragma unroll
             for (int i = 0; i < kTurns * 2; ++i)
                 reinterpret_cast<i32x4 *>(turn)[i * kWave + lane] = i32x4{0, 0, 0, 0};
         }
+        steps = (contraction + lag * kChunk + kStep - 1) / kStep;
         p = buffer_at(rows, bytes);
         clear();
     }
@@ -348,7 +351,7 @@ struct FewProduct {
     }
     __device__ inline void load(Slot &to, int s)
     {
-        const int begin = s * kStep - kLag * kChunk, left = contract - begin;
+        const int begin = s * kStep - lag * kChunk, left = contract - begin;
         const uint32_t at = (uint32_t)s * kStepBytes, xat = (uint32_t)begin * 2;
         const bool in = (uint32_t)(s * 8 + chunk) < (uint32_t)contract / kChunk;
 #pragma unroll
@@ -414,14 +417,14 @@ struct FewProduct {
             for (int h = 0; h < 2; ++h) {
                 const int r = h * 8 + (lane >> 3);
                 *reinterpret_cast<i32x4 *>(at + r * kStepBytes +
-                                           (((chunk + kLag) & 7) ^ (r & 7)) * 16) = line[h];
+                                           (((chunk + lag) & 7) ^ (r & 7)) * 16) = line[h];
             }
         };
         const auto sync = [] {
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
             __builtin_amdgcn_wave_barrier();
         };
-        if (kWhole || chunk <= 0)
+        if (kWhole || chunk <= 7 - lag)
             write();
         sync();
 #pragma unroll
@@ -429,7 +432,7 @@ struct FewProduct {
             w[h] = Turn::frag(at, 0, h, lane);
         sync();
         if constexpr (!kWhole) {   // the next window's
-            if (chunk > 0)
+            if (chunk > 7 - lag)
                 write();
         }
     }

@@ -347,7 +347,8 @@ def _at(w, chunks, fill):
 
 @pytest.mark.parametrize("T,act", [(5, "silu"), (40, "geglu")])
 @pytest.mark.parametrize("kind,H,I", [("bf16", 280, 4104), ("bf16", 1032, 72), ("int8", 528, 4112),
-                                      ("int8", 1040, 80), ("fp8", 384, 2048)])
+                                      ("int8", 1040, 80), ("int8", 544, 576), ("bf16", 96, 1120),
+                                      ("fp8", 384, 2048)])
 def test_rows_that_begin_inside_a_line(kind, H, I, T, act):
     """Weights at every place in a line, with rows that are no whole lines: what lies before and
     behind, and the experts between those that are asked for, hold NaN (int8: other
