@@ -108,6 +108,8 @@ __device__ inline uint32_t four_codes(const float *v, float s, float r, bool pla
         if (plain)
             q[i] = kCodes == kCodesE4m3 ? __builtin_amdgcn_fmed3f(q[i], -448.0f, 448.0f)
                                         : __builtin_amdgcn_fmed3f(q[i], -127.0f, 127.0f);
+        else if (kCodes == kCodesE4m3)   // a zero's sign, which it lost to a remainder of +0
+            q[i] = __builtin_copysignf(q[i], v[i]);
     }
     if constexpr (kCodes == kCodesE4m3) {
         const uint32_t lo = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0u, false);
