@@ -53,8 +53,9 @@ struct RowSums {
     int top;
 };
 
-// Over a team, in every lane.  `parts` is used by every second call, so that one
-// barrier separates a call's readers from the writers of the next that uses it.
+// Over a team, in every lane.  Between two calls with the same `parts` there is always one
+// with others, whose barrier separates the readers of the first from the writers of the
+// second.
 template <int kWaves, bool kCross, bool kTop>
 __device__ inline RowSums team_reduce(RowSums s, RowSums (&parts)[kWaves])
 {
@@ -171,18 +172,22 @@ __device__ inline float inverse_rms(const NormArgs &a, const RowSums &s)
     return 0x1p-80f / sqrtf(s.far / a.features);
 }
 
+// Whether a product that should be a number of the usual size is one: not 0, beyond fp32
+// or so small that it may have lost bits.
+__device__ inline bool in_range(float v) { return v >= 0x1p-100f && v < __builtin_inff(); }
+
 // s = x + r, y = s w / rms(s), each rounded once from fp32; codes from the unrounded y.
 // Bytes are the bound.  The sum leaves past the caches, as nothing reads it before the
 // layer's weights have gone through them, out does not: with the router's product behind it
 // 4096 x 7168 took 68.8 us, sum past the caches 67.7, both 75.9.  (4096 x 7168 with the
-// residual into bf16 and e4m3, 265 MB: 47.7 us, 5.6 TB/s; one row 3.6.)  y is (s w) times
-// the inverse, in that order: the rounded product keeps the order of s w, so that the
-// largest |y| is known from the largest |s w| and int8 rows need no second reduction.
+// residual into bf16 and e4m3, 265 MB: 47.7 us, 5.6 TB/s; one row 3.6.)  The weight comes
+// last, as s w can leave fp32 where y does not.  The largest |y| of an int8 row still
+// comes with the first reduction, from the largest |s w|, unless that has left it.
 template <int kWaves, int kV, int kCodes>
 __global__ __launch_bounds__(team_threads(kWaves)) void k_rms_norm(const NormArgs a)
 {
     constexpr int kTeams = team_threads(kWaves) / (kWaves * 64), kLanes = kWaves * 64;
-    __shared__ RowSums parts[2][kWaves];
+    __shared__ RowSums parts[2][kWaves], tops[kWaves];
     const int tid = threadIdx.x & (kLanes - 1), team = threadIdx.x / kLanes;
     int turn = 0;
     for (int64_t row = (int64_t)blockIdx.x * kTeams + team; row < a.rows;
@@ -220,11 +225,10 @@ __global__ __launch_bounds__(team_threads(kWaves)) void k_rms_norm(const NormArg
                 continue;
             if (a.sum)
                 __builtin_nontemporal_store(o, reinterpret_cast<bf16x8 *>(a.sum + (at + v) * 16));
+            if constexpr (kCodes == kCodesInt8) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                t[k][i] *= w[k][i];
-                if (kCodes == kCodesInt8) {
-                    const int b = abs_bits(t[k][i]);
+                for (int i = 0; i < 8; ++i) {
+                    const int b = abs_bits(t[k][i] * w[k][i]);
                     s.top = s.top > b ? s.top : b;
                 }
             }
@@ -234,7 +238,21 @@ __global__ __launch_bounds__(team_threads(kWaves)) void k_rms_norm(const NormArg
         float scale = 0.0f, recip = 0.0f;
         bool plain = false;
         if constexpr (kCodes == kCodesInt8) {
-            scale = __int_as_float(s.top) * inv / 127.0f;
+            float top = __int_as_float(s.top) * inv;
+            if (!in_range(__int_as_float(s.top))) {
+                RowSums y = {0.0f, 0.0f, 0.0f, 0};
+#pragma unroll
+                for (int k = 0; k < kV; ++k)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int b = k * kLanes + tid < a.vecs
+                                          ? abs_bits(t[k][i] * inv * w[k][i])
+                                          : 0;
+                        y.top = y.top > b ? y.top : b;
+                    }
+                top = __int_as_float(team_reduce<kWaves, false, true>(y, tops).top);
+            }
+            scale = top / 127.0f;
             recip = 1.0f / scale;
             plain = plain_scale(scale);
             if (tid == 0)
@@ -249,7 +267,7 @@ __global__ __launch_bounds__(team_threads(kWaves)) void k_rms_norm(const NormArg
             int top = 0;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                t[k][i] *= inv;
+                t[k][i] = t[k][i] * inv * w[k][i];
                 o[i] = (__bf16)t[k][i];
                 if (kCodes == kCodesE4m3) {
                     const int b = abs_bits(t[k][i]);

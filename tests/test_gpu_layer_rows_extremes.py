@@ -1,11 +1,12 @@
-"""Rows in 8 bits and the norm at the ends of their numbers."""
+"""The norm, its gradient and rows in 8 bits where a number on the way leaves fp32's range or
+loses its sign, against 64 bits; the bounds are those of test_gpu_layer_rows.py."""
 import numpy as np
 import pytest
 import torch
 
 from layer_common import DEV
 from oracle import oracle
-from test_gpu_layer_rows import BF, op  # noqa: F401
+from test_gpu_layer_rows import BF, FORMATS, U, _check_codes, _norm, _within, op  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -32,3 +33,34 @@ def test_negative_zeros_in_e4m3_rows(op):  # noqa: F811
     codes = op.add_rms_norm(t[:3].to(DEV), w, quant="fp8_e4m3_b128", eps=1e-20)[2]
     got = codes.view(torch.uint8).cpu().numpy()
     assert (got[:, ::2][zero[:3, ::2]] == 0x80).all() and not got[:, 1::2][zero[:3, 1::2]].any()
+
+
+def _steady(rng, shape):
+    """Numbers of either sign between 0.5 and 1.5."""
+    v = rng.uniform(0.5, 1.5, shape) * rng.choice([-1.0, 1.0], shape)
+    return torch.from_numpy(v.astype(np.float32)).to(DEV)
+
+
+@pytest.mark.parametrize("H", [16, 1152, 2176, 4224, 8320, 32768])
+def test_products_outside_fp32(op, H):  # noqa: F811
+    """s * w beyond fp32, or too small for it, where y = s * w / rms(s) is neither; also where
+    that is so of some columns or rows alone."""
+    rng = np.random.default_rng(H)
+    base = _steady(rng, (4, H))
+    mixed = torch.where(torch.arange(H, device=DEV) % 3 == 0, 2.0 ** 60, 1.0)
+    for power, wide, eps in ((80, 2.0 ** 60, 1e-6), (120, 2.0 ** 30, 1e-6), (-40, 2.0 ** -95, 1e-20),
+                             (-50, 2.0 ** -90, 1e-24), (80, mixed, 1e-6)):
+        x = (base * 2.0 ** power).to(BF)
+        x[1] = base[1].to(BF)
+        x[2] = 0
+        x[2, 0] = 2.0 ** power
+        w = _steady(rng, (H,)) * wide
+        y = _norm(x, None, w, eps)[1]
+        for quant in ["none"] + sorted(FORMATS):
+            if quant != "none" and H % (FORMATS[quant][0] or 16):
+                continue
+            print(f"H={H} rows of 2^{power} {quant}", flush=True)
+            out, _, codes, scales = op.add_rms_norm(x, w, eps=eps, quant=quant)
+            _within(out, y, (U + 2.0 ** -18) * y.abs() + 2.0 ** -133, "out")
+            if quant != "none":
+                _check_codes(codes, scales, y, quant)
