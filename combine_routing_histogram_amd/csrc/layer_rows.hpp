@@ -46,10 +46,10 @@ __device__ inline int group_top(int a)
     return a;
 }
 
-// What a row is reduced to: the sum of its squares, that of its elements times
-// 2^-80 (inverse_rms), a sum of products, the largest pattern.
+// What a row is reduced to: the sum of its squares, a sum of products, the largest
+// pattern.
 struct RowSums {
-    float squares, far, cross;
+    float squares, cross;
     int top;
 };
 
@@ -60,7 +60,6 @@ template <int kWaves, bool kCross, bool kTop>
 __device__ inline RowSums team_reduce(RowSums s, RowSums (&parts)[kWaves])
 {
     s.squares = group_sum<64>(s.squares);
-    s.far = group_sum<64>(s.far);
     if constexpr (kCross)
         s.cross = group_sum<64>(s.cross);
     if constexpr (kTop)
@@ -73,7 +72,6 @@ __device__ inline RowSums team_reduce(RowSums s, RowSums (&parts)[kWaves])
 #pragma unroll
         for (int w = 1; w < kWaves; ++w) {
             s.squares += parts[w].squares;
-            s.far += parts[w].far;
             s.cross += parts[w].cross;
             s.top = s.top > parts[w].top ? s.top : parts[w].top;
         }
@@ -162,14 +160,20 @@ __device__ inline void weight_at(const NormArgs &a, int v, float (&w)[8])
     }
 }
 
-// 1 / sqrt(mean of squares + eps).  Where the sum of squares is beyond fp32 (elements
-// from 2^60 or so on) the squares of the elements times 2^-80 serve; beside those
-// eps is nothing.
-__device__ inline float inverse_rms(const NormArgs &a, const RowSums &s)
+// 1 / sqrt(mean of squares + eps) from the team's sum of squares.  Where the sum, or the mean
+// with eps, is beyond fp32, or the mean is so small that squares may have lost bits below
+// the normal numbers, the team adds squares(c) instead, those of its elements times a
+// power of two.  Elements are below 2^128, and below 2^-12 where the mean is below 2^-40.
+template <int kWaves, typename F>
+__device__ inline float inverse_rms(const NormArgs &a, float sum, RowSums (&parts)[kWaves],
+                                    F &&squares)
 {
-    if (s.squares < __builtin_inff())
-        return 1.0f / sqrtf(s.squares / a.features + a.eps);
-    return 0x1p-80f / sqrtf(s.far / a.features);
+    const float mean = sum / a.features + a.eps;
+    if (mean >= 0x1p-40f && mean < __builtin_inff())
+        return 1.0f / sqrtf(mean);
+    const float c = mean < 1.0f ? 0x1p72f : 0x1p-80f;
+    const RowSums s = team_reduce<kWaves, false, false>(RowSums{squares(c), 0.0f, 0}, parts);
+    return c / sqrtf(s.squares / a.features + a.eps * c * c);
 }
 
 // Whether a product that should be a number of the usual size is one: not 0, beyond fp32
@@ -187,7 +191,7 @@ template <int kWaves, int kV, int kCodes>
 __global__ __launch_bounds__(team_threads(kWaves)) void k_rms_norm(const NormArgs a)
 {
     constexpr int kTeams = team_threads(kWaves) / (kWaves * 64), kLanes = kWaves * 64;
-    __shared__ RowSums parts[2][kWaves], tops[kWaves];
+    __shared__ RowSums parts[2][kWaves], again[kWaves], tops[kWaves];
     const int tid = threadIdx.x & (kLanes - 1), team = threadIdx.x / kLanes;
     int turn = 0;
     for (int64_t row = (int64_t)blockIdx.x * kTeams + team; row < a.rows;
@@ -206,7 +210,7 @@ __global__ __launch_bounds__(team_threads(kWaves)) void k_rms_norm(const NormArg
                 weight_at(a, v, w[k]);
             }
         }
-        RowSums s = {0.0f, 0.0f, 0.0f, 0};
+        RowSums s = {0.0f, 0.0f, 0};
 #pragma unroll
         for (int k = 0; k < kV; ++k) {
             const int v = k * kLanes + tid;
@@ -217,9 +221,7 @@ __global__ __launch_bounds__(team_threads(kWaves)) void k_rms_norm(const NormArg
                 if (a.residual)
                     t[k][i] += (float)res[k][i];
                 o[i] = (__bf16)t[k][i];
-                const float far = t[k][i] * 0x1p-80f;
                 s.squares = __builtin_fmaf(t[k][i], t[k][i], s.squares);
-                s.far = __builtin_fmaf(far, far, s.far);
             }
             if (v >= a.vecs)
                 continue;
@@ -234,13 +236,21 @@ __global__ __launch_bounds__(team_threads(kWaves)) void k_rms_norm(const NormArg
             }
         }
         s = team_reduce<kWaves, false, kCodes == kCodesInt8>(s, parts[turn]);
-        const float inv = inverse_rms(a, s);
+        const float inv = inverse_rms(a, s.squares, again, [&](float c) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int k = 0; k < kV; ++k)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    sum = __builtin_fmaf(t[k][i] * c, t[k][i] * c, sum);
+            return sum;
+        });
         float scale = 0.0f, recip = 0.0f;
         bool plain = false;
         if constexpr (kCodes == kCodesInt8) {
             float top = __int_as_float(s.top) * inv;
             if (!in_range(__int_as_float(s.top))) {
-                RowSums y = {0.0f, 0.0f, 0.0f, 0};
+                RowSums y = {0.0f, 0.0f, 0};
 #pragma unroll
                 for (int k = 0; k < kV; ++k)
 #pragma unroll
@@ -300,7 +310,7 @@ template <int kWaves, int kV>
 __global__ __launch_bounds__(team_threads(kWaves)) void k_rms_norm_grad(const NormArgs a)
 {
     constexpr int kTeams = team_threads(kWaves) / (kWaves * 64), kLanes = kWaves * 64;
-    __shared__ RowSums parts[2][kWaves];
+    __shared__ RowSums parts[2][kWaves], again[kWaves];
     const int tid = threadIdx.x & (kLanes - 1), team = threadIdx.x / kLanes;
     // Where registers allow, a row's loads are in flight while the row before it is worked
     // on, and the weight stays in registers: its loads would wait for theirs.
@@ -353,7 +363,7 @@ __global__ __launch_bounds__(team_threads(kWaves)) void k_rms_norm_grad(const No
         } else {
             load(row, s, dy, ds);
         }
-        RowSums sums = {0.0f, 0.0f, 0.0f, 0};
+        RowSums sums = {0.0f, 0.0f, 0};
 #pragma unroll
         for (int k = 0; k < kV; ++k) {
             const int v = k * kLanes + tid;
@@ -363,14 +373,23 @@ __global__ __launch_bounds__(team_threads(kWaves)) void k_rms_norm_grad(const No
             weight(k, w);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float x = (float)s[k][i], far = x * 0x1p-80f;
+                const float x = (float)s[k][i];
                 sums.squares = __builtin_fmaf(x, x, sums.squares);
-                sums.far = __builtin_fmaf(far, far, sums.far);
                 sums.cross = __builtin_fmaf((float)dy[k][i] * w[i], x, sums.cross);
             }
         }
         sums = team_reduce<kWaves, true, false>(sums, parts[turn]);
-        const float inv = inverse_rms(a, sums);
+        const float inv = inverse_rms(a, sums.squares, again, [&](float c) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int k = 0; k < kV; ++k)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float x = (float)s[k][i] * c;
+                    sum = __builtin_fmaf(x, x, sum);
+                }
+            return sum;
+        });
         const float mean = sums.cross * inv / a.features;   // of g n
 #pragma unroll
         for (int k = 0; k < kV; ++k) {

@@ -235,9 +235,9 @@ epdc_status epdc_combine_backward(void *stream, int32_t num_tokens, int32_t topk
  *   s = input + residual (residual NULL: input), in fp32
  *   y = s * weight / sqrt(mean(s^2) + eps)
  *   sum = round(s), out = round(y), codes and scales those of y before its rounding
- * Rows whose sum of squares is beyond fp32 are right too (eps is nothing beside
- * it), and so are those whose s * weight alone is.  Squares below fp32, of elements
- * under 2^-74, count as 0, which shows only with eps 0.
+ * Rows whose squares or their sum, or s * weight alone, are beyond fp32 or below it are
+ * right too, while mean(s^2) + eps is at least 2^-252 (eps 0 is for rows of normal
+ * numbers).
  */
 typedef struct epdc_norm_args {
     int32_t rows;            /* [0, 2^30] */

@@ -4,9 +4,9 @@ import numpy as np
 import pytest
 import torch
 
-from layer_common import DEV
+from layer_common import DEV, normal
 from oracle import oracle
-from test_gpu_layer_rows import BF, FORMATS, U, _check_codes, _norm, _within, op  # noqa: F401
+from test_gpu_layer_rows import BF, FORMATS, U, _check_codes, _gradient, _norm, _within, op  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -41,6 +41,42 @@ def _steady(rng, shape):
     return torch.from_numpy(v.astype(np.float32)).to(DEV)
 
 
+# (power of two of the rows, eps): sums of squares beyond fp32 beside an eps of their size, a
+# mean that fp32 holds and the eps with it does not, squares at and below the smallest numbers
+# beside no eps or one of their size
+RANGES = [(61, 3e38), (61, 3.4e38), (62, 0.0), (0, 3.4e38), (120, 3e38), (126, 1e-6), (-50, 0.0),
+          (-60, 0.0), (-66, 1e-40), (-72, 0.0), (-75, 0.0), (-75, 1e-45), (-100, 0.0),
+          (-124, 0.0), (-20, 1e-30)]
+
+
+@pytest.mark.parametrize("H", [16, 1040, 4104])
+def test_means_outside_fp32(op, H):  # noqa: F811
+    """Every row by the whole of mean(s^2) + eps, with its gradient."""
+    rng = np.random.default_rng(H)
+    base, dy = _steady(rng, (3, H)), normal(rng, (3, H))
+    for power, eps in RANGES:
+        print(f"H={H} rows of 2^{power} eps={eps}", flush=True)
+        x = (base * 2.0 ** power).to(BF)
+        w = _steady(rng, (H,))
+        eps = float(np.float32(eps))
+        y = _norm(x, None, w, eps)[1]
+        for quant in ["none"] + sorted(FORMATS):
+            if quant == "none" or H % (FORMATS[quant][0] or 16) == 0:
+                out, _, codes, scales = op.add_rms_norm(x, w, eps=eps, quant=quant)
+                _within(out, y, (U + 2.0 ** -18) * y.abs() + 2.0 ** -133, "out")
+                if quant != "none":
+                    _check_codes(codes, scales, y, quant)
+        if power > 100:
+            continue    # sum(dy w s) is beyond fp32
+        gx, gw = op.add_rms_norm_backward(dy, x, w, eps=eps)
+        dx, tol, dw, wtol = _gradient(x, dy, w, eps, None)
+        held = dx.abs() < 2.0 ** 127          # bf16 has no larger numbers
+        tol = torch.where(held, tol, torch.inf)
+        _within(torch.where(held, gx.double(), 0), torch.where(held, dx, 0), tol + 2.0 ** -133,
+                "grad_input")
+        _within(gw, dw, wtol + 2.0 ** -149, "grad_weight")
+
+
 @pytest.mark.parametrize("H", [16, 1152, 2176, 4224, 8320, 32768])
 def test_products_outside_fp32(op, H):  # noqa: F811
     """s * w beyond fp32, or too small for it, where y = s * w / rms(s) is neither; also where
@@ -49,7 +85,8 @@ def test_products_outside_fp32(op, H):  # noqa: F811
     base = _steady(rng, (4, H))
     mixed = torch.where(torch.arange(H, device=DEV) % 3 == 0, 2.0 ** 60, 1.0)
     for power, wide, eps in ((80, 2.0 ** 60, 1e-6), (120, 2.0 ** 30, 1e-6), (-40, 2.0 ** -95, 1e-20),
-                             (-50, 2.0 ** -90, 1e-24), (80, mixed, 1e-6)):
+                             (-50, 2.0 ** -90, 1e-24), (-100, 2.0 ** -40, 0.0), (80, mixed, 1e-6),
+                             (-100, 1 / mixed, 0.0)):
         x = (base * 2.0 ** power).to(BF)
         x[1] = base[1].to(BF)
         x[2] = 0
