@@ -310,7 +310,7 @@ template <int kWaves, int kV>
 __global__ __launch_bounds__(team_threads(kWaves)) void k_rms_norm_grad(const NormArgs a)
 {
     constexpr int kTeams = team_threads(kWaves) / (kWaves * 64), kLanes = kWaves * 64;
-    __shared__ RowSums parts[2][kWaves], again[kWaves];
+    __shared__ RowSums parts[2][kWaves], again[kWaves], crosses[kWaves];
     const int tid = threadIdx.x & (kLanes - 1), team = threadIdx.x / kLanes;
     // Where registers allow, a row's loads are in flight while the row before it is worked
     // on, and the weight stays in registers: its loads would wait for theirs.
@@ -390,7 +390,25 @@ __global__ __launch_bounds__(team_threads(kWaves)) void k_rms_norm_grad(const No
                 }
             return sum;
         });
-        const float mean = sums.cross * inv / a.features;   // of g n
+        float mean = sums.cross * inv / a.features;   // of g n
+        // Products dy w x beyond fp32, or of an x so small that they may be below it: from
+        // n instead, which is of the usual size, before the sum.
+        if (!(fabsf(sums.cross) < __builtin_inff()) || inv > 0x1p20f) {
+            RowSums c = {0.0f, 0.0f, 0};
+            const float part = 1.0f / a.features;
+#pragma unroll
+            for (int k = 0; k < kV; ++k) {
+                if (k * kLanes + tid >= a.vecs)
+                    continue;
+                float w[8];
+                weight(k, w);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    c.cross = __builtin_fmaf((float)dy[k][i] * w[i],
+                                             (float)s[k][i] * inv * part, c.cross);
+            }
+            mean = team_reduce<kWaves, true, false>(c, crosses).cross;
+        }
 #pragma unroll
         for (int k = 0; k < kV; ++k) {
             const int v = k * kLanes + tid;

@@ -268,6 +268,8 @@ epdc_status epdc_rms_norm_scratch_bytes(int32_t features, size_t *bytes);
  *   grad_weight = sum over rows of grad_out * n           [features] fp32 or NULL
  * grad_sum (bf16 or NULL) is what flows into sum from elsewhere; grad_input is the
  * gradient of input and of residual alike, and may be grad_out or grad_sum itself.
+ * Rows beyond fp32 or below it are right as rms_norm's are, as long as g, and the sum of
+ * |g n| / features, are not beyond it.
  * grad_weight and scratch (16-byte aligned, epdc_rms_norm_scratch_bytes) go together.
  * No rows: grad_weight 0.
  */

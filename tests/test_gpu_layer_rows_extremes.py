@@ -66,8 +66,6 @@ def test_means_outside_fp32(op, H):  # noqa: F811
                 _within(out, y, (U + 2.0 ** -18) * y.abs() + 2.0 ** -133, "out")
                 if quant != "none":
                     _check_codes(codes, scales, y, quant)
-        if power > 100:
-            continue    # sum(dy w s) is beyond fp32
         gx, gw = op.add_rms_norm_backward(dy, x, w, eps=eps)
         dx, tol, dw, wtol = _gradient(x, dy, w, eps, None)
         held = dx.abs() < 2.0 ** 127          # bf16 has no larger numbers
@@ -75,6 +73,21 @@ def test_means_outside_fp32(op, H):  # noqa: F811
         _within(torch.where(held, gx.double(), 0), torch.where(held, dx, 0), tol + 2.0 ** -133,
                 "grad_input")
         _within(gw, dw, wtol + 2.0 ** -149, "grad_weight")
+
+
+@pytest.mark.parametrize("H", [16, 520, 2056, 7168, 16392])
+def test_gradient_of_large_rows(op, H):  # noqa: F811
+    """Rows and gradients whose products are beyond fp32: sum(dy w s), and its terms."""
+    rng = np.random.default_rng(H)
+    x = _steady(rng, (5, H)) * 2.0 ** torch.tensor([60.0, 100, 120, 126, 0], device=DEV)[:, None]
+    dy = _steady(rng, (5, H)) * 2.0 ** torch.tensor([70.0, 40, 20, 0, 0], device=DEV)[:, None]
+    x, dy = x.to(BF), dy.to(BF)
+    x[3] = 3.38e38 * x[3].sign()
+    for w in (_steady(rng, (H,)), _steady(rng, (H,)).to(BF)):
+        gx, gw = op.add_rms_norm_backward(dy, x, w)
+        dx, tol, dw, wtol = _gradient(x, dy, w, 1e-6, None)
+        _within(gx, dx, tol + 2.0 ** -133, "grad_input")
+        _within(gw, dw, wtol, "grad_weight")
 
 
 @pytest.mark.parametrize("H", [16, 1152, 2176, 4224, 8320, 32768])
