@@ -393,7 +393,7 @@ __global__ __launch_bounds__(team_threads(kWaves)) void k_rms_norm_grad(const No
         float mean = sums.cross * inv / a.features;   // of g n
         // Products dy w x beyond fp32, or of an x so small that they may be below it: from
         // n instead, which is of the usual size, before the sum.
-        if (!(fabsf(sums.cross) < __builtin_inff()) || inv > 0x1p20f) {
+        if (!(fabsf(mean) < __builtin_inff()) || inv > 0x1p20f) {
             RowSums c = {0.0f, 0.0f, 0};
             const float part = 1.0f / a.features;
 #pragma unroll

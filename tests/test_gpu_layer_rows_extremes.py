@@ -114,3 +114,15 @@ def test_products_outside_fp32(op, H):  # noqa: F811
             _within(out, y, (U + 2.0 ** -18) * y.abs() + 2.0 ** -133, "out")
             if quant != "none":
                 _check_codes(codes, scales, y, quant)
+
+
+def test_gradient_whose_mean_alone_is_in_range(op):  # noqa: F811
+    """sum(dy w s) within fp32, that times 1 / rms(s) beyond it, its mean within it again."""
+    rng = np.random.default_rng(7)
+    H = 16392
+    x, w = (_steady(rng, (2, H)) * 2.0 ** -8).to(BF), _steady(rng, (H,))
+    dy = (_steady(rng, (2, H)).abs() * 2.0 ** 115 * (x.float() * w).sign()).to(BF)
+    gx, gw = op.add_rms_norm_backward(dy, x, w)
+    dx, tol, dw, wtol = _gradient(x, dy, w, 1e-6, None)
+    _within(gx, dx, tol, "grad_input")
+    _within(gw, dw, wtol, "grad_weight")
