@@ -390,8 +390,8 @@ int team_blocks(int64_t rows)
 }
 
 // f(waves of a team, vectors of a lane) for rows of `vecs` vectors.  Eight waves of two
-// where four of four would do: 4096 x 7168 into bf16 and e4m3 50 us where it took 55, the
-// gradient of 8192 x 7168 110 where it took 115.
+// where four of four would do: 4096 x 7168 into bf16 and e4m3 47 us for 52, the gradient
+// of 8192 x 7168 94 for 122, one row 2.7 for 3.1.
 template <typename F>
 void row_form(int vecs, F &&f)
 {
@@ -455,7 +455,7 @@ void launch_norm(hipStream_t st, const NormArgs &a)
 
 // Blocks that share the rows of a gradient: each of their teams leaves a row of fp32
 // sums, so no more of them than the chip holds at once.  (8192 x 7168, eight waves: 256
-// blocks 97 and 4.8 us, 512 102 and 5.4.)
+// blocks 94 and 4.9 us, 512 96 and 5.1.)
 constexpr int norm_grad_blocks(int waves) { return waves < 8 ? 512 : 256; }
 constexpr int norm_grad_teams(int waves)
 {
@@ -596,7 +596,8 @@ epdc_status launch_few_rows(hipStream_t st, const FewArgs &a)
     // unit.  64 tokens, experts of 4096 x 1024, us of both launches with units of 4, 16, 32
     // rows, int8: 1: 100, 107, 138; 2: 139, 144, 175; 4: 194, 167, 202; 10: 354, 196, 220;
     // 16 (32 experts): 265, 139, 136; 32 (16 experts): 239, 124, 118.  bf16, 16 and 32: 1:
-    // 168, 176; 10: 314, 320; 16: 220, 179; 32: 183, 142.
+    // 168, 176; 10: 314, 320; 16: 220, 179; 32: 183, 142.  (Even routing; one expert of far
+    // more rows than the mean is read once per unit of its own.)
     const int mean = a.tokens * a.topk / a.experts;
     if constexpr (kType != kTypeBf16) {
         if (a.tokens <= kFewLineRows || mean <= 2)

@@ -3,9 +3,10 @@
 //   k_few_up:    h[t, k]  = act(x[t] W1[e]^T + b1[e]),      e = indices[t, k]
 //   k_few_down:  y[t]     = sum_k w[t, k] (h[t, k] W2[e]^T + b2[e])
 //
-// The weights of the experts that are asked for are the traffic, read once in whole
-// 128-byte lines past the caches and turned through LDS into fragments, as in
-// k_product_stream; nothing is routed in memory.  Every block finds the experts' rows
+// The weights of the experts that are asked for are the traffic, read once for every
+// unit of up to 4, 16 or 32 rows of an expert, in whole 128-byte lines, past the caches if
+// rows of weight are whole lines and through them if not, and turned through LDS into
+// fragments, as in k_product_stream; nothing is routed in memory.  Every block finds the experts' rows
 // from the indices itself: at most 1024, a token set per expert in one 64-bit
 // word.  8-bit weights are widened to bf16, which holds them exactly, so the
 // activations stay bf16.

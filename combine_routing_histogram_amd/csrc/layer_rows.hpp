@@ -184,7 +184,7 @@ __device__ inline bool in_range(float v) { return v >= 0x1p-100f && v < __builti
 // Bytes are the bound.  The sum leaves past the caches, as nothing reads it before the
 // layer's weights have gone through them, out does not: with the router's product behind it
 // 4096 x 7168 took 68.8 us, sum past the caches 67.7, both 75.9.  (4096 x 7168 with the
-// residual into bf16 and e4m3, 265 MB: 47.7 us, 5.6 TB/s; one row 3.6.)  The weight comes
+// residual into bf16 and e4m3, 265 MB: 46.5 us, 5.7 TB/s; one row 2.7.)  The weight comes
 // last, as s w can leave fp32 where y does not.  The largest |y| of an int8 row still
 // comes with the first reduction, from the largest |s w|, unless that has left it.
 template <int kWaves, int kV, int kCodes>
@@ -304,8 +304,9 @@ __global__ __launch_bounds__(team_threads(kWaves)) void k_rms_norm(const NormArg
 // With q = 1 / rms(s), n = s q and g = dy w:  dx = q (g - n mean(g n)) + dsum, and the
 // team's share of dw = sum dy n over its rows.  Rows are dealt to the teams in
 // turn, and the teams' shares are added in order (k_norm_weight_grad), so nothing
-// varies.  (8192 x 7168 with dsum, 470 MB: 98 us, 4.8 TB/s, and 5 for the shares; with the
-// weight loaded for every row, and so every row's loads waited for, 112.)
+// varies.  (8192 x 7168 with dsum, 470 MB: 94 us, 5.0 TB/s, and 5 for the shares; with the
+// weight loaded for every row, and so every row's loads waited for, 14 us more.)  Rows of
+// more than 16384 elements spill: 2048 x 32768 157 us, 153 without the second sum below.
 template <int kWaves, int kV>
 __global__ __launch_bounds__(team_threads(kWaves)) void k_rms_norm_grad(const NormArgs a)
 {
@@ -553,7 +554,8 @@ __global__ __launch_bounds__(kQuantThreads) void k_quantize_e4m3(const QuantArgs
     }
 }
 
-// int8: a team per row.  (1000 x 2048: 5.3 us.)
+// int8: a team per row.  (1000 x 2048: 5.4 us, 4096 x 7168 17; 32768 x 2048, where half the
+// lanes of a team have nothing to load, 81.)
 template <int kWaves, int kV>
 __global__ __launch_bounds__(team_threads(kWaves)) void k_quantize_int8(const QuantArgs a)
 {

@@ -1001,13 +1001,16 @@ class EpDispatchCombineOp:
         """dispatch, both expert products and combine for up to 64 tokens, in two
         launches: out[t] = sum_k weights[t,k] * (act(input[t] @ w1[e].T + bias1[e])
         @ w2[e].T + bias2[e]), e = indices[t,k] - first_expert, over the k whose
-        expert is one of these n; a token without one gets 0.
+        expert is one of these n; a token without one gets 0.  act(...) is rounded to
+        bf16 before the second product, as expert_product's result is.
 
         input: bf16 [T, hidden]; weights fp32 [T, K] (None: 1) and indices int32
         [T, K] as gate gives them; w1: [n, inner, hidden] (gated: [n, 2 * inner,
         hidden], gate rows first), w2: [n, hidden, inner], both bf16, float8_e4m3fn
         or int8 with scales as expert_product's weight_scales; biases fp32 [n, rows].
-        The rows stay bf16 whatever the weights are.
+        The rows stay bf16 whatever the weights are.  Weights are read once per 4 to
+        32 rows of an expert: up to 64 tokens that takes no longer than the separate
+        calls (at most 3% more, with many int8 experts from 32 tokens on).
 
         Returns out, bf16 [T, hidden] (allocated if None; may be input).  The
         routing of the last dispatch is neither used nor changed."""

@@ -65,9 +65,9 @@ typedef enum epdc_layer_dtype {
  *   e4m3  scales [rows, features/128] fp32, per block of 128 columns amax/448: the
  *         layout and the rounding of dispatch's EPDC_QUANT_FP8_E4M3_B128
  *   int8  scales [rows] fp32, amax/127 of the row
- * code = round(x / scale), both divisions fp32 to nearest even; a scale of 0 (all
- * zeros) gives codes 0.  A block or row that holds a NaN or an infinity gets that
- * as its scale.
+ * code = round(x / scale), both divisions fp32 to nearest even, an e4m3 zero with x's
+ * sign; a scale of 0 (all zeros) gives codes 0.  A block or row that holds a NaN or an
+ * infinity gets that as its scale.
  */
 
 /* The score a gate takes of its logits. */
