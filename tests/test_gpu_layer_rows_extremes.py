@@ -6,7 +6,8 @@ import torch
 
 from layer_common import DEV, normal
 from oracle import oracle
-from test_gpu_layer_rows import BF, FORMATS, U, _check_codes, _gradient, _norm, _within, op  # noqa: F401
+from test_gpu_layer_rows import (BF, FORMATS, U, _check_codes, _gradient, _int8,  # noqa: F401
+                                 _norm, _within, op)
 
 pytestmark = pytest.mark.gpu
 
@@ -126,3 +127,20 @@ def test_gradient_whose_mean_alone_is_in_range(op):  # noqa: F811
     dx, tol, dw, wtol = _gradient(x, dy, w, 1e-6, None)
     _within(gx, dx, tol, "grad_input")
     _within(gw, dw, wtol, "grad_weight")
+
+
+def test_codes_of_subnormal_rows(op):  # noqa: F811
+    """Blocks and rows of bf16's subnormal numbers, whose scales fp32 holds to a few bits: codes
+    and scales of whole fp32 divisions, e4m3 as the oracle has them."""
+    rng = np.random.default_rng(9)
+    bits = rng.integers(0, 1 << np.arange(1, 8).repeat(3)[:, None], (21, 256)).astype(np.uint16)
+    bits |= (rng.integers(0, 2, bits.shape) << 15).astype(np.uint16)
+    t = torch.from_numpy(bits.view(np.int16)).view(BF)
+    codes, scales = op.quantize_rows(t.to(DEV), "fp8_e4m3_b128")
+    want, scale = oracle.quant_fp8(bits)
+    assert np.array_equal(scales.cpu().numpy(), np.asarray(scale).reshape(21, -1))
+    assert np.array_equal(codes.view(torch.uint8).cpu().numpy(), np.asarray(want).reshape(21, -1))
+    codes, scales = op.quantize_rows(t.to(DEV), "int8_row")
+    want, scale = _int8(t.float().numpy())
+    assert np.array_equal(scales.cpu().numpy(), scale)
+    assert np.array_equal(codes.cpu().numpy(), want)
